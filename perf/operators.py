@@ -218,7 +218,6 @@ def prepare(case, seed):
         rows = _normal(gen, sum(q), 2, h, d).to(BF16)
         s["k"], s["v"] = rows[:, 0], rows[:, 1]
         s["cu"], s["start"] = _whole(_offsets(q)), _whole(held)
-        s["most"] = max(q)
         s["pos"] = _whole([[b + i for a, b in zip(q, held) for i in range(a)]])
         s["wk"] = (1 + 0.2 * _normal(gen, d)).to(BF16) if case["norm"] else None
     elif kind == "shared":
@@ -301,7 +300,7 @@ def run(s):
             from bit_kv_cache_23_b200 import qwm_norm_rope
             return qwm_norm_rope(h, s["q"], s["k"], s["pos"], s["wq"], s["wk"])
         if kind == "append":
-            h[0].append(s["table"], s["cu"], s["start"], s["k"], s["v"], s["most"], rope=h[1],
+            h[0].append(s["table"], s["cu"], s["start"], s["k"], s["v"], rope=h[1],
                         pos=s["pos"] if h[1] is not None else None, k_weight=s["wk"])
             return s["K"], s["V"]
         if kind == "shared":
