@@ -23,6 +23,9 @@ __all__ = [
     "qwm_build_centroids", "qwm_build_centroids_noalloc", "qwm_update_query_stats", "qwm_append_kv", "qwm_attention",
     "qwm_attention_ext", "qwm_reconstruct", "qwm_top1_shift", "qwm_device_status", "QuantKVCache",
     "QWM_FLAG_QSAC_FULL", "QWM_NOALLOC_SCRATCH_BYTES", "QWM_ATTN_MAX_SPLIT",
+    "qwm_rope", "qwm_pages", "qwm_rope_init", "qwm_norm_rope", "qwm_paged_append",
+    "qwm_attention_shared_workspace", "qwm_attention_shared", "qwm_cross_attention_workspace",
+    "qwm_cross_attention", "PagedKV", "ROPE_LAYOUTS", "ROPE_SCALINGS",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -68,6 +71,23 @@ class qwm_cache(ctypes.Structure):
                 ("n_cent_versions", ctypes.c_int32), ("cur_cent_version", ctypes.c_int32)]
 
 
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "parts": 3}
+
+
+class qwm_rope(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("n_axes", ctypes.c_int32),
+                ("axis_dim", ctypes.c_int32 * 3), ("magic", ctypes.c_int32),
+                ("gain", ctypes.c_double), ("freq", ctypes.c_double * 64)]
+
+
+class qwm_pages(ctypes.Structure):
+    _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 class QwmError(RuntimeError):
     def __init__(self, fn: str, status: int):
         self.status = status
@@ -87,7 +107,8 @@ def lib():
                               "python -m bit_kv_cache_23_b200.build")
         L = ctypes.CDLL(LIB_PATH)
         I32, I64, F32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
-        pc = ctypes.POINTER(qwm_cache)
+        U64, F64 = ctypes.c_uint64, ctypes.c_double
+        pc, pu = ctypes.POINTER(qwm_cache), ctypes.POINTER(U64)
         sig = {
             "qwm_abi_version": (I32, []),
             "qwm_status_string": (ctypes.c_char_p, [I32]),
@@ -102,6 +123,18 @@ def lib():
             "qwm_top1_shift": (I32, [pc, _P, I64, _P, _P, _P, _P]),
             "qwm_device_status": (I32, [ctypes.POINTER(ctypes.c_int32)]),
             "qwm_build_centroids_noalloc": (I32, [pc, _P, _P, I64, I32, _P]),
+            "qwm_rope_init": (I32, [ctypes.POINTER(qwm_rope), I32, I32, I32, F64, I32,
+                                    ctypes.POINTER(I32), I32, F64, F64, F64, F64]),
+            "qwm_norm_rope": (I32, [_P, I32, I64, _P, I64, I32, _P, _P, I64, _P, I64, I32, _P, _P,
+                                    I64, _P, I64, F32, _P]),
+            "qwm_paged_append": (I32, [ctypes.POINTER(qwm_pages), _P, I64, I32, _P, _P, _P, I64, _P,
+                                       I64, I64, _P, _P, I64, _P, F32, _P]),
+            "qwm_attention_shared_workspace": (I32, [pc, I64, I32, I64, I64, I64, pu, pu]),
+            "qwm_attention_shared": (I32, [pc, _P, I64, I64, I32, _P, I64, I64, _P, _P, I32, _P, I64,
+                                           I32, F32, _P, _P, _P, U64, _P]),
+            "qwm_cross_attention_workspace": (I32, [I32, I32, I32, I64, I64, I64, I64, pu, pu]),
+            "qwm_cross_attention": (I32, [_P, I64, I64, I32, _P, I64, _P, I64, I64, I32, I32, _P, _P,
+                                          _P, I64, I64, I64, F32, _P, _P, _P, U64, _P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -238,12 +271,316 @@ def qwm_top1_shift(cache: qwm_cache, Q: torch.Tensor, K_exact: torch.Tensor, str
 
 def qwm_device_status() -> int:
     """Synchronize and return 1 if a bounded device wait timed out since the
-    last call (the flag is cleared), else 0."""
+    last call (the flag is cleared), plus 2 if an offset, length or page number
+    in a device array lay outside its buffer and was clamped, else 0."""
     f = ctypes.c_int32(0)
     st = lib().qwm_device_status(ctypes.byref(f))
-    if st not in (0, 6):
+    if st not in (0, 6) and not (st == 1 and f.value):
         raise QwmError("qwm_device_status", st)
     return int(f.value)
+
+
+# ----------------------------------------------------------------- around the cache
+def _rows_ptr(t: torch.Tensor, name: str, like=None, heads=None, dim=None):
+    """(pointer, row distance) of a [n][heads][head_dim] bf16 CUDA tensor whose
+    heads are contiguous within a row; its rows may be strided."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if like is not None and t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [n][heads][head_dim]")
+    n, h, d = t.shape
+    if (heads is not None and h != heads) or (dim is not None and d != dim):
+        raise ValueError(f"{name} has heads x head_dim = {h} x {d}, expected {heads} x {dim}")
+    row, head, one = t.stride()
+    if (one != 1 and d > 1) or (h > 1 and head != d):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return t.data_ptr(), (row if n > 1 else max(h * d, 8))
+
+
+def _ints_ptr(t: torch.Tensor, name: str, shape, like):
+    """Pointer of a contiguous int32 tensor of this shape (None: any length)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda or t.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}")
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
+    if t.dim() != len(shape) or any(b is not None and a != b for a, b in zip(t.shape, shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _weight_ptr(w, name, dim, like):
+    if w is None:
+        return None
+    if w.shape != (dim,):
+        raise ValueError(f"{name} must be [{dim}]")
+    if w.device != like.device:
+        raise ValueError(f"{name} is on {w.device}, expected {like.device}")
+    return _dev_ptr(w, name, torch.bfloat16)
+
+
+class _on:
+    """Make `device` current for a call (the library launches on the current
+    device); no work when it already is."""
+
+    def __init__(self, device):
+        self.index = device.index
+
+    def __enter__(self):
+        self.before = torch.cuda.current_device()
+        if self.before != self.index:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.before != self.index:
+            torch.cuda.set_device(self.before)
+
+
+def _held(stream, *tensors):
+    """Tensors allocated here (on the current stream) and used on `stream`."""
+    if stream is not None and hasattr(stream, "cuda_stream"):
+        for t in tensors:
+            if t is not None and stream != torch.cuda.current_stream(t.device):
+                t.record_stream(stream)
+
+
+def qwm_rope_init(head_dim: int, rot_dim: int, layout: str = "half", theta: float = 10000.0,
+                  axis_dims=None, scaling: str = "none", factor: float = 1.0,
+                  orig_len: float = 4096.0, beta_fast: float = 32.0,
+                  beta_slow: float = 1.0) -> qwm_rope:
+    """The rotation of `rot_dim` channels: layout "half" or "interleaved", one
+    entry of axis_dims per position axis, scaling "none", "linear", "ntk" or
+    "parts" (see include/qwm.h)."""
+    if layout not in ROPE_LAYOUTS or scaling not in ROPE_SCALINGS:
+        raise ValueError(f"layout {layout!r} or scaling {scaling!r} unknown")
+    dims = [rot_dim] if axis_dims is None else list(axis_dims)
+    r = qwm_rope()
+    arr = (ctypes.c_int32 * max(len(dims), 1))(*dims)
+    _check("qwm_rope_init", lib().qwm_rope_init(
+        ctypes.byref(r), head_dim, rot_dim, ROPE_LAYOUTS[layout], theta, len(dims), arr,
+        ROPE_SCALINGS[scaling], factor, orig_len, beta_fast, beta_slow))
+    return r
+
+
+def _pos_ptr(rope, pos, n, like):
+    if rope is None:
+        if pos is not None:
+            raise ValueError("positions without a rotation")
+        return None, None
+    if pos is None:
+        raise ValueError("a rotation needs positions")
+    if pos.dim() == 1 and rope.n_axes == 1:
+        pos = pos[None]
+    return ctypes.addressof(rope), _ints_ptr(pos, "pos", (rope.n_axes, n), like)
+
+
+def qwm_norm_rope(rope: qwm_rope | None, Q: torch.Tensor | None, K: torch.Tensor | None = None,
+                  pos: torch.Tensor | None = None, q_weight: torch.Tensor | None = None,
+                  k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                  Q_out: torch.Tensor | None = None, K_out: torch.Tensor | None = None,
+                  stream=None):
+    """Per-head RMS norm (where a weight is given) and rotation (where `rope` is)
+    of queries and keys in one pass; returns (Q_out, K_out).  Q and K may be
+    parts of a fused projection; Q or K may be None.  pos: [axes][n] int32."""
+    x0 = Q if Q is not None else K
+    if x0 is None:
+        raise ValueError("neither Q nor K given")
+    args, n, d = [], None, None
+    for x, w, o, name in ((Q, q_weight, Q_out, "Q"), (K, k_weight, K_out, "K")):
+        if x is None:
+            if w is not None or o is not None:
+                raise ValueError(f"{name} is missing")
+            args += [None, 0, 0, None, None, 0]
+            continue
+        p, ld = _rows_ptr(x, name, x0)
+        if n is not None and (x.shape[0] != n or x.shape[2] != d):
+            raise ValueError("Q and K differ in rows or head_dim")
+        n, h, d = x.shape
+        if o is None:
+            o = torch.empty((n, h, d), dtype=torch.bfloat16, device=x.device)
+            _held(stream, o)
+        elif o.shape != x.shape:
+            raise ValueError(f"{name}_out must have the shape of {name}")
+        po, ldo = _rows_ptr(o, name + "_out", x0)
+        if name == "Q":
+            Q_out = o
+        else:
+            K_out = o
+        args += [p, ld, h, _weight_ptr(w, name + " weight", d, x0), po, ldo]
+    rp, pp = _pos_ptr(rope, pos, n, x0)
+    with _on(x0.device):
+        _check("qwm_norm_rope", lib().qwm_norm_rope(rp, d, n, *args, pp, n, float(eps),
+                                                    _stream(stream, x0.device)))
+    return Q_out, K_out
+
+
+def qwm_paged_append(pages: qwm_pages, table: torch.Tensor, cu: torch.Tensor, start: torch.Tensor,
+                     K: torch.Tensor, V: torch.Tensor, rope: qwm_rope | None = None,
+                     pos: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                     eps: float = 1e-6, stream=None) -> None:
+    """Write the rows cu[b] .. cu[b+1]-1 of K (normed and rotated on the way) and
+    V to positions start[b], start[b]+1, ... of sequence b's pages."""
+    kp, ldk = _rows_ptr(K, "K", None, pages.heads, pages.head_dim)
+    vp, ldv = _rows_ptr(V, "V", K, pages.heads, pages.head_dim)
+    if V.shape[0] != K.shape[0]:
+        raise ValueError("K and V differ in rows")
+    n, n_seq = K.shape[0], table.shape[0]
+    rp, pp = _pos_ptr(rope, pos, n, K)
+    with _on(K.device):
+        _check("qwm_paged_append", lib().qwm_paged_append(
+            ctypes.byref(pages), _ints_ptr(table, "table", (None, None), K), n_seq, table.shape[1],
+            _ints_ptr(cu, "cu", (n_seq + 1,), K), _ints_ptr(start, "start", (n_seq,), K), kp, ldk, vp,
+            ldv, n, rp, pp, n, _weight_ptr(k_weight, "k_weight", pages.head_dim, K), float(eps),
+            _stream(stream, K.device)))
+
+
+def _lse_ptr(lse, n, heads, like):
+    if lse is None:
+        return None
+    if lse.shape != (n, heads) or lse.device != like.device:
+        raise ValueError(f"lse must be [{n}][{heads}] on {like.device}")
+    return _dev_ptr(lse, "lse", torch.float32)
+
+
+def _out(O, Q, stream):
+    if O is None:
+        O = torch.empty(Q.shape, dtype=torch.bfloat16, device=Q.device)
+        _held(stream, O)
+    elif O.shape != Q.shape or O.device != Q.device:
+        raise ValueError("O must have the shape and device of Q")
+    return O
+
+
+def _scratch(workspace, nbytes, like, stream):
+    """The caller's workspace, or one for this call."""
+    if workspace is None:
+        if nbytes == 0:
+            return None, None, 0
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        _held(stream, workspace)
+    elif workspace.device != like.device:
+        raise ValueError(f"workspace must be on {like.device}")
+    p = _dev_ptr(workspace, "workspace")
+    return workspace, p, workspace.numel() * workspace.element_size()
+
+
+def qwm_attention_shared_workspace(cache: qwm_cache, n_q: int, heads_q: int, n_seq: int, max_q: int,
+                                   max_kv: int) -> tuple[int, int]:
+    """(least, full) workspace bytes of qwm_attention_shared."""
+    least, full = ctypes.c_uint64(0), ctypes.c_uint64(0)
+    _check("qwm_attention_shared_workspace", lib().qwm_attention_shared_workspace(
+        ctypes.byref(cache), n_q, heads_q, n_seq, max_q, max_kv, ctypes.byref(least),
+        ctypes.byref(full)))
+    return least.value, full.value
+
+
+def qwm_attention_shared(cache: qwm_cache, Q: torch.Tensor, cu: torch.Tensor, max_q: int,
+                         pages: qwm_pages | None = None, table: torch.Tensor | None = None,
+                         kv_len: torch.Tensor | None = None, max_kv: int = 0, causal: bool = False,
+                         O: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                         scale: float = 0.0, workspace: torch.Tensor | None = None,
+                         stream=None) -> torch.Tensor:
+    """Attention of the branches (rows cu[b] .. cu[b+1]-1 of Q) over the packed
+    history that they share, followed by the first kv_len[b] positions of each
+    branch's pages.  max_q, max_kv: upper bounds of a branch's rows and keys."""
+    n, h, d = Q.shape
+    qp, ldq = _rows_ptr(Q, "Q", None, None, cache.cfg.head_dim)
+    n_seq = cu.shape[0] - 1
+    cup = _ints_ptr(cu, "cu", (None,), Q)
+    pg = tp = kp = None
+    width = 0
+    if pages is not None:
+        if table is None or kv_len is None:
+            raise ValueError("pages need a table and kv_len")
+        pg, width = ctypes.addressof(pages), table.shape[1]
+        tp = _ints_ptr(table, "table", (n_seq, None), Q)
+        kp = _ints_ptr(kv_len, "kv_len", (n_seq,), Q)
+    O = _out(O, Q, stream)
+    lp = _lse_ptr(lse, n, h, Q)
+    full = 0
+    if workspace is None:
+        full = qwm_attention_shared_workspace(cache, n, h, n_seq, max_q, max_kv)[1]
+    ws, wp, wn = _scratch(workspace, full, Q, stream)
+    with _on(Q.device):
+        _check("qwm_attention_shared", lib().qwm_attention_shared(
+            ctypes.byref(cache), qp, ldq, n, h, cup, n_seq, max_q, pg, tp, width, kp, max_kv,
+            int(causal), float(scale), _dev_ptr(O, "O", torch.bfloat16), lp, wp, wn,
+            _stream(stream, Q.device)))
+    return O
+
+
+def qwm_cross_attention_workspace(heads_q: int, heads_kv: int, head_dim: int, n_q: int, n_seq: int,
+                                  max_q: int, max_kv: int) -> tuple[int, int]:
+    """(least, full) workspace bytes of qwm_cross_attention."""
+    least, full = ctypes.c_uint64(0), ctypes.c_uint64(0)
+    _check("qwm_cross_attention_workspace", lib().qwm_cross_attention_workspace(
+        heads_q, heads_kv, head_dim, n_q, n_seq, max_q, max_kv, ctypes.byref(least),
+        ctypes.byref(full)))
+    return least.value, full.value
+
+
+def qwm_cross_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu: torch.Tensor,
+                        kv_start: torch.Tensor, kv_len: torch.Tensor, max_q: int, max_kv: int,
+                        O: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                        scale: float = 0.0, workspace: torch.Tensor | None = None,
+                        stream=None) -> torch.Tensor:
+    """Rows cu[b] .. cu[b+1]-1 of Q attend to rows kv_start[b] ..
+    kv_start[b]+kv_len[b]-1 of K and V (strided rows allowed)."""
+    n, h, d = Q.shape
+    qp, ldq = _rows_ptr(Q, "Q")
+    kp, ldk = _rows_ptr(K, "K", Q, None, d)
+    vp, ldv = _rows_ptr(V, "V", Q, K.shape[1], d)
+    if V.shape[0] != K.shape[0]:
+        raise ValueError("K and V differ in rows")
+    n_seq = cu.shape[0] - 1
+    cup = _ints_ptr(cu, "cu", (None,), Q)
+    sp = _ints_ptr(kv_start, "kv_start", (n_seq,), Q)
+    lnp = _ints_ptr(kv_len, "kv_len", (n_seq,), Q)
+    O = _out(O, Q, stream)
+    lp = _lse_ptr(lse, n, h, Q)
+    full = 0
+    if workspace is None:
+        full = qwm_cross_attention_workspace(h, K.shape[1], d, n, n_seq, max_q, max_kv)[1]
+    ws, wp, wn = _scratch(workspace, full, Q, stream)
+    with _on(Q.device):
+        _check("qwm_cross_attention", lib().qwm_cross_attention(
+            qp, ldq, n, h, kp, ldk, vp, ldv, K.shape[0], K.shape[1], d, cup, sp, lnp, n_seq, max_q,
+            max_kv, float(scale), _dev_ptr(O, "O", torch.bfloat16), lp, wp, wn,
+            _stream(stream, Q.device)))
+    return O
+
+
+class PagedKV:
+    """A pool of pages of bf16 keys and values, [n_pages][heads][page_size][head_dim]
+    each; the pools are the caller's tensors (PagedKV.empty allocates them)."""
+
+    def __init__(self, K: torch.Tensor, V: torch.Tensor):
+        if K.dim() != 4 or K.shape != V.shape or K.device != V.device:
+            raise ValueError("K and V must be [n_pages][heads][page_size][head_dim] alike")
+        self.K, self.V = K, V
+        n, h, p, d = K.shape
+        self.pages = qwm_pages(_dev_ptr(K, "K", torch.bfloat16).value,
+                               _dev_ptr(V, "V", torch.bfloat16).value, n, h, d, p, 0)
+
+    @classmethod
+    def empty(cls, n_pages: int, heads: int, page_size: int, head_dim: int, device="cuda"):
+        shape = (n_pages, heads, page_size, head_dim)
+        return cls(*(torch.empty(shape, dtype=torch.bfloat16, device=device) for _ in range(2)))
+
+    def append(self, table, cu, start, K, V, rope=None, pos=None, k_weight=None, eps=1e-6,
+               stream=None):
+        if K.device != self.K.device:
+            raise ValueError(f"K is on {K.device}, the pages on {self.K.device}")
+        qwm_paged_append(self.pages, table, cu, start, K, V, rope, pos, k_weight, eps, stream)
 
 
 # ----------------------------------------------------------------- convenience owner
@@ -305,6 +642,14 @@ class QuantKVCache:
     def attention_ext(self, Q, K_seg=None, V_seg=None, O=None, lse=None, scale=0.0,
                       stream=None):
         return qwm_attention_ext(self.c, Q, K_seg, V_seg, O, lse, scale, stream)
+
+    def attention_shared(self, Q, cu, max_q, pages: PagedKV | None = None, table=None, kv_len=None,
+                         max_kv=0, causal=False, O=None, lse=None, scale=0.0, workspace=None,
+                         stream=None):
+        if Q.device != self.buffers["k_codes"].device:
+            raise ValueError(f"Q is on {Q.device}, the cache on {self.device}")
+        return qwm_attention_shared(self.c, Q, cu, max_q, pages.pages if pages else None, table,
+                                    kv_len, max_kv, causal, O, lse, scale, workspace, stream)
 
     def reconstruct(self, t0=0, n=None, stream=None):
         n = self.len - t0 if n is None else n

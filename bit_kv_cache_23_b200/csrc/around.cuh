@@ -1,0 +1,29 @@
+// around.cuh -- declarations shared by the operators around the packed cache
+// (norm and rotation, paged append, shared-history and cross attention).
+#pragma once
+#include "common.cuh"
+
+namespace qwm {
+
+// Whether an offset, length or page number read from a device array had to be
+// clamped since the last call (1 or 0; -1: CUDA error).
+int read_and_clear_append_fault();
+int read_and_clear_flash_fault();
+int read_and_clear_flash_timeout();
+
+inline bool aligned_to(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
+
+inline int page_shift(const qwm_pages* p) {
+  int s = 0;
+  while ((1 << s) < p->page_size) ++s;
+  return s;
+}
+
+inline bool pages_ok(const qwm_pages* p) {
+  if (!p || !p->K || !p->V || p->n_pages < 1 || p->n_pages > (int64_t(1) << 31) - 1) return false;
+  if (p->heads < 1 || p->heads > 4096 || (p->head_dim != 64 && p->head_dim != 128)) return false;
+  if (p->page_size < 16 || p->page_size > 256 || (p->page_size & (p->page_size - 1))) return false;
+  return p->reserved == 0;
+}
+
+}  // namespace qwm

@@ -1,0 +1,1052 @@
+// attention_bf16.cu -- attention over bf16 keys on the sm_100a tensor cores
+// (tcgen05.mma; S, P and O live in TMEM), for queries whose keys come from two
+// sources in turn: keys that all sequences share, then each sequence's own.
+//   qwm_attention_shared  shared: the packed history, unpacked once per head
+//                         into the workspace; own: pages.
+//   qwm_cross_attention   shared: none; own: rows of an encoder's states.
+//
+//   S = Q K^T,  m = running row maximum,  P = 2^(scale log2e S - m),
+//   l = sum P,  O = sum P V,  out = O / l,  lse = ln 2 (m + log2 l).
+//
+// One CTA serves up to 256 query rows of one key head (two 128-row Q tiles; the
+// query heads that share the key head are rows too) over a range of 128-key
+// tiles; nothing but Q, K, V and the result crosses HBM.  With too few row
+// blocks to fill the GPU the key range is split; each range gives a normalized
+// fp32 partial and its log-sum-exp, which a last kernel merges.
+//
+// 448 threads: warps 0-7 softmax (one row per thread; warp w serves Q tile w/4),
+// warps 8-11 loaders, warps 12 and 13 one issuing thread per Q tile.  The two Q
+// tiles alternate on the tensor cores: while one's softmax runs, the other's
+// products do.  Loaders copy 16-byte pieces into the 128-byte-swizzled layout
+// that the MMA descriptors read, K and V tiles in turn through one ring; pages,
+// strides and ragged ends cost address arithmetic only, and rows behind a
+// sequence's end are written as zeros, so that what lies there (NaN included)
+// never meets a product.
+//
+// Every mbarrier wait is bounded (about 1 s) and reported by qwm_device_status.
+#include <math.h>
+
+#include "around.cuh"
+#include "dequant.cuh"
+#include "tc.cuh"
+
+namespace qwm {
+namespace {
+using namespace tc;
+
+__device__ int g_flash_timeout;
+__device__ int g_flash_fault;  // a length, offset or page number was clamped
+
+constexpr int KT = 128;          // keys per tile
+constexpr int QT = 128;          // query rows per Q tile (TMEM lanes)
+constexpr int ROWS = 2 * QT;     // query rows per CTA
+constexpr int NTHREADS = 448;
+constexpr int W_LOAD = 8, W_MMA = 12;
+constexpr int NLOAD = 128;       // loader threads
+
+template <int D>
+struct Lay {
+  static constexpr uint32_t Q_TILE = QT * D * 2;  // [D / 64 column blocks][128 rows][128 B]
+  static constexpr uint32_t ENT = KT * D * 2;     // one K or V tile, the same layout
+  static constexpr int NST = D == 128 ? 5 : 10;   // ring entries (K, V, K, V, ...)
+  static constexpr int LAG = 3;                   // entries in flight behind the newest
+  static constexpr uint32_t OFF_KV = 2 * Q_TILE;
+  static constexpr uint32_t OFF_BAR = OFF_KV + NST * ENT;
+  static constexpr int B_FULL = 0, B_EMPTY = NST, B_Q = 2 * NST, B_S = B_Q + 1, B_P = B_S + 2,
+                       B_O = B_P + 2, B_DONE = B_O + 2, NBAR = B_DONE + 2;
+  static constexpr uint32_t SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
+};
+static_assert(Lay<128>::SMEM <= 227 * 1024 && Lay<64>::SMEM <= 227 * 1024, "shared memory");
+
+enum { OWN_NONE = 0, OWN_ROWS = 1, OWN_PAGES = 2 };
+
+struct FlashArgs {
+  const uint16_t* Q;
+  int64_t ldq, nq;
+  int Hq, g;           // query heads; query heads per key head
+  const int32_t* cu;   // [n_seq + 1], or null: one sequence of all rows
+  int64_t max_q;       // rows of a sequence at most
+  // keys that every sequence sees first: [heads of the pass][len0][D]
+  const uint16_t *K0, *V0;
+  int64_t len0;
+  // keys of each sequence
+  int own;
+  const uint16_t *K1, *V1;
+  int64_t ldk, ldv, n_kv;       // rows
+  const int32_t *kv_start, *kv_len, *table;
+  int64_t max_kv, n_pages;
+  int width, shift, pool_heads; // pages
+  int causal;
+  float scale_log2;
+  uint16_t* O;
+  float* lse;          // or null
+  int head0;           // first key head of the pass
+  int qblocks, nsplit;
+  int part0;           // first partial of this launch; -1: no partials
+  float *ws_o, *ws_l;  // [partial][nq][Hq][D], [partial][nq][Hq]
+};
+
+// What one CTA does: rows r0 .. r0 + nr - 1 of sequence b (a row is a token
+// and one of the g query heads of key head h), key tiles j0 .. j0 + n - 1.
+struct Work {
+  int64_t tok0;    // first token row of the sequence
+  int64_t nb;      // its tokens
+  int64_t r0;
+  int nr, nqt;     // rows of this CTA; Q tiles with rows
+  int h;
+  int64_t len1;    // own keys
+  int64_t start1;  // first own row (OWN_ROWS)
+  int64_t b;
+  int nt0;         // tiles of the shared keys
+  int j0, n, part;
+};
+
+__device__ __forceinline__ bool work_of(const FlashArgs& A, Work& w) {
+  const int qb = blockIdx.x % A.qblocks, split = blockIdx.x / A.qblocks;
+  w.h = A.head0 + blockIdx.y;
+  w.b = blockIdx.z;
+  w.part = A.part0 + split;
+  bool fault = false;
+  w.tok0 = 0;
+  w.nb = A.nq;
+  if (A.cu) {
+    const int64_t c0 = A.cu[w.b], c1 = A.cu[w.b + 1];
+    fault = c0 < 0 || c1 < c0 || c1 > A.nq;
+    if (!fault) {
+      w.tok0 = c0;
+      w.nb = c1 - c0;
+    } else {
+      w.nb = 0;
+    }
+  }
+  const int64_t rows = (w.nb < A.max_q ? w.nb : A.max_q) * A.g;
+  w.r0 = (int64_t)qb * ROWS;
+  w.len1 = 0;
+  w.start1 = 0;
+  if (A.own != OWN_NONE) {
+    int64_t len = A.kv_len[w.b];
+    int64_t room = A.own == OWN_PAGES ? (int64_t)A.width << A.shift : A.n_kv;
+    if (A.own == OWN_ROWS) {
+      w.start1 = A.kv_start[w.b];
+      fault |= w.start1 < 0 || w.start1 > A.n_kv;
+      w.start1 = w.start1 < 0 ? 0 : w.start1 > A.n_kv ? A.n_kv : w.start1;
+      room -= w.start1;
+    }
+    fault |= len < 0 || len > room;
+    len = len < 0 ? 0 : len > room ? room : len;
+    w.len1 = len < A.max_kv ? len : A.max_kv;
+  }
+  if (fault && threadIdx.x == 0) atomicExch(&g_flash_fault, 1);
+  if (w.r0 >= rows) return false;
+  w.nr = (int)(rows - w.r0 < ROWS ? rows - w.r0 : ROWS);
+  w.nqt = w.nr > QT ? 2 : 1;
+  int64_t seen = w.len1;
+  if (A.causal) {  // own keys that the CTA's last row sees
+    seen = w.len1 - w.nb + (w.r0 + w.nr - 1) / A.g + 1;
+    seen = seen < 0 ? 0 : seen > w.len1 ? w.len1 : seen;
+  }
+  w.nt0 = (int)((A.len0 + KT - 1) / KT);
+  const int64_t nt = w.nt0 + (seen + KT - 1) / KT;
+  w.j0 = (int)(split * nt / A.nsplit);
+  w.n = (int)((split + 1) * nt / A.nsplit) - w.j0;
+  return true;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+__device__ __forceinline__ void timeout_flag() { atomicExch(&g_flash_timeout, 1); }
+
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  const bool w = mbar_wait(bar, parity);
+  return __all_sync(0xffffffffu, w);
+}
+
+// ------------------------------------------------------------------ softmax role
+// The exponent reference m_used moves only when the row maximum has grown by
+// more than TAU (log2 units): P stays below 2^TAU, and O, which accumulates in
+// TMEM, is rescaled in place on such moves only.
+constexpr float TAU = 8.0f;
+
+template <int D>
+__device__ __forceinline__ void store_row(const FlashArgs& A, const Work& w, bool valid, int64_t row,
+                                          uint32_t to, float inv, float lse) {
+  if (A.part0 >= 0) {
+    const size_t at = (size_t)w.part * A.nq * A.Hq + row;
+    if (valid) A.ws_l[at] = lse;
+    float4* dst = reinterpret_cast<float4*>(A.ws_o + at * D);
+#pragma unroll 1
+    for (int c = 0; c < D / 32; ++c) {
+      float o[32];
+      tmem_ld32(to + c * 32, o);
+      if (valid) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          dst[c * 8 + k] = make_float4(o[4 * k] * inv, o[4 * k + 1] * inv, o[4 * k + 2] * inv,
+                                       o[4 * k + 3] * inv);
+      }
+    }
+    return;
+  }
+  if (A.lse && valid) A.lse[row] = lse;
+  uint4* dst = reinterpret_cast<uint4*>(A.O + row * D);
+#pragma unroll 1
+  for (int c = 0; c < D / 32; ++c) {
+    float o[32];
+    tmem_ld32(to + c * 32, o);
+    if (valid) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        dst[c * 4 + k] = make_uint4(pack_bf16(o[8 * k] * inv, o[8 * k + 1] * inv),
+                                    pack_bf16(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                                    pack_bf16(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
+                                    pack_bf16(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+    }
+  }
+}
+
+// 64 scores with those at or behind `lim` hidden.
+__device__ __forceinline__ void hide(float (&s)[64], int lim) {
+#pragma unroll
+  for (int e = 0; e < 64; ++e)
+    if (e >= lim) s[e] = -INFINITY;
+}
+
+__device__ __forceinline__ float max64(const float (&s)[64]) {
+  float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+#pragma unroll
+  for (int e = 0; e < 64; e += 8) {
+    m0 = fmax3(m0, s[e], s[e + 1]);
+    m1 = fmax3(m1, s[e + 2], s[e + 3]);
+    m2 = fmax3(m2, s[e + 4], s[e + 5]);
+    m3 = fmax3(m3, s[e + 6], s[e + 7]);
+  }
+  return fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+}
+
+template <int D>
+__device__ __forceinline__ void softmax_role(const FlashArgs& A, uint64_t* bars, uint32_t tmem,
+                                             const Work& w) {
+  using L = Lay<D>;
+  const int warp = threadIdx.x >> 5, p = warp >> 2;
+  if (p >= w.nqt) return;
+  const int rr = p * QT + (threadIdx.x & 127);  // row in the CTA
+  const bool valid = rr < w.nr;
+  const int64_t r = w.r0 + (valid ? rr : 0);
+  const int64_t tok = r / A.g;
+  const int64_t row = (w.tok0 + tok) * A.Hq + (int64_t)w.h * A.g + (r - tok * A.g);
+  int64_t seen = w.len1;  // own keys that this row sees
+  if (A.causal) {
+    seen = w.len1 - w.nb + tok + 1;
+    seen = seen < 0 ? 0 : seen > w.len1 ? w.len1 : seen;
+  }
+  const uint32_t lane0 = (uint32_t)(32 * (warp & 3)) << 16;
+  const uint32_t ts = tmem + lane0 + 128 * p, to = tmem + lane0 + 256 + 128 * p;
+  float m_used = -INFINITY;
+  uint64_t l2 = 0;  // running row sum, as a pair of partial sums
+  const uint64_t sc2 = f2pack(A.scale_log2, A.scale_log2);
+  for (int t = 0; t < w.n; ++t) {
+    const int j = w.j0 + t;
+    const int64_t left = j < w.nt0 ? A.len0 - (int64_t)j * KT : seen - (int64_t)(j - w.nt0) * KT;
+    const int lim = (int)(left < 0 ? 0 : left < KT ? left : KT);  // visible keys of the tile
+    const bool ragged = __any_sync(0xffffffffu, lim < KT);
+    if (!warp_wait(&bars[L::B_S + p], t & 1)) {
+      if ((threadIdx.x & 31) == 0) timeout_flag();
+      return;
+    }
+    tc_fence_after();
+    float m_row = -INFINITY;
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      float s[64];
+      tmem_ld64(ts + 64 * hf, s);
+      if (ragged) hide(s, lim - 64 * hf);
+      m_row = fmaxf(m_row, max64(s));
+    }
+    m_row *= A.scale_log2;
+    const bool need = m_row > m_used + TAU;  // (-inf + TAU = -inf: the first visible key)
+    if (t == 0) {
+      m_used = m_row;
+    } else if (__any_sync(0xffffffffu, need)) {
+      // every product issued before this tile's S is complete, so O is at rest
+      const float f = need ? ex2(m_used - m_row) : 1.0f;
+#pragma unroll 1
+      for (int c = 0; c < D / 16; ++c) {
+        float o[16];
+        tmem_ld16(to + c * 16, o);
+        uint32_t ou[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) ou[e] = __float_as_uint(o[e] * f);
+        tmem_st16u_nw(to + c * 16, ou);
+      }
+      l2 = ffma2(l2, f2pack(f, f), 0ull);
+      if (need) m_used = m_row;
+    }
+    // a row that has seen no key yet: 2^(-inf - 0) = 0 rather than NaN
+    const float mref = m_used == -INFINITY ? 0.0f : m_used;
+    const uint64_t nm2 = f2pack(-mref, -mref);
+    // P (bf16 pairs; rounded to nearest: 2^-8 relative per weight at most, l sums the
+    // unrounded ones) over the columns of S, keys 2i, 2i+1 in column i
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      float s[32];
+      tmem_ld32(ts + 32 * c, s);
+      uint32_t pk[16];
+#pragma unroll
+      for (int e = 0; e < 32; e += 2) {
+        if (ragged) {
+          if (32 * c + e >= lim) s[e] = -INFINITY;
+          if (32 * c + e + 1 >= lim) s[e + 1] = -INFINITY;
+        }
+        float x0, x1;
+        f2unpack(ffma2(f2pack(s[e], s[e + 1]), sc2, nm2), x0, x1);
+        const float p0 = ex2(x0), p1 = ex2(x1);
+        l2 = fadd2(l2, f2pack(p0, p1));
+        pk[e / 2] = pack_bf16(p0, p1);
+      }
+      tmem_st16u_nw(ts + 16 * c, pk);
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    warp_arrive(&bars[L::B_P + p]);
+  }
+  if (!warp_wait(&bars[L::B_O + p], 0)) {
+    if ((threadIdx.x & 31) == 0) timeout_flag();
+    return;
+  }
+  tc_fence_after();
+  float la, lb;
+  f2unpack(l2, la, lb);
+  const float l = la + lb;
+  store_row<D>(A, w, valid, row, to, l > 0.0f ? 1.0f / l : 0.0f,
+               l > 0.0f ? (m_used + log2f(l)) * 0.6931471805599453f : -INFINITY);
+}
+
+// ------------------------------------------------------------------ loader role
+// One 16-byte piece; `bytes` 16, or 0 to write zeros (the address is then not read).
+__device__ __forceinline__ void cp_async16_z(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+
+// The K (v = 0) or V (v = 1) rows of key tile j into the ring entry at `dst`.
+template <int D>
+__device__ __forceinline__ void issue_tile(const FlashArgs& A, const Work& w, int j, int v,
+                                           uint32_t dst, int tid) {
+  constexpr int C = D / 8;         // 16-byte pieces per row
+  constexpr int STEP = NLOAD / C;  // rows per round
+  const int c = tid % C, rf = tid / C;
+  if (j < w.nt0) {
+    const int64_t k0 = (int64_t)j * KT;
+    const int n = (int)(A.len0 - k0 < KT ? A.len0 - k0 : KT);
+    const uint16_t* src = (v ? A.V0 : A.K0) +
+                          ((int64_t)(w.h - A.head0) * A.len0 + k0) * D + 8 * c;
+#pragma unroll 4
+    for (int r = rf; r < KT; r += STEP)
+      cp_async16_z(dst + sw128_off(r, c, KT), src + (r < n ? r : 0) * D, r < n ? 16u : 0u);
+    return;
+  }
+  const int64_t k0 = (int64_t)(j - w.nt0) * KT;
+  const int n = (int)(w.len1 - k0 < KT ? w.len1 - k0 : KT);  // > 0
+  if (A.own == OWN_ROWS) {
+    const int64_t ld = v ? A.ldv : A.ldk;
+    const uint16_t* src = (v ? A.V1 : A.K1) + (w.start1 + k0) * ld + (int64_t)w.h * D + 8 * c;
+#pragma unroll 4
+    for (int r = rf; r < KT; r += STEP)
+      cp_async16_z(dst + sw128_off(r, c, KT), src + (r < n ? r : 0) * ld, r < n ? 16u : 0u);
+    return;
+  }
+  const uint16_t* pool = (v ? A.V1 : A.K1) + 8 * c;
+  const int32_t* table = A.table + w.b * A.width;
+  const int mask = (1 << A.shift) - 1;
+#pragma unroll 4
+  for (int r = rf; r < KT; r += STEP) {
+    const int64_t k = k0 + (r < n ? r : 0);
+    int64_t page = __ldg(table + (k >> A.shift));
+    bool ok = r < n;
+    if (page < 0 || page >= A.n_pages) {
+      atomicExch(&g_flash_fault, 1);
+      page = 0;
+      ok = false;
+    }
+    const int64_t at = (((page * A.pool_heads + w.h) << A.shift) + (k & mask)) * D;
+    cp_async16_z(dst + sw128_off(r, c, KT), pool + at, ok ? 16u : 0u);
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void load_role(const FlashArgs& A, uint8_t* smem, uint64_t* bars,
+                                          const Work& w) {
+  using L = Lay<D>;
+  const int tid = threadIdx.x - 32 * W_LOAD;
+  const uint32_t base = smem_u32(smem);
+  {  // Q rows, zeros behind the last
+    constexpr int C = D / 8;
+    const int c = tid % C;
+    for (int rr = tid / C; rr < w.nqt * QT; rr += NLOAD / C) {
+      const bool ok = rr < w.nr;
+      const int64_t r = w.r0 + (ok ? rr : 0);
+      const int64_t tok = r / A.g;
+      const uint16_t* src =
+          A.Q + (w.tok0 + tok) * A.ldq + ((int64_t)w.h * A.g + (r - tok * A.g)) * D + 8 * c;
+      cp_async16_z(base + (rr / QT) * L::Q_TILE + sw128_off(rr % QT, c, QT), src, ok ? 16u : 0u);
+    }
+    cp_async_commit();
+  }
+  // entry 2t holds K of tile t, entry 2t + 1 its V; Q counts as the group before
+  const int ne = 2 * w.n;
+  int told = -1;  // the next entry to be announced; -1: Q
+  bool ok = true;
+  auto announce = [&](int upto) {  // groups up to entry `upto` have landed
+    fence_proxy_async_smem();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+      for (int e = told; e <= upto; ++e) mbar_arrive(e < 0 ? &bars[L::B_Q] : &bars[L::B_FULL + e % L::NST]);
+    told = upto + 1;
+  };
+  for (int e = 0; e < ne; ++e) {
+    const int slot = e % L::NST;
+    if (e >= L::NST) {
+      const uint32_t parity = ((e / L::NST) - 1) & 1;
+      if (!__all_sync(0xffffffffu, mbar_test(&bars[L::B_EMPTY + slot], parity))) {
+        // the ring is full: hand over all that was issued, then wait
+        cp_async_wait<0>();
+        if (told < e) announce(e - 1);
+        if (!warp_wait(&bars[L::B_EMPTY + slot], parity)) { ok = false; break; }
+      }
+    }
+    issue_tile<D>(A, w, w.j0 + e / 2, e & 1, base + L::OFF_KV + slot * L::ENT, tid);
+    cp_async_commit();
+    if (e - L::LAG >= told) {
+      cp_async_wait<L::LAG>();
+      announce(e - L::LAG);
+    }
+  }
+  cp_async_wait<0>();
+  if (ok) announce(ne - 1);
+  if (!ok && (threadIdx.x & 31) == 0) timeout_flag();
+}
+
+// ------------------------------------------------------------------ MMA role
+// One thread per Q tile: S = Q K^T of tile t, wait for P, O += P V, then S of
+// tile t + 1, whose columns P occupied.  K's entry is free after S of both Q
+// tiles, V's after both products with P (one commit each).
+template <int D>
+__device__ __forceinline__ void mma_role(uint8_t* smem, uint64_t* bars, uint32_t tmem, int n,
+                                         int p) {
+  using L = Lay<D>;
+  constexpr uint32_t IDQ = idesc_bf16(QT, KT, false, false);
+  constexpr uint32_t IDP = idesc_bf16(QT, D, false, true);
+  const uint32_t base = smem_u32(smem);
+  const uint64_t qd = desc_sw128(base + p * L::Q_TILE, 16, 1024);
+  const uint64_t kd = desc_sw128(base + L::OFF_KV, 16, 1024);
+  // V: channels are the contiguous dimension; its 64-channel blocks lie KT * 128 bytes apart
+  const uint64_t vd = desc_sw128(base + L::OFF_KV, KT * 128, 1024);
+  const uint32_t ts = tmem + 128 * p, to = tmem + 256 + 128 * p;
+  bool ok = mbar_wait(&bars[L::B_Q], 0);
+  tc_fence_after();
+  for (int t = 0; ok && t < n; ++t) {
+    const int ek = 2 * t, ev = 2 * t + 1;
+    const int sk = ek % L::NST, sv = ev % L::NST;
+    if (!mbar_wait(&bars[L::B_FULL + sk], (ek / L::NST) & 1)) { ok = false; break; }
+    tc_fence_after();
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      const uint32_t off = ((k >> 2) * (KT * 128) + (k & 3) * 32) >> 4;
+      mma_bf16_ss(ts, qd + off, kd + ((sk * L::ENT) >> 4) + off, IDQ, k > 0);
+    }
+    mma_commit(&bars[L::B_S + p]);
+    mma_commit(&bars[L::B_EMPTY + sk]);
+    if (!mbar_wait(&bars[L::B_P + p], t & 1)) { ok = false; break; }
+    if (!mbar_wait(&bars[L::B_FULL + sv], (ev / L::NST) & 1)) { ok = false; break; }
+    tc_fence_after();
+#pragma unroll
+    for (int k = 0; k < KT / 16; ++k)
+      mma_bf16_ts(to, ts + 8 * k, vd + ((sv * L::ENT + k * 16 * 128) >> 4), IDP,
+                  (t > 0 || k > 0) ? 1u : 0u);
+    mma_commit(&bars[L::B_EMPTY + sv]);
+    if (t == n - 1) mma_commit(&bars[L::B_O + p]);
+  }
+  mma_commit(&bars[L::B_DONE + p]);
+  if (!mbar_wait(&bars[L::B_DONE + p], 0)) ok = false;
+  if (!ok) timeout_flag();
+}
+
+template <int D>
+__global__ void __launch_bounds__(NTHREADS, 1) flash_kernel(const __grid_constant__ FlashArgs A) {
+  using L = Lay<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Work w;
+  if (!work_of(A, w)) return;
+  if (w.n == 0) {  // no keys in this range
+    const int rr = threadIdx.x;
+    for (int e = rr; e < w.nr * (D / 8); e += NTHREADS) {
+      const int64_t r = w.r0 + e / (D / 8), tok = r / A.g;
+      const int64_t row = (w.tok0 + tok) * A.Hq + (int64_t)w.h * A.g + (r - tok * A.g);
+      const int c = e % (D / 8);
+      if (A.part0 >= 0) {
+        const size_t at = (size_t)w.part * A.nq * A.Hq + row;
+        float4* dst = reinterpret_cast<float4*>(A.ws_o + at * D) + 2 * c;
+        dst[0] = dst[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (c == 0) A.ws_l[at] = -INFINITY;
+      } else {
+        reinterpret_cast<uint4*>(A.O + row * D)[c] = make_uint4(0, 0, 0, 0);
+        if (c == 0 && A.lse) A.lse[row] = -INFINITY;
+      }
+    }
+    return;
+  }
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
+  uint32_t* holder = reinterpret_cast<uint32_t*>(smem + L::OFF_BAR + L::NBAR * 8);
+  const int warp = threadIdx.x / 32;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::NST; ++i) {
+      mbar_init(&bars[L::B_FULL + i], NLOAD / 32);
+      mbar_init(&bars[L::B_EMPTY + i], w.nqt);
+    }
+    mbar_init(&bars[L::B_Q], NLOAD / 32);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars[L::B_S + i], 1);
+      mbar_init(&bars[L::B_P + i], 4);
+      mbar_init(&bars[L::B_O + i], 1);
+      mbar_init(&bars[L::B_DONE + i], 1);
+    }
+    fence_mbar_init();
+  }
+  if (warp == W_MMA) {
+    tmem_alloc(holder, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *holder;
+  if (warp < W_LOAD) {
+    softmax_role<D>(A, bars, tmem, w);
+  } else if (warp < W_MMA) {
+    load_role<D>(A, smem, bars, w);
+  } else {
+    const int p = warp - W_MMA;
+    if ((threadIdx.x & 31) == 0 && p < w.nqt) mma_role<D>(smem, bars, tmem, w.n, p);
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == W_MMA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Merge of `np` partials per (query row, head): one warp per row.  With L_c
+// their log-sum-exps, O = sum_c e^(L_c - L) O_c / sum_c e^(L_c - L), L = max L_c;
+// rows of no sequence, or beyond max_q, stay as they were.
+template <int D>
+__global__ void __launch_bounds__(256) merge_kernel(const float* __restrict__ ws_o,
+                                                    const float* __restrict__ ws_l, int np,
+                                                    int64_t nq, int Hq,
+                                                    const int32_t* __restrict__ cu, int64_t n_seq,
+                                                    int64_t max_q, uint16_t* __restrict__ O,
+                                                    float* __restrict__ lse) {
+  const int64_t rows = nq * Hq;
+  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= rows) return;
+  const int lane = threadIdx.x & 31;
+  const int64_t t = row / Hq;
+  int64_t lo = 0, hi = n_seq;
+  if (t >= __ldg(cu + n_seq) || t < __ldg(cu)) return;
+  while (hi - lo > 1) {
+    const int64_t mid = (lo + hi) >> 1;
+    if (__ldg(cu + mid) <= t) lo = mid;
+    else hi = mid;
+  }
+  const int64_t c0 = __ldg(cu + lo), c1 = __ldg(cu + lo + 1);
+  if (t - c0 >= max_q || c0 < 0 || c1 > nq || c1 <= t) return;
+  float L = -INFINITY;
+  for (int c = lane; c < np; c += 32) L = fmaxf(L, __ldg(ws_l + (size_t)c * rows + row));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) L = fmaxf(L, __shfl_xor_sync(0xffffffffu, L, o));
+  constexpr int V = D / 32;
+  float acc[V], den = 0.0f;
+#pragma unroll
+  for (int e = 0; e < V; ++e) acc[e] = 0.0f;
+  if (L > -INFINITY) {
+    for (int c = 0; c < np; ++c) {
+      const float wt = expf(__ldg(ws_l + (size_t)c * rows + row) - L);
+      const float* o = ws_o + ((size_t)c * rows + row) * D + V * lane;
+      den += wt;
+#pragma unroll
+      for (int e = 0; e < V; e += 2) {
+        const float2 x = __ldg(reinterpret_cast<const float2*>(o + e));
+        acc[e] = fmaf(wt, x.x, acc[e]);
+        acc[e + 1] = fmaf(wt, x.y, acc[e + 1]);
+      }
+    }
+  }
+  const float inv = den > 0.0f ? 1.0f / den : 0.0f;
+#pragma unroll
+  for (int e = 0; e < V; e += 2)
+    *reinterpret_cast<uint32_t*>(O + row * D + V * lane + e) =
+        pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+  if (lse && lane == 0) lse[row] = den > 0.0f ? L + logf(den) : -INFINITY;
+}
+
+// ------------------------------------------------------------------ unpacking
+// K' and V' of the cache's first T tokens, heads h0 .. h0 + gridDim.y - 1, as
+// [head][T][D] bf16, each element summed in fp32 in the order of the cache's
+// reconstruction and rounded once.  A thread owns 16 channels (within one INT2
+// group) of two tokens at a time, so that each basis value that it reads from
+// shared memory serves two; the basis of the block's first token is staged
+// transposed, tokens of another version read theirs from global memory.
+constexpr int UT = 64;  // tokens per block
+
+__device__ __forceinline__ void add_residual(uint4 lo, uint4 hi, uint32_t code, uint32_t par,
+                                             float (&v)[16]) {
+  const float mn = h2f((uint16_t)(par & 0xffffu)), sc = h2f((uint16_t)(par >> 16));
+  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const float c = __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+    v[e] = c + fmaf((float)((code >> (2 * e)) & 3u), sc, mn);
+  }
+}
+
+__device__ __forceinline__ void store16(uint16_t* dst, const float (&v)[16]) {
+  uint4* d = reinterpret_cast<uint4*>(dst);
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    d[k] = make_uint4(pack_bf16(v[8 * k], v[8 * k + 1]), pack_bf16(v[8 * k + 2], v[8 * k + 3]),
+                      pack_bf16(v[8 * k + 4], v[8 * k + 5]), pack_bf16(v[8 * k + 6], v[8 * k + 7]));
+}
+
+template <int D>
+__global__ void __launch_bounds__(256) unpack_kernel(const Dims Dm, const CacheView cv, int64_t T,
+                                                     int h0, uint16_t* __restrict__ Kd,
+                                                     uint16_t* __restrict__ Vd) {
+  constexpr int SL = D / 16;      // 16-channel slices
+  constexpr int TP = 256 / SL;    // tokens per round
+  __shared__ __align__(16) float Us[16 * D];
+  const int h = h0 + blockIdx.y;
+  const int64_t t0 = (int64_t)blockIdx.x * UT;
+  const int r = Dm.r, sl = threadIdx.x % SL, tr = threadIdx.x / SL;
+  const PackedHead p = packed_head(cv, Dm, h);
+  const int ver0 = cv.tokver[t0];
+  if (r > 0) {
+    const float* U = basis_of(cv, Dm, ver0, h);
+    for (int e = threadIdx.x; e < r * D; e += 256) Us[e] = __ldg(U + (size_t)(e % D) * r + e / D);
+  }
+  __syncthreads();
+  const int gi = 16 * sl / Dm.G;
+  uint16_t* kh = Kd + (int64_t)blockIdx.y * T * D + 16 * sl;
+  uint16_t* vh = Vd + (int64_t)blockIdx.y * T * D + 16 * sl;
+  for (int k0 = tr; k0 < UT; k0 += 2 * TP) {
+    float kv[2][16];
+    bool ok[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int64_t t = t0 + k0 + u * TP;
+      ok[u] = k0 + u * TP < UT && t < T;
+      if (!ok[u]) continue;
+      const size_t cs = (size_t)p.centver[t] * p.cstride;
+      const uint4* ck = reinterpret_cast<const uint4*>(
+          p.cent_k + cs + (size_t)load_idx(p.k_idx, t, Dm.idx_bytes) * D + 16 * sl);
+      const uint4* cw = reinterpret_cast<const uint4*>(
+          p.cent_v + cs + (size_t)load_idx(p.v_idx, t, Dm.idx_bytes) * D + 16 * sl);
+      const uint32_t kc = *reinterpret_cast<const uint32_t*>(p.k_codes + t * (D / 4) + 4 * sl);
+      const uint32_t vc = *reinterpret_cast<const uint32_t*>(p.v_codes + t * (D / 4) + 4 * sl);
+      const uint32_t kp = reinterpret_cast<const uint32_t*>(p.k_params)[t * Dm.ng + gi];
+      const uint32_t vp = reinterpret_cast<const uint32_t*>(p.v_params)[t * Dm.ng + gi];
+      add_residual(__ldg(ck), __ldg(ck + 1), kc, kp, kv[u]);
+      float vv[16];
+      add_residual(__ldg(cw), __ldg(cw + 1), vc, vp, vv);
+      store16(vh + t * D, vv);
+    }
+    if (r > 0) {
+      float cr[2][16];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) cr[u][e] = 0.0f;
+      const int64_t ta = t0 + k0, tb = ta + TP;
+      const bool same0 = ok[0] && cv.tokver[ta] == ver0, same1 = ok[1] && cv.tokver[tb] == ver0;
+      const float sa = ok[0] ? h2f(p.k_cscale[ta]) : 0.0f, sb = ok[1] ? h2f(p.k_cscale[tb]) : 0.0f;
+      for (int q = 0; q < r; ++q) {
+        const float ca = ok[0] ? (float)p.k_coef[ta * r + q] * sa : 0.0f;
+        const float cb = ok[1] ? (float)p.k_coef[tb * r + q] * sb : 0.0f;
+        const float4* u4 = reinterpret_cast<const float4*>(Us + q * D + 16 * sl);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float4 x = u4[k];
+          cr[0][4 * k] = fmaf(x.x, ca, cr[0][4 * k]);
+          cr[0][4 * k + 1] = fmaf(x.y, ca, cr[0][4 * k + 1]);
+          cr[0][4 * k + 2] = fmaf(x.z, ca, cr[0][4 * k + 2]);
+          cr[0][4 * k + 3] = fmaf(x.w, ca, cr[0][4 * k + 3]);
+          cr[1][4 * k] = fmaf(x.x, cb, cr[1][4 * k]);
+          cr[1][4 * k + 1] = fmaf(x.y, cb, cr[1][4 * k + 1]);
+          cr[1][4 * k + 2] = fmaf(x.z, cb, cr[1][4 * k + 2]);
+          cr[1][4 * k + 3] = fmaf(x.w, cb, cr[1][4 * k + 3]);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (!ok[u]) continue;
+        const int64_t t = u ? tb : ta;
+        if (!(u ? same1 : same0)) {  // another version than the staged one
+          const float* U = basis_of(cv, Dm, cv.tokver[t], h) + (size_t)16 * sl * r;
+          const float cs = u ? sb : sa;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float a = 0.0f;
+            for (int q = 0; q < r; ++q)
+              a = fmaf(__ldg(U + e * r + q), (float)p.k_coef[t * r + q] * cs, a);
+            cr[u][e] = a;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) kv[u][e] += cr[u][e];
+      }
+    }
+    if (ok[0]) store16(kh + (t0 + k0) * D, kv[0]);
+    if (ok[1]) store16(kh + (t0 + k0 + TP) * D, kv[1]);
+  }
+}
+
+// ------------------------------------------------------------------ host side
+int device_sms() {
+  static int cache[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+  if (!cache[dev]) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+      n = 148;
+    cache[dev] = n;
+  }
+  return cache[dev];
+}
+
+// Key ranges for `units` CTAs over `ntile` tiles each: the count that minimizes
+// (rounds of CTAs on the GPU) x (tiles per range + a fixed cost of 4 tiles).
+int choose_split(int64_t units, int64_t ntile, int most) {
+  const int64_t slots = device_sms();
+  int best = 1;
+  double bestc = 1e300;
+  for (int s = 1; s <= most && s * 2 <= (ntile > 2 ? ntile : 2); ++s) {
+    const double c = (double)((units * s + slots - 1) / slots) * ((double)ntile / s + 4.0);
+    if (c < bestc * 0.98) {
+      bestc = c;
+      best = s;
+    }
+  }
+  return best;
+}
+
+template <int D>
+cudaError_t launch_flash(const FlashArgs& a, int heads, int64_t n_seq, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(flash_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)Lay<D>::SMEM);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((unsigned)((int64_t)a.qblocks * a.nsplit), (unsigned)heads, (unsigned)n_seq);
+  flash_kernel<D><<<grid, NTHREADS, Lay<D>::SMEM, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_flash(int D, const FlashArgs& a, int heads, int64_t n_seq, cudaStream_t s) {
+  return D == 128 ? launch_flash<128>(a, heads, n_seq, s) : launch_flash<64>(a, heads, n_seq, s);
+}
+
+cudaError_t launch_merge(int D, const FlashArgs& a, int np, const int32_t* cu, int64_t n_seq,
+                         int64_t max_q, cudaStream_t s) {
+  const unsigned grid = (unsigned)((a.nq * a.Hq + 7) / 8);
+  if (D == 128)
+    merge_kernel<128><<<grid, 256, 0, s>>>(a.ws_o, a.ws_l, np, a.nq, a.Hq, cu, n_seq, max_q, a.O, a.lse);
+  else
+    merge_kernel<64><<<grid, 256, 0, s>>>(a.ws_o, a.ws_l, np, a.nq, a.Hq, cu, n_seq, max_q, a.O, a.lse);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_unpack(const Dims& D, const CacheView& v, int64_t T, int h0, int heads,
+                          uint16_t* K, uint16_t* V, cudaStream_t s) {
+  const dim3 grid((unsigned)((T + UT - 1) / UT), (unsigned)heads);
+  if (D.d == 128) unpack_kernel<128><<<grid, 256, 0, s>>>(D, v, T, h0, K, V);
+  else unpack_kernel<64><<<grid, 256, 0, s>>>(D, v, T, h0, K, V);
+  return cudaGetLastError();
+}
+
+constexpr int64_t kMaxGridX = (int64_t(1) << 31) - 1;
+
+// Partials that a call may use: as many as 64 MiB hold, 64 at most.
+int partials_of(int64_t n_q, int Hq, int d) {
+  const int64_t one = n_q * Hq * (d + 1) * 4;
+  if (one <= 0) return 0;
+  const int64_t n = (int64_t(64) << 20) / one;
+  return (int)(n > 64 ? 64 : n);
+}
+
+size_t partial_bytes(int np, int64_t n_q, int Hq, int d) {
+  return ((size_t)np * n_q * Hq * (d + 1) * 4 + 255) / 256 * 256;
+}
+
+// How a shared-history call runs.  joined: one CTA takes its rows through the
+// history and then through its branch's own keys.  Otherwise all branches' rows
+// pack into common row blocks for the history, which few rows per branch would
+// leave mostly empty, the own keys follow per branch, and the two are merged.
+struct SharedPlan {
+  bool joined;
+  int np;  // partials that the workspace holds
+};
+
+SharedPlan plan_shared(int64_t T, int g, int d, int64_t n_q, int Hq, int64_t n_seq, int64_t max_q,
+                       int64_t max_kv) {
+  SharedPlan p;
+  const int64_t mq = max_q < n_q ? max_q : n_q;
+  const int64_t apart = (n_q * g + QT - 1) / QT, joined = n_seq * ((mq * g + QT - 1) / QT);
+  p.joined = T == 0 || max_kv == 0 ? T == 0 : joined * 8 <= apart * 9;
+  p.np = partials_of(n_q, Hq, d);
+  if (!p.joined && p.np < 2) p.np = 2;
+  return p;
+}
+
+bool lengths_ok(int64_t n_q, int64_t n_seq, int64_t max_q, int64_t max_kv) {
+  return n_q >= 0 && n_q <= kMaxGridX && n_seq >= 1 && n_seq <= 65535 && max_q >= 0 &&
+         max_q <= kMaxGridX && max_kv >= 0 && max_kv <= kMaxGridX;
+}
+
+}  // namespace
+
+int read_and_clear_flash_timeout() {
+  int v = 0, z = 0;
+  if (cudaMemcpyFromSymbol(&v, g_flash_timeout, sizeof(int)) != cudaSuccess) return -1;
+  if (v) cudaMemcpyToSymbol(g_flash_timeout, &z, sizeof(int));
+  return v;
+}
+
+int read_and_clear_flash_fault() {
+  int v = 0, z = 0;
+  if (cudaMemcpyFromSymbol(&v, g_flash_fault, sizeof(int)) != cudaSuccess) return -1;
+  if (v) cudaMemcpyToSymbol(g_flash_fault, &z, sizeof(int));
+  return v;
+}
+
+}  // namespace qwm
+
+using namespace qwm;
+
+extern "C" qwm_status qwm_attention_shared_workspace(const qwm_cache* c, int64_t n_q,
+                                                     int32_t heads_q, int64_t n_seq, int64_t max_q,
+                                                     int64_t max_kv, uint64_t* least,
+                                                     uint64_t* full) {
+  if (!cache_ok(c) || !least || !full || !lengths_ok(n_q, n_seq, max_q, max_kv) || heads_q < 1 ||
+      heads_q > 65535 || heads_q % c->cfg.heads)
+    return QWM_ERR_INVALID_ARG;
+  const Dims D = dims_of(&c->cfg);
+  const SharedPlan p =
+      plan_shared(c->len, heads_q / D.H, D.d, n_q, heads_q, n_seq, max_q, max_kv);
+  const uint64_t head = (uint64_t)c->len * D.d * 4;
+  const uint64_t part = partial_bytes(p.np, n_q, heads_q, D.d);
+  *least = part + head;
+  *full = part + head * D.H;
+  return QWM_OK;
+}
+
+extern "C" qwm_status qwm_attention_shared(const qwm_cache* c, const void* Q, int64_t ldq,
+                                           int64_t n_q, int32_t heads_q, const int32_t* cu,
+                                           int64_t n_seq, int64_t max_q, const qwm_pages* pages,
+                                           const int32_t* table, int32_t table_width,
+                                           const int32_t* kv_len, int64_t max_kv, int32_t causal,
+                                           float scale, void* O, float* lse, void* workspace,
+                                           uint64_t workspace_bytes, void* stream) {
+  uint64_t least = 0, full = 0;
+  const qwm_status st =
+      qwm_attention_shared_workspace(c, n_q, heads_q, n_seq, max_q, max_kv, &least, &full);
+  if (st != QWM_OK) return st;
+  const Dims D = dims_of(&c->cfg);
+  if (!cu || (n_q > 0 && (!Q || !O)) || ldq < (int64_t)heads_q * D.d || ldq % 8)
+    return QWM_ERR_INVALID_ARG;
+  if (pages) {
+    if (!pages_ok(pages) || pages->heads != D.H || pages->head_dim != D.d || !table || !kv_len ||
+        table_width < 1)
+      return QWM_ERR_INVALID_ARG;
+  } else if (max_kv > 0) {
+    return QWM_ERR_INVALID_ARG;
+  }
+  if (!aligned_to(Q, 16) || !aligned_to(O, 16) || !aligned_to(lse, 4) || !aligned_to(cu, 4) ||
+      !aligned_to(table, 4) || !aligned_to(kv_len, 4) || !aligned_to(workspace, 256) ||
+      (pages && (!aligned_to(pages->K, 16) || !aligned_to(pages->V, 16))))
+    return QWM_ERR_ALIGNMENT;
+  if (c->len > 0 && !c->has_centroids) return QWM_ERR_STATE;
+  if (n_q == 0 || max_q == 0) return QWM_OK;
+  if (workspace_bytes < least || (least > 0 && !workspace)) return QWM_ERR_CAPACITY;
+
+  const int g = heads_q / D.H;
+  const int64_t T = c->len;
+  const SharedPlan plan = plan_shared(T, g, D.d, n_q, heads_q, n_seq, max_q, max_kv);
+  const CacheView v = view_of(c);
+  const cudaStream_t s = (cudaStream_t)stream;
+  const int64_t mq = max_q < n_q ? max_q : n_q;
+  FlashArgs a = {};
+  a.Q = (const uint16_t*)Q;
+  a.ldq = ldq;
+  a.nq = n_q;
+  a.Hq = heads_q;
+  a.g = g;
+  a.max_q = max_q;
+  a.scale_log2 = (scale > 0.0f ? scale : 1.0f / sqrtf((float)D.d)) * 1.4426950408889634f;
+  a.O = (uint16_t*)O;
+  a.lse = lse;
+  a.ws_o = (float*)workspace;
+  a.ws_l = a.ws_o + (size_t)plan.np * n_q * heads_q * D.d;
+  uint8_t* scratch = (uint8_t*)workspace + partial_bytes(plan.np, n_q, heads_q, D.d);
+  // the branches' own keys
+  FlashArgs own = a;
+  own.cu = cu;
+  own.causal = causal != 0;
+  if (pages) {
+    own.own = OWN_PAGES;
+    own.K1 = (const uint16_t*)pages->K;
+    own.V1 = (const uint16_t*)pages->V;
+    own.kv_len = kv_len;
+    own.table = table;
+    own.max_kv = max_kv;
+    own.n_pages = pages->n_pages;
+    own.width = table_width;
+    own.shift = page_shift(pages);
+    own.pool_heads = pages->heads;
+  }
+  own.qblocks = (int)((mq * g + ROWS - 1) / ROWS);
+  // heads per pass: what the workspace holds unpacked
+  const uint64_t head = (uint64_t)T * D.d * 4;
+  int hp = D.H;
+  if (head > 0) {
+    const uint64_t fit = (workspace_bytes - (uint64_t)(scratch - (uint8_t*)workspace)) / head;
+    hp = fit < (uint64_t)D.H ? (int)fit : D.H;
+  }
+  // passes of even size
+  const int passes = (D.H + hp - 1) / hp;
+  hp = (D.H + passes - 1) / passes;
+  const int64_t tiles0 = (T + KT - 1) / KT, tiles1 = (max_kv + KT - 1) / KT;
+  int np = 0;
+  if (plan.joined) {
+    const int ns = plan.np < 2 ? 1
+                               : choose_split((int64_t)own.qblocks * hp * n_seq, tiles0 + tiles1, plan.np);
+    own.nsplit = ns;
+    own.part0 = ns > 1 ? 0 : -1;
+    np = ns > 1 ? ns : 0;
+  } else {
+    const int ns1 = pages && max_kv > 0 ? choose_split((int64_t)own.qblocks * D.H * n_seq, tiles1, plan.np / 2) : 0;
+    a.qblocks = (int)((n_q * g + ROWS - 1) / ROWS);
+    a.max_q = n_q;
+    a.nsplit = choose_split((int64_t)a.qblocks * hp, tiles0, plan.np - ns1);
+    a.part0 = 0;
+    own.part0 = a.nsplit;
+    own.nsplit = ns1;
+    np = a.nsplit + ns1;
+  }
+  FlashArgs& with0 = plan.joined ? own : a;
+  for (int h0 = 0; h0 < D.H; h0 += hp) {
+    const int nh = D.H - h0 < hp ? D.H - h0 : hp;
+    if (T > 0) {
+      with0.K0 = (const uint16_t*)scratch;
+      with0.V0 = with0.K0 + (size_t)nh * T * D.d;
+      with0.len0 = T;
+      if (launch_unpack(D, v, T, h0, nh, (uint16_t*)with0.K0, (uint16_t*)with0.V0, s) != cudaSuccess)
+        return QWM_ERR_CUDA;
+    }
+    with0.head0 = h0;
+    if (launch_flash(D.d, with0, nh, plan.joined ? n_seq : 1, s) != cudaSuccess) return QWM_ERR_CUDA;
+  }
+  if (!plan.joined && own.nsplit > 0 && launch_flash(D.d, own, D.H, n_seq, s) != cudaSuccess)
+    return QWM_ERR_CUDA;
+  if (np > 0 && launch_merge(D.d, a, np, cu, n_seq, max_q, s) != cudaSuccess) return QWM_ERR_CUDA;
+  return QWM_OK;
+}
+
+extern "C" qwm_status qwm_cross_attention_workspace(int32_t heads_q, int32_t heads_kv,
+                                                    int32_t head_dim, int64_t n_q, int64_t n_seq,
+                                                    int64_t max_q, int64_t max_kv, uint64_t* least,
+                                                    uint64_t* full) {
+  if (!least || !full || !lengths_ok(n_q, n_seq, max_q, max_kv) || heads_kv < 1 || heads_q < 1 ||
+      heads_q > 65535 || heads_q % heads_kv || (head_dim != 64 && head_dim != 128))
+    return QWM_ERR_INVALID_ARG;
+  const int64_t mq = max_q < n_q ? max_q : n_q;
+  const int64_t units = (mq * (heads_q / heads_kv) + ROWS - 1) / ROWS * heads_kv * n_seq;
+  const int np = choose_split(units, (max_kv + KT - 1) / KT, partials_of(n_q, heads_q, head_dim));
+  *least = 0;
+  *full = np > 1 ? partial_bytes(np, n_q, heads_q, head_dim) : 0;
+  return QWM_OK;
+}
+
+extern "C" qwm_status qwm_cross_attention(const void* Q, int64_t ldq, int64_t n_q, int32_t heads_q,
+                                          const void* K, int64_t ldk, const void* V, int64_t ldv,
+                                          int64_t n_kv, int32_t heads_kv, int32_t head_dim,
+                                          const int32_t* cu, const int32_t* kv_start,
+                                          const int32_t* kv_len, int64_t n_seq, int64_t max_q,
+                                          int64_t max_kv, float scale, void* O, float* lse,
+                                          void* workspace, uint64_t workspace_bytes, void* stream) {
+  uint64_t least = 0, full = 0;
+  const qwm_status st = qwm_cross_attention_workspace(heads_q, heads_kv, head_dim, n_q, n_seq, max_q,
+                                                      max_kv, &least, &full);
+  if (st != QWM_OK) return st;
+  if (!cu || !kv_start || !kv_len || (n_q > 0 && (!Q || !O)) || n_kv < 0 ||
+      (n_kv > 0 && max_kv > 0 && (!K || !V)) || ldq < (int64_t)heads_q * head_dim || ldq % 8 ||
+      ldk < (int64_t)heads_kv * head_dim || ldk % 8 || ldv < (int64_t)heads_kv * head_dim || ldv % 8)
+    return QWM_ERR_INVALID_ARG;
+  if (!aligned_to(Q, 16) || !aligned_to(K, 16) || !aligned_to(V, 16) || !aligned_to(O, 16) ||
+      !aligned_to(lse, 4) || !aligned_to(cu, 4) || !aligned_to(kv_start, 4) ||
+      !aligned_to(kv_len, 4) || !aligned_to(workspace, 256))
+    return QWM_ERR_ALIGNMENT;
+  if (n_q == 0 || max_q == 0) return QWM_OK;
+  const int g = heads_q / heads_kv;
+  const int64_t mq = max_q < n_q ? max_q : n_q;
+  FlashArgs a = {};
+  a.Q = (const uint16_t*)Q;
+  a.ldq = ldq;
+  a.nq = n_q;
+  a.Hq = heads_q;
+  a.g = g;
+  a.cu = cu;
+  a.max_q = max_q;
+  a.own = OWN_ROWS;
+  a.K1 = (const uint16_t*)K;
+  a.V1 = (const uint16_t*)V;
+  a.ldk = ldk;
+  a.ldv = ldv;
+  a.n_kv = n_kv;
+  a.kv_start = kv_start;
+  a.kv_len = kv_len;
+  a.max_kv = max_kv;
+  a.scale_log2 = (scale > 0.0f ? scale : 1.0f / sqrtf((float)head_dim)) * 1.4426950408889634f;
+  a.O = (uint16_t*)O;
+  a.lse = lse;
+  a.qblocks = (int)((mq * g + ROWS - 1) / ROWS);
+  a.nsplit = 1;
+  a.part0 = -1;
+  if (full > 0 && workspace && workspace_bytes >= full) {
+    const int np = choose_split((int64_t)a.qblocks * heads_kv * n_seq, (max_kv + KT - 1) / KT,
+                                partials_of(n_q, heads_q, head_dim));
+    a.nsplit = np;
+    a.part0 = 0;
+    a.ws_o = (float*)workspace;
+    a.ws_l = a.ws_o + (size_t)np * n_q * heads_q * head_dim;
+  }
+  const cudaStream_t s = (cudaStream_t)stream;
+  if (launch_flash(head_dim, a, heads_kv, n_seq, s) != cudaSuccess) return QWM_ERR_CUDA;
+  if (a.nsplit > 1 && launch_merge(head_dim, a, a.nsplit, cu, n_seq, max_q, s) != cudaSuccess)
+    return QWM_ERR_CUDA;
+  return QWM_OK;
+}

@@ -289,10 +289,165 @@ QWM_API qwm_status qwm_top1_shift(const qwm_cache* c, const void* Q, int64_t n_q
 QWM_API qwm_status qwm_build_centroids_noalloc(qwm_cache* c, const void* K, const void* V,
                                                int64_t n, int32_t iters, void* stream);
 
+/* ------------------------------------------------------------------ around the cache
+ * The rest of an attention layer of a world model: queries and keys are normed
+ * and rotated before they reach the cache, several continuations ("branches")
+ * of one history keep the keys of their own frames in pages, attend over the
+ * shared packed history followed by their own pages, and attend to an
+ * encoder's states.  No counterpart in the pages.
+ *
+ * Conventions of these calls, beside those above:
+ *   - rows of a batch are stored one sequence after another; `cu` [n_seq + 1]
+ *     (int32, device, cu[0] = 0, not falling) holds where each begins.  Rows at
+ *     or behind cu[n_seq] belong to no sequence: their outputs are left as
+ *     they were;
+ *   - a row's heads are contiguous ([heads][head_dim]); the distance between
+ *     rows, `ld`, is given in elements: a multiple of 8, at least
+ *     heads * head_dim, so that parts of a fused projection need no copy;
+ *   - what the device arrays hold (offsets, lengths, page numbers) cannot be
+ *     checked on the host.  The kernels clamp it to the sizes given beside it
+ *     and never read or write outside the buffers; where they had to, bit 1 of
+ *     qwm_device_status is set and the outputs concerned mean nothing. */
+
+#define QWM_ROPE_MAX_PAIRS 64
+#define QWM_ROPE_MAX_AXES 3
+
+typedef enum qwm_rope_layout {
+  QWM_ROPE_HALF = 0,       /* pair i: channels i and i + rot_dim / 2 */
+  QWM_ROPE_INTERLEAVED = 1 /* pair i: channels 2 i and 2 i + 1       */
+} qwm_rope_layout;
+
+/* Frequencies of longer contexts than a model was trained on (s = factor):
+ *   LINEAR  f / s;
+ *   NTK     theta s^(D / (D - 2)) in place of theta, D = channels of the axis;
+ *   PARTS   k f + (1 - k) f / s, k = clamp((turns - beta_slow) / (beta_fast -
+ *           beta_slow), 0, 1), turns = orig_len f / (2 pi); cos and sin are
+ *           multiplied by 0.1 ln s + 1. */
+typedef enum qwm_rope_scaling {
+  QWM_ROPE_SCALE_NONE = 0, QWM_ROPE_SCALE_LINEAR, QWM_ROPE_SCALE_NTK, QWM_ROPE_SCALE_PARTS
+} qwm_rope_scaling;
+
+/* Host-side description of a rotation; filled by qwm_rope_init. */
+typedef struct qwm_rope {
+  int32_t head_dim;
+  int32_t rot_dim;    /* the first rot_dim channels of a head are rotated  */
+  int32_t layout;     /* qwm_rope_layout                                   */
+  int32_t n_axes;     /* position axes (time, height, width)               */
+  int32_t axis_dim[QWM_ROPE_MAX_AXES]; /* channels of each axis            */
+  int32_t magic;
+  double gain;        /* factor of cos and sin                             */
+  double freq[QWM_ROPE_MAX_PAIRS];     /* angle per position of each pair  */
+} qwm_rope;
+
+/* Frequencies theta^(-2 i / D) for the pairs i of each axis (D = axis_dim of
+ * the axis; the axes' pairs follow one another), scaled as chosen.  Host only.
+ * Supported: head_dim 64 or 128; rot_dim a multiple of 16, 16 <= rot_dim <=
+ * head_dim; 1 <= n_axes <= 3 with even axis_dim >= 2 that add up to rot_dim
+ * (null: one axis; NTK needs axis_dim >= 4); theta > 1; factor >= 1; for PARTS
+ * orig_len > 0 and beta_fast > beta_slow >= 0.  Errors: INVALID_ARG. */
+QWM_API qwm_status qwm_rope_init(qwm_rope* r, int32_t head_dim, int32_t rot_dim, int32_t layout,
+                                 double theta, int32_t n_axes, const int32_t* axis_dim,
+                                 int32_t scaling, double factor, double orig_len,
+                                 double beta_fast, double beta_slow);
+
+/* Norm and rotation of n rows of queries and keys in one pass:
+ *   y = x rsqrt(mean_j x_j^2 + eps) w      per head, where w is not null;
+ *   (a, b) -> gain (a cos t - b sin t, a sin t + b cos t) for each pair, t =
+ *   pos freq (fp64) of the pair's axis,    where rope is not null;
+ * in fp32, rounded once.  Q: [n] rows of heads_q heads, ldq apart, written to
+ * Q_out (ldqo apart); K alike.  Either side may have 0 heads (its pointers are
+ * then ignored).  w_q, w_k: [head_dim] bf16 or null (no norm).  pos: [n_axes]
+ * rows of n int32 positions, ldpos apart; any int32 value.  An output may be
+ * its own input (same pointer and ld); other overlaps are not supported.
+ * Without rope and w the call copies.  eps >= 0.
+ * Errors: INVALID_ARG, ALIGNMENT, CUDA. */
+QWM_API qwm_status qwm_norm_rope(const qwm_rope* rope, int32_t head_dim, int64_t n, const void* Q,
+                                 int64_t ldq, int32_t heads_q, const void* w_q, void* Q_out,
+                                 int64_t ldqo, const void* K, int64_t ldk, int32_t heads_k,
+                                 const void* w_k, void* K_out, int64_t ldko, const int32_t* pos,
+                                 int64_t ldpos, float eps, void* stream);
+
+/* A pool of pages of keys and values, owned by the caller; sequences own pages
+ * through tables [n_seq][table_width] of page numbers (int32, device): position
+ * p of a sequence lies in page table[p / page_size], place p % page_size.
+ * page_size: 16, 32, 64, 128 or 256.  K, V: 16-byte aligned. */
+typedef struct qwm_pages {
+  void* K;            /* [n_pages][heads][page_size][head_dim] bf16 */
+  void* V;
+  int64_t n_pages;    /* 1 .. 2^31 - 1                              */
+  int32_t heads;
+  int32_t head_dim;   /* 64 or 128                                  */
+  int32_t page_size;
+  int32_t reserved;   /* 0                                          */
+} qwm_pages;
+
+/* Append rows to paged sequences: row i of sequence b (rows cu[b] .. cu[b+1]-1
+ * of K and V) goes to position start[b] + i, the key after the norm (w_k not
+ * null) and the rotation (rope not null) of qwm_norm_rope, the value as it is.
+ * n: rows of K and V.  Every place is written by one row at most (the caller's
+ * tables share no page that is being written).  n_seq >= 1.
+ * Errors: INVALID_ARG, ALIGNMENT, CUDA. */
+QWM_API qwm_status qwm_paged_append(const qwm_pages* p, const int32_t* table, int64_t n_seq,
+                                    int32_t table_width, const int32_t* cu, const int32_t* start,
+                                    const void* K, int64_t ldk, const void* V, int64_t ldv,
+                                    int64_t n, const qwm_rope* rope, const int32_t* pos,
+                                    int64_t ldpos, const void* w_k, float eps, void* stream);
+
+/* Attention of n_seq branches over one packed history, which all share,
+ * followed by each branch's own paged keys:
+ *   O = softmax(scale Q [K' ; K_b]^T) [V' ; V_b]
+ * with K', V' as in qwm_attention (all `len` cached tokens; len may be 0) and
+ * K_b, V_b the first kv_len[b] positions of branch b's pages.  causal != 0:
+ * row i of the n_b rows of branch b sees its own keys up to position
+ * kv_len[b] - n_b + i only (and the whole history).  Rows without any key give
+ * O = 0 and lse = -inf.  Places of the pages that no row sees may hold anything.
+ * Q: [n_q] rows of heads_q heads, ldq apart; heads_q a multiple of the cache's
+ * heads, query head j attends to key head j / (heads_q / heads).  O: [n_q][heads_q][head_dim].
+ * lse: null or [n_q][heads_q] fp32.  pages, table and kv_len may be null
+ * (history only).  max_q, max_kv: upper bounds of a branch's rows and own keys,
+ * which size the launch: rows and keys beyond them are left out.
+ * workspace: device scratch of this call, 256-byte aligned, not shared with
+ * calls that can run at the same time; at least the `least` bytes of
+ * qwm_attention_shared_workspace; `full` bytes serve all heads in one pass.
+ * Errors: INVALID_ARG, ALIGNMENT, CAPACITY (workspace too small), STATE (a
+ * non-empty cache without centroids), CUDA. */
+QWM_API qwm_status qwm_attention_shared_workspace(const qwm_cache* c, int64_t n_q, int32_t heads_q,
+                                                  int64_t n_seq, int64_t max_q, int64_t max_kv,
+                                                  uint64_t* least, uint64_t* full);
+QWM_API qwm_status qwm_attention_shared(const qwm_cache* c, const void* Q, int64_t ldq, int64_t n_q,
+                                        int32_t heads_q, const int32_t* cu, int64_t n_seq,
+                                        int64_t max_q, const qwm_pages* pages,
+                                        const int32_t* table, int32_t table_width,
+                                        const int32_t* kv_len, int64_t max_kv, int32_t causal,
+                                        float scale, void* O, float* lse, void* workspace,
+                                        uint64_t workspace_bytes, void* stream);
+
+/* Cross attention: row block b of Q (rows cu[b] .. cu[b+1]-1) attends to rows
+ * kv_start[b] .. kv_start[b] + kv_len[b] - 1 of K and V (n_kv rows of heads_kv
+ * heads, ldk and ldv apart), an encoder's states of any other length, padded or
+ * packed.  No mask.  kv_len[b] = 0 gives O = 0 and lse = -inf.  heads_q a
+ * multiple of heads_kv.  head_dim 64 or 128.  max_q, max_kv, O, lse, workspace
+ * and errors as for qwm_attention_shared (`least` may be 0 bytes: then
+ * workspace may be null). */
+QWM_API qwm_status qwm_cross_attention_workspace(int32_t heads_q, int32_t heads_kv,
+                                                 int32_t head_dim, int64_t n_q, int64_t n_seq,
+                                                 int64_t max_q, int64_t max_kv, uint64_t* least,
+                                                 uint64_t* full);
+QWM_API qwm_status qwm_cross_attention(const void* Q, int64_t ldq, int64_t n_q, int32_t heads_q,
+                                       const void* K, int64_t ldk, const void* V, int64_t ldv,
+                                       int64_t n_kv, int32_t heads_kv, int32_t head_dim,
+                                       const int32_t* cu, const int32_t* kv_start,
+                                       const int32_t* kv_len, int64_t n_seq, int64_t max_q,
+                                       int64_t max_kv, float scale, void* O, float* lse,
+                                       void* workspace, uint64_t workspace_bytes, void* stream);
+
 /* Device-side health check: synchronizes the current device, then reads and
  * clears the flag that the tensor-core kernels set when one of their bounded
  * waits gave up (about one second per wait) instead of hanging.  *flags = 1 and
  * QWM_ERR_TIMEOUT if any wait timed out since the last call, else 0 and QWM_OK.
+ * Bit 1 of *flags (value 2, QWM_ERR_INVALID_ARG when no wait timed out): an
+ * offset, length or page number in a device array lay outside its buffer and
+ * was clamped.
  * Errors: INVALID_ARG (null), CUDA. */
 QWM_API qwm_status qwm_device_status(int32_t* flags);
 
