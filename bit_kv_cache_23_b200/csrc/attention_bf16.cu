@@ -9,21 +9,29 @@
 //   l = sum P,  O = sum P V,  out = O / l,  lse = ln 2 (m + log2 l).
 //
 // One CTA serves up to 256 query rows of one key head (two 128-row Q tiles; the
-// query heads that share the key head are rows too) over a range of 128-key
+// query heads that share the key head are rows too) over a range of 64-key
 // tiles; nothing but Q, K, V and the result crosses HBM.  With too few row
 // blocks to fill the GPU the key range is split; each range gives a normalized
 // fp32 partial and its log-sum-exp, which a last kernel merges.
 //
-// 448 threads: warps 0-7 softmax (one row per thread; warp w serves Q tile w/4),
-// warps 8-11 loaders, warps 12 and 13 one issuing thread per Q tile.  The two Q
-// tiles alternate on the tensor cores: while one's softmax runs, the other's
-// products do.  Loaders copy 16-byte pieces into the 128-byte-swizzled layout
-// that the MMA descriptors read, K and V tiles in turn through one ring; pages,
-// strides and ragged ends cost address arithmetic only, and rows behind a
-// sequence's end are written as zeros, so that what lies there (NaN included)
-// never meets a product.
+// 352 threads: warps 0-7 softmax (one row per thread; warpgroup p serves group
+// p), warp 8 the loader, warps 9 and 10 one issuing thread per group.  A group
+// is one of the two Q tiles or, when there is only one, its even or its odd key
+// tiles (joined at the end through shared memory).  Each group has two score
+// buffers in TMEM, so that Q K^T of the next tiles runs while the softmax works
+// on this one, and neither softmax group ever waits for a product it has just
+// asked for: with one buffer of 128 keys both groups waited together and then
+// shared the exponential unit, 5000 clocks per 128 keys of 256 rows.
+//
+// K and V tiles go through one ring of TMA boxes in the 128-byte-swizzled layout
+// that the MMA descriptors read (one box per 64 channels and, for pages, per
+// page).  What lies behind a sequence's end never meets a product: boxes beyond
+// a tensor arrive as zeros, and the loader overwrites the V rows behind the end
+// of the last tile with zeros (scores of hidden keys are replaced, so K rows may
+// hold anything).
 //
 // Every mbarrier wait is bounded (about 1 s) and reported by qwm_device_status.
+#include <cuda.h>
 #include <math.h>
 
 #include "around.cuh"
@@ -37,24 +45,37 @@ using namespace tc;
 __device__ int g_flash_timeout;
 __device__ int g_flash_fault;  // a length, offset or page number was clamped
 
-constexpr int KT = 128;          // keys per tile
+constexpr int KT = 64;           // keys per tile
 constexpr int QT = 128;          // query rows per Q tile (TMEM lanes)
 constexpr int ROWS = 2 * QT;     // query rows per CTA
-constexpr int NTHREADS = 448;
-constexpr int W_LOAD = 8, W_MMA = 12;
-constexpr int NLOAD = 128;       // loader threads
+constexpr int NTHREADS = 352;
+constexpr int W_LOAD = 8, W_MMA = 9;
 
 template <int D>
 struct Lay {
   static constexpr uint32_t Q_TILE = QT * D * 2;  // [D / 64 column blocks][128 rows][128 B]
-  static constexpr uint32_t ENT = KT * D * 2;     // one K or V tile, the same layout
-  static constexpr int NST = D == 128 ? 5 : 10;   // ring entries (K, V, K, V, ...)
-  static constexpr int LAG = 3;                   // entries in flight behind the newest
+  static constexpr uint32_t ENT = KT * D * 2;     // one K or V tile, [D / 64][64 rows][128 B]
+  // Ring entries (K, V, K, V, ...), of an even number of tiles: when the groups
+  // take even and odd tiles, each slot then serves one group, which sees every
+  // phase of the slot's barrier.  (Copies land out of order; a group that waits
+  // for a slot's next phase but one finds the parity of the phase before.)
+  static constexpr int NST = D == 128 ? 8 : 16;
+  static_assert(NST % 4 == 0, "an even number of K and V tiles");
   static constexpr uint32_t OFF_KV = 2 * Q_TILE;
   static constexpr uint32_t OFF_BAR = OFF_KV + NST * ENT;
-  static constexpr int B_FULL = 0, B_EMPTY = NST, B_Q = 2 * NST, B_S = B_Q + 1, B_P = B_S + 2,
-                       B_O = B_P + 2, B_DONE = B_O + 2, NBAR = B_DONE + 2;
-  static constexpr uint32_t SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
+  static constexpr int B_FULL = 0,        // loader -> MMA
+                       B_EMPTY = NST,     // MMA commits -> loader
+                       B_Q = 2 * NST,     // softmax warps: Q is in shared memory
+                       B_S = B_Q + 1,     // [group][buffer] commit of Q K^T -> softmax
+                       B_P = B_S + 4,     // [group][buffer] softmax -> MMA
+                       B_PV = B_P + 4,    // [group] commit of P V -> softmax
+                       B_O = B_PV + 2,    // [group] commit of the last P V -> softmax
+                       B_DONE = B_O + 2,  // [group] drain before exit
+                       B_M = B_DONE + 2,  // odd tiles' result in shared memory
+                       B_RAG = B_M + 1,   // a ragged V tile has landed -> loader
+                       NBAR = B_RAG + 1;
+  static constexpr uint32_t OFF_LSE = OFF_BAR + NBAR * 8 + 16;
+  static constexpr uint32_t SMEM = OFF_LSE + QT * 4 + 1024;
 };
 static_assert(Lay<128>::SMEM <= 227 * 1024 && Lay<64>::SMEM <= 227 * 1024, "shared memory");
 
@@ -66,13 +87,12 @@ struct FlashArgs {
   int Hq, g;           // query heads; query heads per key head
   const int32_t* cu;   // [n_seq + 1], or null: one sequence of all rows
   int64_t max_q;       // rows of a sequence at most
-  // keys that every sequence sees first: [heads of the pass][len0][D]
-  const uint16_t *K0, *V0;
+  // keys that every sequence sees first (maps: channel, key, head of the pass)
   int64_t len0;
-  // keys of each sequence
+  // keys of each sequence (maps: channel, key head, row; pages: channel, head and
+  // place in the page, page)
   int own;
-  const uint16_t *K1, *V1;
-  int64_t ldk, ldv, n_kv;       // rows
+  int64_t n_kv;                 // rows
   const int32_t *kv_start, *kv_len, *table;
   int64_t max_kv, n_pages;
   int width, shift, pool_heads; // pages
@@ -84,6 +104,7 @@ struct FlashArgs {
   int qblocks, nsplit;
   int part0;           // first partial of this launch; -1: no partials
   float *ws_o, *ws_l;  // [partial][nq][Hq][D], [partial][nq][Hq]
+  CUtensorMap k0, v0, k1, v1;
 };
 
 // What one CTA does: rows r0 .. r0 + nr - 1 of sequence b (a row is a token
@@ -92,13 +113,20 @@ struct Work {
   int64_t tok0;    // first token row of the sequence
   int64_t nb;      // its tokens
   int64_t r0;
-  int nr, nqt;     // rows of this CTA; Q tiles with rows
+  int nr;          // rows of this CTA
+  int parity;      // 1: one Q tile; the groups take its even and odd key tiles
+  int groups;      // active groups (softmax warpgroup and issuing thread)
   int h;
   int64_t len1;    // own keys
   int64_t start1;  // first own row (OWN_ROWS)
   int64_t b;
   int nt0;         // tiles of the shared keys
   int j0, n, part;
+  // rows in group p's Q tile
+  __device__ __forceinline__ int rows_of(int p) const {
+    const int left = nr - (parity ? 0 : p * QT);
+    return left < QT ? left : QT;
+  }
 };
 
 __device__ __forceinline__ bool work_of(const FlashArgs& A, Work& w) {
@@ -139,7 +167,6 @@ __device__ __forceinline__ bool work_of(const FlashArgs& A, Work& w) {
   if (fault && threadIdx.x == 0) atomicExch(&g_flash_fault, 1);
   if (w.r0 >= rows) return false;
   w.nr = (int)(rows - w.r0 < ROWS ? rows - w.r0 : ROWS);
-  w.nqt = w.nr > QT ? 2 : 1;
   int64_t seen = w.len1;
   if (A.causal) {  // own keys that the CTA's last row sees
     seen = w.len1 - w.nb + (w.r0 + w.nr - 1) / A.g + 1;
@@ -149,12 +176,14 @@ __device__ __forceinline__ bool work_of(const FlashArgs& A, Work& w) {
   const int64_t nt = w.nt0 + (seen + KT - 1) / KT;
   w.j0 = (int)(split * nt / A.nsplit);
   w.n = (int)((split + 1) * nt / A.nsplit) - w.j0;
+  w.parity = w.nr <= QT && w.n > 1;
+  w.groups = w.nr > QT || w.parity ? 2 : 1;
   return true;
 }
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
-  asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
@@ -182,107 +211,152 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
 // TMEM, is rescaled in place on such moves only.
 constexpr float TAU = 8.0f;
 
+__device__ __forceinline__ float max64(const float (&s)[64]) {
+  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int e = 0; e < 64; e += 8)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m[k] = fmax3(m[k], s[e + 2 * k], s[e + 2 * k + 1]);
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// P = 2^(sc S - m) of one row's 64 scores over the columns of S (bf16 pairs, keys
+// 2i, 2i+1 in column i; rounded to nearest: 2^-8 relative per weight at most, l2
+// sums the unrounded ones).
+__device__ __forceinline__ void weights(float (&s)[64], uint64_t sc2, uint64_t nm2,
+                                        uint64_t (&l2)[2], uint32_t ts) {
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int e = 32 * c; e < 32 * c + 32; e += 2) {
+      f2unpack(ffma2(f2pack(s[e], s[e + 1]), sc2, nm2), s[e], s[e + 1]);
+      s[e] = ex2(s[e]);
+      s[e + 1] = ex2(s[e + 1]);
+    }
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+      l2[0] = fadd2(l2[0], f2pack(s[32 * c + e], s[32 * c + e + 1]));
+      l2[1] = fadd2(l2[1], f2pack(s[32 * c + e + 2], s[32 * c + e + 3]));
+      pk[e / 2] = pack_bf16(s[32 * c + e], s[32 * c + e + 1]);
+      pk[e / 2 + 1] = pack_bf16(s[32 * c + e + 2], s[32 * c + e + 3]);
+    }
+    tmem_st16u_nw(ts + 16 * c, pk);
+  }
+}
+
+// Row r's place among O's rows.
+__device__ __forceinline__ int64_t out_row(const FlashArgs& A, const Work& w, int64_t r) {
+  const int64_t tok = r / A.g;
+  return (w.tok0 + tok) * A.Hq + (int64_t)w.h * A.g + (r - tok * A.g);
+}
+
+// One row of O from TMEM, times `inv` (plus, where `more` is set, `w1` times the
+// other group's row in shared memory), to O or to this CTA's partial.
 template <int D>
 __device__ __forceinline__ void store_row(const FlashArgs& A, const Work& w, bool valid, int64_t row,
-                                          uint32_t to, float inv, float lse) {
-  if (A.part0 >= 0) {
-    const size_t at = (size_t)w.part * A.nq * A.Hq + row;
-    if (valid) A.ws_l[at] = lse;
-    float4* dst = reinterpret_cast<float4*>(A.ws_o + at * D);
-#pragma unroll 1
-    for (int c = 0; c < D / 32; ++c) {
-      float o[32];
-      tmem_ld32(to + c * 32, o);
-      if (valid) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          dst[c * 8 + k] = make_float4(o[4 * k] * inv, o[4 * k + 1] * inv, o[4 * k + 2] * inv,
-                                       o[4 * k + 3] * inv);
-      }
-    }
-    return;
+                                          uint32_t to, float inv, float lse, const float4* more,
+                                          int swz, float w1) {
+  const size_t at = A.part0 >= 0 ? (size_t)w.part * A.nq * A.Hq + row : (size_t)row;
+  if (valid) {
+    if (A.part0 >= 0) A.ws_l[at] = lse;
+    else if (A.lse) A.lse[at] = lse;
   }
-  if (A.lse && valid) A.lse[row] = lse;
-  uint4* dst = reinterpret_cast<uint4*>(A.O + row * D);
 #pragma unroll 1
   for (int c = 0; c < D / 32; ++c) {
     float o[32];
     tmem_ld32(to + c * 32, o);
-    if (valid) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) o[e] *= inv;
+    if (more) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float4 x = more[(8 * c + k) ^ swz];
+        o[4 * k] = fmaf(w1, x.x, o[4 * k]);
+        o[4 * k + 1] = fmaf(w1, x.y, o[4 * k + 1]);
+        o[4 * k + 2] = fmaf(w1, x.z, o[4 * k + 2]);
+        o[4 * k + 3] = fmaf(w1, x.w, o[4 * k + 3]);
+      }
+    }
+    if (!valid) continue;
+    if (A.part0 >= 0) {
+      float4* dst = reinterpret_cast<float4*>(A.ws_o + at * D) + 8 * c;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+    } else {
+      uint4* dst = reinterpret_cast<uint4*>(A.O + at * D) + 4 * c;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        dst[c * 4 + k] = make_uint4(pack_bf16(o[8 * k] * inv, o[8 * k + 1] * inv),
-                                    pack_bf16(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
-                                    pack_bf16(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
-                                    pack_bf16(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+        dst[k] = make_uint4(pack_bf16(o[8 * k], o[8 * k + 1]), pack_bf16(o[8 * k + 2], o[8 * k + 3]),
+                            pack_bf16(o[8 * k + 4], o[8 * k + 5]),
+                            pack_bf16(o[8 * k + 6], o[8 * k + 7]));
     }
   }
-}
-
-// 64 scores with those at or behind `lim` hidden.
-__device__ __forceinline__ void hide(float (&s)[64], int lim) {
-#pragma unroll
-  for (int e = 0; e < 64; ++e)
-    if (e >= lim) s[e] = -INFINITY;
-}
-
-__device__ __forceinline__ float max64(const float (&s)[64]) {
-  float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
-#pragma unroll
-  for (int e = 0; e < 64; e += 8) {
-    m0 = fmax3(m0, s[e], s[e + 1]);
-    m1 = fmax3(m1, s[e + 2], s[e + 3]);
-    m2 = fmax3(m2, s[e + 4], s[e + 5]);
-    m3 = fmax3(m3, s[e + 6], s[e + 7]);
-  }
-  return fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
 }
 
 template <int D>
-__device__ __forceinline__ void softmax_role(const FlashArgs& A, uint64_t* bars, uint32_t tmem,
-                                             const Work& w) {
+__device__ __forceinline__ void softmax_role(const FlashArgs& A, uint8_t* smem, uint64_t* bars,
+                                             uint32_t tmem, const Work& w) {
   using L = Lay<D>;
-  const int warp = threadIdx.x >> 5, p = warp >> 2;
-  if (p >= w.nqt) return;
-  const int rr = p * QT + (threadIdx.x & 127);  // row in the CTA
+  const int warp = threadIdx.x >> 5, p = warp >> 2, lane = threadIdx.x & 127;
+  {  // Q rows into shared memory, zeros behind the last
+    constexpr int C = D / 8;
+    const int c = threadIdx.x % C;
+    for (int rr = threadIdx.x / C; rr < (w.nr > QT ? 2 : 1) * QT; rr += 256 / C) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (rr < w.nr) {
+        const int64_t r = w.r0 + rr, tok = r / A.g;
+        v = __ldg(reinterpret_cast<const uint4*>(
+            A.Q + (w.tok0 + tok) * A.ldq + ((int64_t)w.h * A.g + (r - tok * A.g)) * D + 8 * c));
+      }
+      *reinterpret_cast<uint4*>(smem + (rr / QT) * L::Q_TILE + sw128_off(rr % QT, c, QT)) = v;
+    }
+    fence_proxy_async_smem();
+    warp_arrive(&bars[L::B_Q]);
+  }
+  if (p >= w.groups || 32 * (warp & 3) >= w.rows_of(p)) return;
+  const int rr = (w.parity ? 0 : p * QT) + lane;  // row in the CTA
   const bool valid = rr < w.nr;
   const int64_t r = w.r0 + (valid ? rr : 0);
-  const int64_t tok = r / A.g;
-  const int64_t row = (w.tok0 + tok) * A.Hq + (int64_t)w.h * A.g + (r - tok * A.g);
-  int64_t seen = w.len1;  // own keys that this row sees
+  int seen = (int)w.len1;  // own keys that this row sees
   if (A.causal) {
-    seen = w.len1 - w.nb + tok + 1;
-    seen = seen < 0 ? 0 : seen > w.len1 ? w.len1 : seen;
+    const int64_t x = w.len1 - w.nb + r / A.g + 1;
+    seen = x < 0 ? 0 : x > w.len1 ? (int)w.len1 : (int)x;
   }
+  // tiles with hidden keys: the shared keys' last, if not full, and own ones
+  // from the first that some row of the warp does not see whole
+  int cut0 = (int)(A.len0 % KT);
+  if (cut0 == 0) cut0 = KT;
+  const int whole = w.nt0 + __reduce_min_sync(0xffffffffu, seen) / KT;
   const uint32_t lane0 = (uint32_t)(32 * (warp & 3)) << 16;
-  const uint32_t ts = tmem + lane0 + 128 * p, to = tmem + lane0 + 256 + 128 * p;
+  const uint32_t ts0 = tmem + lane0 + 128 * p, to = tmem + lane0 + 256 + 128 * p;
   float m_used = -INFINITY;
-  uint64_t l2 = 0;  // running row sum, as a pair of partial sums
+  uint64_t l2[2] = {0, 0};  // running row sum, as pairs of partial sums
   const uint64_t sc2 = f2pack(A.scale_log2, A.scale_log2);
-  for (int t = 0; t < w.n; ++t) {
+  bool ok = true;
+  int i = 0;
+  for (int t = w.parity ? p : 0; t < w.n; t += 1 + w.parity, ++i) {
     const int j = w.j0 + t;
-    const int64_t left = j < w.nt0 ? A.len0 - (int64_t)j * KT : seen - (int64_t)(j - w.nt0) * KT;
-    const int lim = (int)(left < 0 ? 0 : left < KT ? left : KT);  // visible keys of the tile
-    const bool ragged = __any_sync(0xffffffffu, lim < KT);
-    if (!warp_wait(&bars[L::B_S + p], t & 1)) {
-      if ((threadIdx.x & 31) == 0) timeout_flag();
-      return;
-    }
+    const uint32_t ts = ts0 + 64 * (i & 1);
+    if (!warp_wait(&bars[L::B_S + 2 * p + (i & 1)], (i >> 1) & 1)) { ok = false; break; }
     tc_fence_after();
-    float m_row = -INFINITY;
+    float s[64];
+    tmem_ld64(ts, s);
+    if ((j == w.nt0 - 1 && cut0 < KT) || j >= whole) {
+      const int lim = j < w.nt0 ? cut0 : seen - (j - w.nt0) * KT;  // visible keys
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      float s[64];
-      tmem_ld64(ts + 64 * hf, s);
-      if (ragged) hide(s, lim - 64 * hf);
-      m_row = fmaxf(m_row, max64(s));
+      for (int e = 0; e < 64; ++e)
+        if (e >= lim) s[e] = -INFINITY;
     }
-    m_row *= A.scale_log2;
+    const float m_row = max64(s) * A.scale_log2;
     const bool need = m_row > m_used + TAU;  // (-inf + TAU = -inf: the first visible key)
-    if (t == 0) {
+    if (i == 0) {
       m_used = m_row;
     } else if (__any_sync(0xffffffffu, need)) {
-      // every product issued before this tile's S is complete, so O is at rest
+      // O is at rest once the last product with P is complete (this tile's waits for P)
+      if (!warp_wait(&bars[L::B_PV + p], (i - 1) & 1)) { ok = false; break; }
+      tc_fence_after();
       const float f = need ? ex2(m_used - m_row) : 1.0f;
 #pragma unroll 1
       for (int c = 0; c < D / 16; ++c) {
@@ -293,193 +367,194 @@ __device__ __forceinline__ void softmax_role(const FlashArgs& A, uint64_t* bars,
         for (int e = 0; e < 16; ++e) ou[e] = __float_as_uint(o[e] * f);
         tmem_st16u_nw(to + c * 16, ou);
       }
-      l2 = ffma2(l2, f2pack(f, f), 0ull);
+      l2[0] = ffma2(l2[0], f2pack(f, f), 0ull);
+      l2[1] = ffma2(l2[1], f2pack(f, f), 0ull);
       if (need) m_used = m_row;
     }
     // a row that has seen no key yet: 2^(-inf - 0) = 0 rather than NaN
     const float mref = m_used == -INFINITY ? 0.0f : m_used;
     const uint64_t nm2 = f2pack(-mref, -mref);
-    // P (bf16 pairs; rounded to nearest: 2^-8 relative per weight at most, l sums the
-    // unrounded ones) over the columns of S, keys 2i, 2i+1 in column i
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      float s[32];
-      tmem_ld32(ts + 32 * c, s);
-      uint32_t pk[16];
-#pragma unroll
-      for (int e = 0; e < 32; e += 2) {
-        if (ragged) {
-          if (32 * c + e >= lim) s[e] = -INFINITY;
-          if (32 * c + e + 1 >= lim) s[e + 1] = -INFINITY;
-        }
-        float x0, x1;
-        f2unpack(ffma2(f2pack(s[e], s[e + 1]), sc2, nm2), x0, x1);
-        const float p0 = ex2(x0), p1 = ex2(x1);
-        l2 = fadd2(l2, f2pack(p0, p1));
-        pk[e / 2] = pack_bf16(p0, p1);
-      }
-      tmem_st16u_nw(ts + 16 * c, pk);
-    }
+    weights(s, sc2, nm2, l2, ts);
     tmem_wait_st();
     tc_fence_before();
-    warp_arrive(&bars[L::B_P + p]);
+    warp_arrive(&bars[L::B_P + 2 * p + (i & 1)]);
   }
-  if (!warp_wait(&bars[L::B_O + p], 0)) {
+  if (ok) ok = warp_wait(&bars[L::B_O + p], 0);
+  // the groups of a parity pair meet: shared memory is free once both are done
+  if (ok && w.parity) ok = warp_wait(&bars[L::B_O + 1 - p], 0);
+  if (!ok) {
     if ((threadIdx.x & 31) == 0) timeout_flag();
     return;
   }
   tc_fence_after();
   float la, lb;
-  f2unpack(l2, la, lb);
+  f2unpack(fadd2(l2[0], l2[1]), la, lb);
   const float l = la + lb;
-  store_row<D>(A, w, valid, row, to, l > 0.0f ? 1.0f / l : 0.0f,
-               l > 0.0f ? (m_used + log2f(l)) * 0.6931471805599453f : -INFINITY);
+  float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  float lse = l > 0.0f ? (m_used + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  const int swz = lane & (D / 4 - 1);  // spreads the rows over the banks
+  float4* mine = reinterpret_cast<float4*>(smem) + lane * (D / 4);
+  float* lses = reinterpret_cast<float*>(smem + L::OFF_LSE);
+  float w1 = 0.0f;
+  if (w.parity) {
+    if (p == 1) {
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        float o[32];
+        tmem_ld32(to + c * 32, o);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mine[(8 * c + k) ^ swz] = make_float4(o[4 * k] * inv, o[4 * k + 1] * inv,
+                                                o[4 * k + 2] * inv, o[4 * k + 3] * inv);
+      }
+      lses[lane] = lse;
+      warp_arrive(&bars[L::B_M]);
+      return;
+    }
+    if (!warp_wait(&bars[L::B_M], 0)) {
+      if ((threadIdx.x & 31) == 0) timeout_flag();
+      return;
+    }
+    const float lse1 = lses[lane], top = fmaxf(lse, lse1);
+    if (top > -INFINITY) {
+      const float a = expf(lse - top), b = expf(lse1 - top), den = 1.0f / (a + b);
+      inv *= a * den;
+      w1 = b * den;
+      lse = top + logf(a + b);
+    }
+  }
+  store_row<D>(A, w, valid, out_row(A, w, r), to, inv, lse, w.parity ? mine : nullptr, swz, w1);
 }
 
 // ------------------------------------------------------------------ loader role
-// One 16-byte piece; `bytes` 16, or 0 to write zeros (the address is then not read).
-__device__ __forceinline__ void cp_async16_z(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
-}
-
-// The K (v = 0) or V (v = 1) rows of key tile j into the ring entry at `dst`.
+// The boxes of K (v = 0) or V (v = 1) rows of key tile j into the ring entry at
+// `dst`, ENT bytes in all; one thread.
 template <int D>
 __device__ __forceinline__ void issue_tile(const FlashArgs& A, const Work& w, int j, int v,
-                                           uint32_t dst, int tid) {
-  constexpr int C = D / 8;         // 16-byte pieces per row
-  constexpr int STEP = NLOAD / C;  // rows per round
-  const int c = tid % C, rf = tid / C;
+                                           uint32_t dst, uint64_t* bar) {
+  constexpr uint32_t BLK = KT * 128;  // bytes of 64 channels of the tile
   if (j < w.nt0) {
-    const int64_t k0 = (int64_t)j * KT;
-    const int n = (int)(A.len0 - k0 < KT ? A.len0 - k0 : KT);
-    const uint16_t* src = (v ? A.V0 : A.K0) +
-                          ((int64_t)(w.h - A.head0) * A.len0 + k0) * D + 8 * c;
-#pragma unroll 4
-    for (int r = rf; r < KT; r += STEP)
-      cp_async16_z(dst + sw128_off(r, c, KT), src + (r < n ? r : 0) * D, r < n ? 16u : 0u);
+    const CUtensorMap* m = v ? &A.v0 : &A.k0;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c)
+      tma_load_3d(dst + c * BLK, m, 64 * c, j * KT, w.h - A.head0, bar);
     return;
   }
+  const CUtensorMap* m = v ? &A.v1 : &A.k1;
   const int64_t k0 = (int64_t)(j - w.nt0) * KT;
-  const int n = (int)(w.len1 - k0 < KT ? w.len1 - k0 : KT);  // > 0
   if (A.own == OWN_ROWS) {
-    const int64_t ld = v ? A.ldv : A.ldk;
-    const uint16_t* src = (v ? A.V1 : A.K1) + (w.start1 + k0) * ld + (int64_t)w.h * D + 8 * c;
-#pragma unroll 4
-    for (int r = rf; r < KT; r += STEP)
-      cp_async16_z(dst + sw128_off(r, c, KT), src + (r < n ? r : 0) * ld, r < n ? 16u : 0u);
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c)
+      tma_load_3d(dst + c * BLK, m, 64 * c, w.h, (int)(w.start1 + k0), bar);
     return;
   }
-  const uint16_t* pool = (v ? A.V1 : A.K1) + 8 * c;
+  const int psize = 1 << A.shift, rows = psize < KT ? psize : KT;
   const int32_t* table = A.table + w.b * A.width;
-  const int mask = (1 << A.shift) - 1;
-#pragma unroll 4
-  for (int r = rf; r < KT; r += STEP) {
-    const int64_t k = k0 + (r < n ? r : 0);
-    int64_t page = __ldg(table + (k >> A.shift));
-    bool ok = r < n;
-    if (page < 0 || page >= A.n_pages) {
-      atomicExch(&g_flash_fault, 1);
-      page = 0;
-      ok = false;
+  for (int r = 0; r < KT; r += rows) {
+    // pages behind the end, and page numbers outside the pool, arrive as zeros
+    int64_t page = A.n_pages;
+    if (k0 + r < w.len1) {
+      const int32_t at = __ldg(table + ((k0 + r) >> A.shift));
+      if (at >= 0 && at < A.n_pages) page = at;
+      else atomicExch(&g_flash_fault, 1);
     }
-    const int64_t at = (((page * A.pool_heads + w.h) << A.shift) + (k & mask)) * D;
-    cp_async16_z(dst + sw128_off(r, c, KT), pool + at, ok ? 16u : 0u);
+    const int y = (w.h << A.shift) + (int)((k0 + r) & (psize - 1));
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c)
+      tma_load_3d(dst + c * BLK + r * 128, m, 64 * c, y, (int)page, bar);
   }
 }
 
+// One warp; entry 2t holds K of tile t, entry 2t + 1 its V.
 template <int D>
 __device__ __forceinline__ void load_role(const FlashArgs& A, uint8_t* smem, uint64_t* bars,
                                           const Work& w) {
   using L = Lay<D>;
-  const int tid = threadIdx.x - 32 * W_LOAD;
+  const int lane = threadIdx.x & 31;
   const uint32_t base = smem_u32(smem);
-  {  // Q rows, zeros behind the last
-    constexpr int C = D / 8;
-    const int c = tid % C;
-    for (int rr = tid / C; rr < w.nqt * QT; rr += NLOAD / C) {
-      const bool ok = rr < w.nr;
-      const int64_t r = w.r0 + (ok ? rr : 0);
-      const int64_t tok = r / A.g;
-      const uint16_t* src =
-          A.Q + (w.tok0 + tok) * A.ldq + ((int64_t)w.h * A.g + (r - tok * A.g)) * D + 8 * c;
-      cp_async16_z(base + (rr / QT) * L::Q_TILE + sw128_off(rr % QT, c, QT), src, ok ? 16u : 0u);
-    }
-    cp_async_commit();
-  }
-  // entry 2t holds K of tile t, entry 2t + 1 its V; Q counts as the group before
-  const int ne = 2 * w.n;
-  int told = -1;  // the next entry to be announced; -1: Q
   bool ok = true;
-  auto announce = [&](int upto) {  // groups up to entry `upto` have landed
-    fence_proxy_async_smem();
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0)
-      for (int e = told; e <= upto; ++e) mbar_arrive(e < 0 ? &bars[L::B_Q] : &bars[L::B_FULL + e % L::NST]);
-    told = upto + 1;
-  };
-  for (int e = 0; e < ne; ++e) {
+  int rag = 0, e = 0;
+  for (; e < 2 * w.n; ++e) {
     const int slot = e % L::NST;
-    if (e >= L::NST) {
-      const uint32_t parity = ((e / L::NST) - 1) & 1;
-      if (!__all_sync(0xffffffffu, mbar_test(&bars[L::B_EMPTY + slot], parity))) {
-        // the ring is full: hand over all that was issued, then wait
-        cp_async_wait<0>();
-        if (told < e) announce(e - 1);
-        if (!warp_wait(&bars[L::B_EMPTY + slot], parity)) { ok = false; break; }
-      }
+    if (e >= L::NST && !warp_wait(&bars[L::B_EMPTY + slot], ((e / L::NST) - 1) & 1)) {
+      ok = false;
+      break;
     }
-    issue_tile<D>(A, w, w.j0 + e / 2, e & 1, base + L::OFF_KV + slot * L::ENT, tid);
-    cp_async_commit();
-    if (e - L::LAG >= told) {
-      cp_async_wait<L::LAG>();
-      announce(e - L::LAG);
+    const int j = w.j0 + e / 2;
+    const int64_t left = j < w.nt0 ? KT : w.len1 - (int64_t)(j - w.nt0) * KT;
+    const uint32_t dst = base + L::OFF_KV + slot * L::ENT;
+    // V rows behind the end are overwritten before the tile is handed on
+    const bool wipe = (e & 1) && left < KT;
+    uint64_t* bar = &bars[wipe ? L::B_RAG : L::B_FULL + slot];
+    if (lane == 0) {
+      mbar_arrive_expect_tx(bar, L::ENT);
+      issue_tile<D>(A, w, j, e & 1, dst, bar);
+    }
+    __syncwarp();
+    if (wipe) {
+      if (!warp_wait(bar, rag++ & 1)) { ok = false; ++e; break; }
+      constexpr int C = D / 8;
+      for (int x = (int)left * C + lane; x < KT * C; x += 32)
+        *reinterpret_cast<uint4*>(smem + L::OFF_KV + slot * L::ENT + sw128_off(x / C, x % C, KT)) =
+            make_uint4(0, 0, 0, 0);
+      fence_proxy_async_smem();
+      warp_arrive(&bars[L::B_FULL + slot]);
     }
   }
-  cp_async_wait<0>();
-  if (ok) announce(ne - 1);
-  if (!ok && (threadIdx.x & 31) == 0) timeout_flag();
+  // every box issued has landed before the CTA may exit
+  for (int k = e > L::NST ? e - L::NST : 0; k < e; ++k)
+    if (!warp_wait(&bars[L::B_FULL + k % L::NST], (k / L::NST) & 1)) ok = false;
+  if (!ok && lane == 0) timeout_flag();
 }
 
 // ------------------------------------------------------------------ MMA role
-// One thread per Q tile: S = Q K^T of tile t, wait for P, O += P V, then S of
-// tile t + 1, whose columns P occupied.  K's entry is free after S of both Q
-// tiles, V's after both products with P (one commit each).
+// One thread per group: two tiles' S = Q K^T ahead, then for each tile O += P V
+// and S of the tile after the next, into the buffer that P occupied (the tensor
+// core works in issue order).  A commit tells when all before it is complete.
 template <int D>
-__device__ __forceinline__ void mma_role(uint8_t* smem, uint64_t* bars, uint32_t tmem, int n,
-                                         int p) {
+__device__ __forceinline__ void mma_role(uint8_t* smem, uint64_t* bars, uint32_t tmem,
+                                         const Work& w, int p) {
   using L = Lay<D>;
   constexpr uint32_t IDQ = idesc_bf16(QT, KT, false, false);
   constexpr uint32_t IDP = idesc_bf16(QT, D, false, true);
   const uint32_t base = smem_u32(smem);
-  const uint64_t qd = desc_sw128(base + p * L::Q_TILE, 16, 1024);
+  const uint64_t qd = desc_sw128(base + (w.parity ? 0 : p * L::Q_TILE), 16, 1024);
   const uint64_t kd = desc_sw128(base + L::OFF_KV, 16, 1024);
   // V: channels are the contiguous dimension; its 64-channel blocks lie KT * 128 bytes apart
   const uint64_t vd = desc_sw128(base + L::OFF_KV, KT * 128, 1024);
-  const uint32_t ts = tmem + 128 * p, to = tmem + 256 + 128 * p;
-  bool ok = mbar_wait(&bars[L::B_Q], 0);
-  tc_fence_after();
-  for (int t = 0; ok && t < n; ++t) {
-    const int ek = 2 * t, ev = 2 * t + 1;
-    const int sk = ek % L::NST, sv = ev % L::NST;
-    if (!mbar_wait(&bars[L::B_FULL + sk], (ek / L::NST) & 1)) { ok = false; break; }
+  const uint32_t ts0 = tmem + 128 * p, to = tmem + 256 + 128 * p;
+  const int step = 1 + w.parity;
+  auto full = [&](int e) { return mbar_wait(&bars[L::B_FULL + e % L::NST], (e / L::NST) & 1); };
+  auto scores = [&](int t, int i) {  // S of tile t, the group's i-th
+    if (!full(2 * t)) return false;
     tc_fence_after();
+    const int slot = 2 * t % L::NST;
+    const uint64_t k0 = kd + ((slot * L::ENT) >> 4);
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
-      const uint32_t off = ((k >> 2) * (KT * 128) + (k & 3) * 32) >> 4;
-      mma_bf16_ss(ts, qd + off, kd + ((sk * L::ENT) >> 4) + off, IDQ, k > 0);
+      const uint32_t in = (k & 3) * 32;
+      mma_bf16_ss(ts0 + 64 * (i & 1), qd + (((k >> 2) * (QT * 128) + in) >> 4),
+                  k0 + (((k >> 2) * (KT * 128) + in) >> 4), IDQ, k > 0);
     }
-    mma_commit(&bars[L::B_S + p]);
-    mma_commit(&bars[L::B_EMPTY + sk]);
-    if (!mbar_wait(&bars[L::B_P + p], t & 1)) { ok = false; break; }
-    if (!mbar_wait(&bars[L::B_FULL + sv], (ev / L::NST) & 1)) { ok = false; break; }
+    mma_commit(&bars[L::B_S + 2 * p + (i & 1)]);
+    mma_commit(&bars[L::B_EMPTY + slot]);
+    return true;
+  };
+  int t = w.parity ? p : 0;
+  bool ok = mbar_wait(&bars[L::B_Q], 0) && scores(t, 0) && (t + step >= w.n || scores(t + step, 1));
+  for (int i = 0; ok && t < w.n; t += step, ++i) {
+    const int slot = (2 * t + 1) % L::NST;
+    ok = full(2 * t + 1) && mbar_wait(&bars[L::B_P + 2 * p + (i & 1)], (i >> 1) & 1);
+    if (!ok) break;
     tc_fence_after();
+    const uint64_t v0 = vd + ((slot * L::ENT) >> 4);
 #pragma unroll
     for (int k = 0; k < KT / 16; ++k)
-      mma_bf16_ts(to, ts + 8 * k, vd + ((sv * L::ENT + k * 16 * 128) >> 4), IDP,
-                  (t > 0 || k > 0) ? 1u : 0u);
-    mma_commit(&bars[L::B_EMPTY + sv]);
-    if (t == n - 1) mma_commit(&bars[L::B_O + p]);
+      mma_bf16_ts(to, ts0 + 64 * (i & 1) + 8 * k, v0 + ((k * 16 * 128) >> 4), IDP,
+                  (i > 0 || k > 0) ? 1u : 0u);
+    mma_commit(&bars[t + step < w.n ? L::B_PV + p : L::B_O + p]);
+    mma_commit(&bars[L::B_EMPTY + slot]);
+    if (t + 2 * step < w.n) ok = scores(t + 2 * step, i + 2);
   }
   mma_commit(&bars[L::B_DONE + p]);
   if (!mbar_wait(&bars[L::B_DONE + p], 0)) ok = false;
@@ -516,16 +591,22 @@ __global__ void __launch_bounds__(NTHREADS, 1) flash_kernel(const __grid_constan
   const int warp = threadIdx.x / 32;
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::NST; ++i) {
-      mbar_init(&bars[L::B_FULL + i], NLOAD / 32);
-      mbar_init(&bars[L::B_EMPTY + i], w.nqt);
+      mbar_init(&bars[L::B_FULL + i], 1);
+      mbar_init(&bars[L::B_EMPTY + i], w.parity ? 1 : w.groups);
     }
-    mbar_init(&bars[L::B_Q], NLOAD / 32);
+    mbar_init(&bars[L::B_Q], 8);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars[L::B_S + i], 1);
-      mbar_init(&bars[L::B_P + i], 4);
+      const int warps = i < w.groups ? (w.rows_of(i) + 31) / 32 : 1;
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&bars[L::B_S + 2 * i + b], 1);
+        mbar_init(&bars[L::B_P + 2 * i + b], warps);
+      }
+      mbar_init(&bars[L::B_PV + i], 1);
       mbar_init(&bars[L::B_O + i], 1);
       mbar_init(&bars[L::B_DONE + i], 1);
     }
+    mbar_init(&bars[L::B_M], (w.nr + 31) / 32);
+    mbar_init(&bars[L::B_RAG], 1);
     fence_mbar_init();
   }
   if (warp == W_MMA) {
@@ -537,12 +618,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) flash_kernel(const __grid_constan
   tc_fence_after();
   const uint32_t tmem = *holder;
   if (warp < W_LOAD) {
-    softmax_role<D>(A, bars, tmem, w);
+    softmax_role<D>(A, smem, bars, tmem, w);
   } else if (warp < W_MMA) {
     load_role<D>(A, smem, bars, w);
   } else {
     const int p = warp - W_MMA;
-    if ((threadIdx.x & 31) == 0 && p < w.nqt) mma_role<D>(smem, bars, tmem, w.n, p);
+    if ((threadIdx.x & 31) == 0 && p < w.groups) mma_role<D>(smem, bars, tmem, w, p);
     __syncwarp();
   }
   tc_fence_before();
@@ -741,19 +822,52 @@ int device_sms() {
 }
 
 // Key ranges for `units` CTAs over `ntile` tiles each: the count that minimizes
-// (rounds of CTAs on the GPU) x (tiles per range + a fixed cost of 4 tiles).
+// (rounds of CTAs on the GPU) x (tiles per range + a fixed cost of 8 tiles).
 int choose_split(int64_t units, int64_t ntile, int most) {
   const int64_t slots = device_sms();
   int best = 1;
   double bestc = 1e300;
-  for (int s = 1; s <= most && s * 2 <= (ntile > 2 ? ntile : 2); ++s) {
-    const double c = (double)((units * s + slots - 1) / slots) * ((double)ntile / s + 4.0);
+  for (int s = 1; s <= most && s * 4 <= (ntile > 4 ? ntile : 4); ++s) {
+    const double c = (double)((units * s + slots - 1) / slots) * ((double)ntile / s + 8.0);
     if (c < bestc * 0.98) {
       bestc = c;
       best = s;
     }
   }
   return best;
+}
+
+// The driver's encoder of tensor maps (no link to the driver library).
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                              CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                              CUtensorMapFloatOOBfill);
+
+EncodeFn encoder() {
+  static const EncodeFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return (EncodeFn)f;
+  }();
+  return fn;
+}
+
+// Map of bf16 [n2][n1][D] with the given distances in elements; boxes of 64
+// channels by b1 by b2, 128-byte swizzle.
+bool map_3d(CUtensorMap* m, const void* base, int D, int64_t n1, int64_t ld1, int64_t n2, int64_t ld2,
+            int b1, int b2) {
+  const EncodeFn fn = encoder();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)n1, (cuuint64_t)n2};
+  const cuuint64_t strides[2] = {(cuuint64_t)ld1 * 2, (cuuint64_t)ld2 * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)b1, (cuuint32_t)b2};
+  const cuuint32_t one[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D>
@@ -918,8 +1032,12 @@ extern "C" qwm_status qwm_attention_shared(const qwm_cache* c, const void* Q, in
   own.causal = causal != 0;
   if (pages) {
     own.own = OWN_PAGES;
-    own.K1 = (const uint16_t*)pages->K;
-    own.V1 = (const uint16_t*)pages->V;
+    const int64_t rows = (int64_t)pages->heads * pages->page_size;
+    const int box = pages->page_size < KT ? pages->page_size : KT;
+    if (max_kv > 0 &&
+        (!map_3d(&own.k1, pages->K, D.d, rows, D.d, pages->n_pages, rows * D.d, box, 1) ||
+         !map_3d(&own.v1, pages->V, D.d, rows, D.d, pages->n_pages, rows * D.d, box, 1)))
+      return QWM_ERR_CUDA;
     own.kv_len = kv_len;
     own.table = table;
     own.max_kv = max_kv;
@@ -961,10 +1079,12 @@ extern "C" qwm_status qwm_attention_shared(const qwm_cache* c, const void* Q, in
   for (int h0 = 0; h0 < D.H; h0 += hp) {
     const int nh = D.H - h0 < hp ? D.H - h0 : hp;
     if (T > 0) {
-      with0.K0 = (const uint16_t*)scratch;
-      with0.V0 = with0.K0 + (size_t)nh * T * D.d;
+      uint16_t* const K0 = (uint16_t*)scratch;
+      uint16_t* const V0 = K0 + (size_t)nh * T * D.d;
       with0.len0 = T;
-      if (launch_unpack(D, v, T, h0, nh, (uint16_t*)with0.K0, (uint16_t*)with0.V0, s) != cudaSuccess)
+      if (!map_3d(&with0.k0, K0, D.d, T, D.d, nh, T * D.d, KT, 1) ||
+          !map_3d(&with0.v0, V0, D.d, T, D.d, nh, T * D.d, KT, 1) ||
+          launch_unpack(D, v, T, h0, nh, K0, V0, s) != cudaSuccess)
         return QWM_ERR_CUDA;
     }
     with0.head0 = h0;
@@ -1022,11 +1142,11 @@ extern "C" qwm_status qwm_cross_attention(const void* Q, int64_t ldq, int64_t n_
   a.cu = cu;
   a.max_q = max_q;
   a.own = OWN_ROWS;
-  a.K1 = (const uint16_t*)K;
-  a.V1 = (const uint16_t*)V;
-  a.ldk = ldk;
-  a.ldv = ldv;
   a.n_kv = n_kv;
+  if (n_kv > 0 && max_kv > 0 &&
+      (!map_3d(&a.k1, K, head_dim, heads_kv, head_dim, n_kv, ldk, 1, KT) ||
+       !map_3d(&a.v1, V, head_dim, heads_kv, head_dim, n_kv, ldv, 1, KT)))
+    return QWM_ERR_CUDA;
   a.kv_start = kv_start;
   a.kv_len = kv_len;
   a.max_kv = max_kv;

@@ -281,6 +281,8 @@ def test_shared_bad_device_arrays():
     (64, 1, 5, (300,), (1500,), False, False),                # the same in one range (no workspace)
     (128, 4, 1, (513,), (1025,), True, True),
     (128, 1, 1, (1,), (5000,), False, True),                  # one row, many ranges
+    (128, 12, 1, (8,), (16300,), False, False),               # few rows, bound by memory: many laps of the ring
+    (64, 16, 1, (3, 1), (16300, 9000), False, False),
 ])
 def test_cross_attention(d, Hk, gh, new, states, padded, split):
     g = _gen(d + sum(states))
