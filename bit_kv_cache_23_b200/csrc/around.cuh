@@ -10,6 +10,18 @@ namespace qwm {
 int read_and_clear_append_fault();
 int read_and_clear_flash_fault();
 int read_and_clear_flash_timeout();
+int read_and_clear_rows_timeout();
+
+// Attention of few rows per head over the packed tokens (attention_rows.cu): one
+// fp32 partial per row, query head and slot; empty slots get a log-sum-exp of -inf.
+struct RowsPlan {
+  int grid, slots;
+};
+bool rows_supported(const Dims& D, int64_t rows);  // rows: query rows per key head
+RowsPlan rows_plan(const Dims& D, int64_t T, int sms, int most);  // at most `most` >= 3 slots
+cudaError_t launch_rows(const Dims& D, const CacheView& v, int64_t T, const uint16_t* Q, int64_t ldq,
+                        int64_t nq, int Hq, float scale_log2, const RowsPlan& plan, float* ws_o,
+                        float* ws_l, cudaStream_t s);
 
 inline bool aligned_to(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
 

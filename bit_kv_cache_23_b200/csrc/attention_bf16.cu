@@ -669,6 +669,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const float* __restrict__ ws
   if (L > -INFINITY) {
     for (int c = 0; c < np; ++c) {
       const float wt = expf(__ldg(ws_l + (size_t)c * rows + row) - L);
+      if (wt == 0.0f) continue;  // (an empty partial's values are not written)
       const float* o = ws_o + ((size_t)c * rows + row) * D + V * lane;
       den += wt;
 #pragma unroll
@@ -920,18 +921,22 @@ size_t partial_bytes(int np, int64_t n_q, int Hq, int d) {
 // history and then through its branch's own keys.  Otherwise all branches' rows
 // pack into common row blocks for the history, which few rows per branch would
 // leave mostly empty, the own keys follow per branch, and the two are merged.
+// With few rows in all the history is not unpacked at all (attention_rows.cu).
 struct SharedPlan {
-  bool joined;
+  bool joined, rows;
   int np;  // partials that the workspace holds
 };
 
-SharedPlan plan_shared(int64_t T, int g, int d, int64_t n_q, int Hq, int64_t n_seq, int64_t max_q,
+SharedPlan plan_shared(const Dims& D, int64_t T, int Hq, int64_t n_q, int64_t n_seq, int64_t max_q,
                        int64_t max_kv) {
   SharedPlan p;
+  const int g = Hq / D.H, d = D.d;
   const int64_t mq = max_q < n_q ? max_q : n_q;
   const int64_t apart = (n_q * g + QT - 1) / QT, joined = n_seq * ((mq * g + QT - 1) / QT);
   p.joined = T == 0 || max_kv == 0 ? T == 0 : joined * 8 <= apart * 9;
   p.np = partials_of(n_q, Hq, d);
+  p.rows = T > 0 && p.np >= 8 && rows_supported(D, n_q * g);
+  if (p.rows) p.joined = false;
   if (!p.joined && p.np < 2) p.np = 2;
   return p;
 }
@@ -969,9 +974,8 @@ extern "C" qwm_status qwm_attention_shared_workspace(const qwm_cache* c, int64_t
       heads_q > 65535 || heads_q % c->cfg.heads)
     return QWM_ERR_INVALID_ARG;
   const Dims D = dims_of(&c->cfg);
-  const SharedPlan p =
-      plan_shared(c->len, heads_q / D.H, D.d, n_q, heads_q, n_seq, max_q, max_kv);
-  const uint64_t head = (uint64_t)c->len * D.d * 4;
+  const SharedPlan p = plan_shared(D, c->len, heads_q, n_q, n_seq, max_q, max_kv);
+  const uint64_t head = p.rows ? 0 : (uint64_t)c->len * D.d * 4;
   const uint64_t part = partial_bytes(p.np, n_q, heads_q, D.d);
   *least = part + head;
   *full = part + head * D.H;
@@ -1009,7 +1013,7 @@ extern "C" qwm_status qwm_attention_shared(const qwm_cache* c, const void* Q, in
 
   const int g = heads_q / D.H;
   const int64_t T = c->len;
-  const SharedPlan plan = plan_shared(T, g, D.d, n_q, heads_q, n_seq, max_q, max_kv);
+  const SharedPlan plan = plan_shared(D, T, heads_q, n_q, n_seq, max_q, max_kv);
   const CacheView v = view_of(c);
   const cudaStream_t s = (cudaStream_t)stream;
   const int64_t mq = max_q < n_q ? max_q : n_q;
@@ -1048,7 +1052,7 @@ extern "C" qwm_status qwm_attention_shared(const qwm_cache* c, const void* Q, in
   }
   own.qblocks = (int)((mq * g + ROWS - 1) / ROWS);
   // heads per pass: what the workspace holds unpacked
-  const uint64_t head = (uint64_t)T * D.d * 4;
+  const uint64_t head = plan.rows ? 0 : (uint64_t)T * D.d * 4;
   int hp = D.H;
   if (head > 0) {
     const uint64_t fit = (workspace_bytes - (uint64_t)(scratch - (uint8_t*)workspace)) / head;
@@ -1067,16 +1071,23 @@ extern "C" qwm_status qwm_attention_shared(const qwm_cache* c, const void* Q, in
     np = ns > 1 ? ns : 0;
   } else {
     const int ns1 = pages && max_kv > 0 ? choose_split((int64_t)own.qblocks * D.H * n_seq, tiles1, plan.np / 2) : 0;
-    a.qblocks = (int)((n_q * g + ROWS - 1) / ROWS);
-    a.max_q = n_q;
-    a.nsplit = choose_split((int64_t)a.qblocks * hp, tiles0, plan.np - ns1);
+    if (plan.rows) {
+      const RowsPlan rp = rows_plan(D, T, device_sms(), plan.np - ns1);
+      a.nsplit = rp.slots;
+      if (launch_rows(D, v, T, a.Q, ldq, n_q, heads_q, a.scale_log2, rp, a.ws_o, a.ws_l, s) != cudaSuccess)
+        return QWM_ERR_CUDA;
+    } else {
+      a.qblocks = (int)((n_q * g + ROWS - 1) / ROWS);
+      a.max_q = n_q;
+      a.nsplit = choose_split((int64_t)a.qblocks * hp, tiles0, plan.np - ns1);
+    }
     a.part0 = 0;
     own.part0 = a.nsplit;
     own.nsplit = ns1;
     np = a.nsplit + ns1;
   }
   FlashArgs& with0 = plan.joined ? own : a;
-  for (int h0 = 0; h0 < D.H; h0 += hp) {
+  for (int h0 = 0; h0 < D.H && !plan.rows; h0 += hp) {
     const int nh = D.H - h0 < hp ? D.H - h0 : hp;
     if (T > 0) {
       uint16_t* const K0 = (uint16_t*)scratch;

@@ -233,15 +233,39 @@ def test_attention_shared(d, H, gh, T, new, own, page, causal):
 def test_shared_history_is_the_reconstruction(C, G, r, d):
     """The unpacked history is the bf16 cache that the reconstruction returns, bit for bit: it is read
     back from the workspace, which ends with it (keys, then values)."""
-    c, Kp, Vp, rows, kv, table, Q, cu, lens = _shared_case(d, 2, 1, 701, (3,), (20,), 16, False, 5, C=C, G=G, r=r)
-    full = q.qwm_attention_shared_workspace(c.c, Q.shape[0], 2, 1, 3, 20)[1]
+    c, Kp, Vp, rows, kv, table, Q, cu, lens = _shared_case(d, 2, 1, 701, (70,), (20,), 16, False, 5, C=C, G=G, r=r)
+    full = q.qwm_attention_shared_workspace(c.c, Q.shape[0], 2, 1, 70, 20)[1]
     ws = torch.zeros(full, dtype=torch.uint8, device="cuda")
-    c.attention_shared(Q, cu, 3, kv, table, lens, 20, workspace=ws)
+    c.attention_shared(Q, cu, 70, kv, table, lens, 20, workspace=ws)
     _fine()
     n = 2 * 701 * d
     tail = ws[full - 4 * n:].view(torch.int16)
     assert torch.equal(tail[:n].view(2, 701, d), Kp.view(torch.int16))
     assert torch.equal(tail[n:].view(2, 701, d), Vp.view(torch.int16))
+
+
+@pytest.mark.parametrize("C,G,r,d,T,rows", [
+    (256, 32, 8, 128, 4000, 8),     # both tables in shared memory; keys of two basis versions in one tile
+    (300, 32, 8, 128, 1000, 16),    # tables read through the cache, 16-bit centroid numbers
+    (512, 16, 3, 64, 1500, 32),     # two row tiles
+    (40, 16, 8, 128, 129, 1),       # a chunk of one key
+    (16, 32, 1, 64, 1, 5),          # a single key
+    (64, 32, 0, 128, 777, 17),      # no compensation
+    (64, 32, 9, 128, 777, 17),      # a rank that the few-row kernel does not serve
+])
+def test_few_rows_over_the_history(C, G, r, d, T, rows):
+    H, g = 3, _gen(C + T)
+    c = _cache(g, H, d, T, C, G, r)
+    Kp, Vp = c.reconstruct()
+    Q = randn(g, rows, H, d).to(BF16)
+    lse = torch.empty(rows, H, device="cuda")
+    O = c.attention_shared(Q, ints([0, rows]), rows, lse=lse)
+    _fine()
+    for h in range(H):
+        want, bound, wl, lb = attend(Q[:, h], Kp[h], Vp[h], 1 / math.sqrt(d))
+        check("O", O[:, h], want, bound)
+        check_lse("lse", lse[:, h], wl, lb)
+    assert torch.equal(O, c.attention_shared(Q, ints([0, rows]), rows))   # the same bits again
 
 
 def test_shared_history_alone_is_qwm_attention():
