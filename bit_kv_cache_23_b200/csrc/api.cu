@@ -217,11 +217,10 @@ qwm_status qwm_device_status(int32_t* flags) {
   int v = read_and_clear_tc_timeout();
   int v2 = read_and_clear_append_timeout();
   int v3 = read_and_clear_flash_timeout();
-  int v4 = read_and_clear_rows_timeout();
   int f1 = read_and_clear_append_fault();
   int f2 = read_and_clear_flash_fault();
-  if (v < 0 || v2 < 0 || v3 < 0 || v4 < 0 || f1 < 0 || f2 < 0) return QWM_ERR_CUDA;
-  v = v | v2 | v3 | v4;
+  if (v < 0 || v2 < 0 || v3 < 0 || f1 < 0 || f2 < 0) return QWM_ERR_CUDA;
+  v = v | v2 | v3;
   *flags = v | ((f1 | f2) << 1);
   return v ? QWM_ERR_TIMEOUT : *flags ? QWM_ERR_INVALID_ARG : QWM_OK;
 }

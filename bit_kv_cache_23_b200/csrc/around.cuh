@@ -10,7 +10,6 @@ namespace qwm {
 int read_and_clear_append_fault();
 int read_and_clear_flash_fault();
 int read_and_clear_flash_timeout();
-int read_and_clear_rows_timeout();
 
 // Attention of few rows per head over the packed tokens (attention_rows.cu): one
 // fp32 partial per row, query head and slot; empty slots get a log-sum-exp of -inf.
@@ -18,6 +17,10 @@ struct RowsPlan {
   int grid, slots;
 };
 bool rows_supported(const Dims& D, int64_t rows);  // rows: query rows per key head
+// K' and V' of `heads` heads from h0 on, [head][T][d] bf16, for ranks up to 8.
+bool unpack_fast_supported(const Dims& D);
+cudaError_t launch_unpack_fast(const Dims& D, const CacheView& v, int64_t T, int h0, int heads,
+                               uint16_t* K, uint16_t* V, int sms, cudaStream_t s);
 RowsPlan rows_plan(const Dims& D, int64_t T, int sms, int most);  // at most `most` >= 3 slots
 cudaError_t launch_rows(const Dims& D, const CacheView& v, int64_t T, const uint16_t* Q, int64_t ldq,
                         int64_t nq, int Hq, float scale_log2, const RowsPlan& plan, float* ws_o,

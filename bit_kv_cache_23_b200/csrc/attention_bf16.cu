@@ -897,6 +897,7 @@ cudaError_t launch_merge(int D, const FlashArgs& a, int np, const int32_t* cu, i
 
 cudaError_t launch_unpack(const Dims& D, const CacheView& v, int64_t T, int h0, int heads,
                           uint16_t* K, uint16_t* V, cudaStream_t s) {
+  if (unpack_fast_supported(D)) return launch_unpack_fast(D, v, T, h0, heads, K, V, device_sms(), s);
   const dim3 grid((unsigned)((T + UT - 1) / UT), (unsigned)heads);
   if (D.d == 128) unpack_kernel<128><<<grid, 256, 0, s>>>(D, v, T, h0, K, V);
   else unpack_kernel<64><<<grid, 256, 0, s>>>(D, v, T, h0, K, V);

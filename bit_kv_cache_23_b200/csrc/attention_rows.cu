@@ -7,22 +7,22 @@
 // instructions to rebuild.  So the layout serves the decoder.  A warp takes 16
 // keys at a time; in the products' operand layout (lane = 4 g + c) the channels
 // are permuted such that a lane owns a quarter head of keys g and g + 8 of K'
-// (whole INT2 groups: two code words, one or two parameter words per key) and
-// D / 8 channels of keys 2c, 2c+1, 2c+8, 2c+9 of V', and each decoded pair goes
-// from the conversion into its product without passing through shared memory.
+// (whole code words) and D / 8 channels of keys 2c, 2c+1, 2c+8, 2c+9 of V', and
+// each decoded pair goes from the conversion into its product without passing
+// through shared memory.
 //
 //   K'  = bf16((c + mn + code sc) + cs sum_i U_i c8_i).  The compensation is a
-//         product too: c8 is exact in bf16, and U, split into three bf16 parts
-//         (24 bits), stays in registers as the B operand while its version lasts.
+//         product too: c8 is exact in bf16, and U is split into three bf16 parts
+//         (24 bits), kept in shared memory in operand order.
 //   S   = Q K'^T, P = 2^(scale log2e S - m), O += P V': m16n8k16, rows = queries.
 //
-// Each CTA takes an equal run of (head, 128-key chunk) positions, whatever the
-// number of heads, and gives one partial per head it touches; its eight warps
-// share a chunk (16 keys each), keep a running maximum, sum and O of their own
-// and meet at the end of a head.  The head's centroid tables lie in shared
-// memory when both fit (C D <= 32768), tokens of another table version, and
-// larger tables, are read through the cache.  The packed fields of the chunks
-// ahead are copied into a ring; the warp that is last to leave a stage refills it.
+// Each CTA takes an equal run of (head, 16-key tile) positions, whatever the
+// number of heads, and gives one partial per head it touches.  Its warps take
+// tiles in turn, each with a running maximum, sum and O and a small ring of
+// asynchronous copies of its own, and meet at the end of a head and where the
+// basis or table version changes: U and, when both fit (C D <= 32768), the
+// centroid tables of the version at hand lie in shared memory (larger tables are
+// read through the cache).
 #include <math.h>
 
 #include "around.cuh"
@@ -33,12 +33,12 @@ namespace qwm {
 namespace {
 using namespace tc;
 
-__device__ int g_rows_timeout;
-
-constexpr int CH = 128;       // keys per chunk
-constexpr int NW = 8;         // decoding warps
-constexpr int NTHREADS = 32 * NW;  // 255 registers per thread
-constexpr int NSTAGE = 3;
+constexpr int NW_ROWS = 12;     // warps of the attention (168 registers per thread; with 16 it
+                               // spills, 310 us, with 8 too few latencies overlap, 260 us
+                               // against 254 us at the size above)
+constexpr int NW_UNPACK = 16;  // and of the unpacking
+constexpr int KT = 16;        // keys per tile
+constexpr int NSTAGE = 2;     // tiles in a warp's ring
 constexpr int MAX_R = 8;      // PSAC rank served here
 constexpr float TAU = 8.0f;   // a row's reference moves when its maximum grew by more (log2)
 
@@ -53,35 +53,44 @@ struct RowsArgs {
   float *ws_o, *ws_l;  // [slot][token][Hq][D], [slot][token][Hq]
   int64_t nq;
   int nslot;           // slots of a head
-  int64_t nc, total;   // chunks per head, in all
-  int tables;          // both centroid tables in shared memory
+  int64_t nt, total;   // tiles per head, in all
 };
 
-// Stage: the packed fields of 128 keys.
 template <int D>
-struct RLay {
-  static constexpr uint32_t KC = 0, VC = KC + CH * D / 4, KP = VC + CH * D / 4,
-                            VP = KP + CH * (D / 16) * 4, CO = VP + CH * (D / 16) * 4,
-                            CS = CO + CH * MAX_R, KI = CS + CH * 2, VI = KI + CH * 2,
-                            TV = VI + CH * 2, CV = TV + CH * 2, STAGE = CV + CH * 2;
-  static constexpr uint32_t OFF_BAR = 0;                       // copies landed; warps done
-  static constexpr uint32_t OFF_ML = 2 * NSTAGE * 8 + 16;      // [warp][16] m, l
-  static constexpr uint32_t OFF_Q = (OFF_ML + 2 * NW * 16 * 4 + 127) / 128 * 128;  // [16][D] bf16
-  static constexpr uint32_t OFF_ST = OFF_Q + 16 * D * 2;
-  static constexpr uint32_t OFF_TAB = OFF_ST + NSTAGE * STAGE;  // tables, or the warps' O
-  static constexpr uint32_t MERGE = NW * 16 * D * 4;
+struct Stage {  // its fixed fields: code words and K's parameters
+  static constexpr uint32_t KC = 0, VC = KC + KT * D / 4, KP = VC + KT * D / 4;
 };
-static_assert(RLay<128>::OFF_TAB + 2 * 32768 * 2 <= 227 * 1024, "shared memory");
+// Shared memory.  A stage holds the packed fields of a tile; where each begins
+// depends on the rank, the group size and the centroid numbers' width.
+template <int D, int NW>
+struct RLay {
+  static constexpr uint32_t OFF_ML = 0;                        // [warp][16] m, l
+  static constexpr uint32_t OFF_Q = OFF_ML + 2 * NW * 16 * 4;  // [16][D] bf16
+  static constexpr uint32_t OFF_U = OFF_Q + 16 * D * 2;        // [D / 8][32] {high, middle, low, -}
+  static constexpr uint32_t OFF_ST = OFF_U + D / 8 * 32 * 16;  // [warp][NSTAGE] stages
+  static constexpr uint32_t MERGE = NW * 16 * D * 4;           // the warps' O
+};
+struct Fields {  // offsets in a stage
+  uint32_t vp, co, cs, ki, vi, stage, tab;  // and of the tables (or the warps' O) in shared memory
+};
+template <int D, int NW>
+__host__ __device__ __forceinline__ Fields fields_of(const Dims& Dm) {
+  using L = RLay<D, NW>;
+  Fields f;
+  f.vp = Stage<D>::KP + KT * Dm.ng * 4;
+  f.co = f.vp + KT * Dm.ng * 4;
+  f.cs = f.co + KT * Dm.r;
+  f.ki = f.cs + KT * 2;
+  f.vi = f.ki + KT * Dm.idx_bytes;
+  f.stage = f.vi + KT * Dm.idx_bytes;
+  f.tab = (L::OFF_ST + NW * NSTAGE * f.stage + 127) / 128 * 128;
+  return f;
+}
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
   return r;
-}
-__device__ __forceinline__ uint32_t pack_bf16(uint64_t v) {
-  float a, b;
-  f2unpack(v, a, b);
-  return pack_bf16(a, b);
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -89,7 +98,14 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// D (16 x 8, fp32) += A (16 x 16) B (16 x 8), bf16; and with 8 in place of 16.
+// D (16 x 8, fp32) += A (16 x 16) B (16 x 8), bf16; with 8 in place of 16; and D = A B.
+__device__ __forceinline__ void mma16_new(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                       uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
@@ -104,107 +120,189 @@ __device__ __forceinline__ void mma8(float (&d)[4], uint32_t a0, uint32_t a1, ui
       : "r"(a0), "r"(a1), "r"(b0));
 }
 
-__device__ __forceinline__ void timeout_flag() { atomicExch(&g_rows_timeout, 1); }
-
 // The CTA whose run holds position x.
 __device__ __forceinline__ int64_t cta_of(const RowsArgs& A, int64_t x) {
   return ((x + 1) * gridDim.x - 1) / A.total;
 }
 
-// Copy the fields of the chunk at position x into stage s (one thread).
+// What a lane copies of every tile of a head, 16 bytes a piece: code words of K
+// and V, parameters (K in the lower half warp, V in the upper; at 8 groups a
+// second piece each), and one piece of the short fields.  (Capacities are
+// multiples of 128 keys, so whole tiles lie in the buffers.)
 template <int D>
-__device__ __forceinline__ void fill_stage(const RowsArgs& A, uint8_t* smem, uint64_t* full,
-                                           volatile int* issued, int64_t x, int s) {
-  using L = RLay<D>;
-  const Dims& Dm = A.Dm;
-  const int ng = Dm.ng, r = Dm.r, ib = Dm.idx_bytes;
-  const int h = (int)(x / A.nc);
-  const int64_t t0 = (x - (int64_t)h * A.nc) * CH;
-  const PackedHead p = packed_head(A.v, Dm, h);
-  const uint32_t st = smem_u32(smem) + L::OFF_ST + s * L::STAGE;
-  uint64_t* bar = &full[s];
-  issued[s] = issued[s] + 1;
-  mbar_arrive_expect_tx(bar, 2 * (CH * D / 4) + 2 * CH * ng * 4 + (r > 0 ? CH * r + CH * 2 : 0) +
-                                 2 * CH * 2 + 2 * CH * ib);
-  bulk_g2s(st + L::KC, p.k_codes + t0 * (D / 4), CH * D / 4, bar);
-  bulk_g2s(st + L::VC, p.v_codes + t0 * (D / 4), CH * D / 4, bar);
-  bulk_g2s(st + L::KP, p.k_params + t0 * ng * 2, CH * ng * 4, bar);
-  bulk_g2s(st + L::VP, p.v_params + t0 * ng * 2, CH * ng * 4, bar);
-  if (r > 0) {
-    bulk_g2s(st + L::CO, p.k_coef + t0 * r, CH * r, bar);
-    bulk_g2s(st + L::CS, p.k_cscale + t0, CH * 2, bar);
-  }
-  bulk_g2s(st + L::TV, A.v.tokver + t0, CH * 2, bar);
-  bulk_g2s(st + L::CV, A.v.centver + t0, CH * 2, bar);
-  bulk_g2s(st + L::KI, (const uint8_t*)p.k_idx + t0 * ib, CH * ib, bar);
-  bulk_g2s(st + L::VI, (const uint8_t*)p.v_idx + t0 * ib, CH * ib, bar);
+struct Source {
+  const uint8_t *codes, *params, *rest;  // of tile 0; codes of K, V at + vcodes
+  int64_t vcodes;
+  uint32_t dst_params, dst_rest, step_rest;
+};
+
+template <int D>
+__device__ __forceinline__ Source<D> source_of(const Dims& Dm, const Fields& F, const PackedHead& p) {
+  using L = Stage<D>;
+  const int lane = threadIdx.x & 31, ng = Dm.ng, r = Dm.r, ib = Dm.idx_bytes;
+  Source<D> S;
+  S.codes = p.k_codes + 16 * lane;
+  S.vcodes = p.v_codes - p.k_codes;
+  // a tile has 4 ng pieces of parameters for K and as many for V
+  const int half = lane >> 4, i = lane & 15;
+  S.params = (const uint8_t*)(half ? p.v_params : p.k_params) + 16 * i;
+  S.dst_params = (half ? F.vp : L::KP) + 16 * i;
+  // the short ones side by side: at most 8 + 2 + 2 + 2 lanes
+  const int a = r, b = a + 2, c = b + ib, d = c + ib;  // ends, in pieces
+  S.rest = nullptr;
+  S.dst_rest = S.step_rest = 0;
+  auto piece = [&](const void* src, uint32_t dst, int first, int bytes) {
+    S.rest = (const uint8_t*)src + 16 * (lane - first);
+    S.dst_rest = dst + 16 * (lane - first);
+    S.step_rest = KT * bytes;
+  };
+  if (lane < a) piece(p.k_coef, F.co, 0, r);
+  else if (lane < b) piece(p.k_cscale, F.cs, a, 2);
+  else if (lane < c) piece(p.k_idx, F.ki, b, ib);
+  else if (lane < d) piece(p.v_idx, F.vi, c, ib);
+  (void)ng;
+  return S;
 }
 
-// What a decoding warp keeps while it works on one head.
+// Start copying tile t into the stage at `st`.
+template <int D>
+__device__ __forceinline__ void fill_stage(const Source<D>& S, int ng, uint32_t st, int64_t t) {
+  using L = Stage<D>;
+  const int lane = threadIdx.x & 31;
+  if (16 * lane < KT * D / 4) {
+    const uint8_t* src = S.codes + t * (KT * D / 4);
+    cp_async16_cg(st + L::KC + 16 * lane, src);
+    cp_async16_cg(st + L::VC + 16 * lane, src + S.vcodes);
+  }
+  const uint8_t* par = S.params + t * (KT * 4 * ng);
+  if ((lane & 15) < 4 * ng) cp_async16_cg(st + S.dst_params, par);
+  if (ng > 4) cp_async16_cg(st + S.dst_params + 256, par + 256);
+  if (S.rest) cp_async16_cg(st + S.dst_rest, S.rest + t * S.step_rest);
+}
+
+// The first position in (at, end) whose versions are not those of `at`, or end
+// (versions never fall along the cache); 32 probes at a time, one warp.
+__device__ __forceinline__ int64_t versions_end(const CacheView& v, int64_t at, int64_t end) {
+  const int lane = threadIdx.x & 31;
+  const int tv = v.tokver[at], cv = v.centver[at];
+  int64_t lo = at, hi = end;  // position lo has them; hi is end or has not
+  while (hi - lo > 1) {
+    const int64_t step = (hi - lo + 31) / 32, x = lo + (lane + 1) * step;
+    const bool same = x < hi && v.tokver[x] == tv && v.centver[x] == cv;
+    const int n = __popc(__ballot_sync(0xffffffffu, same));  // the first n probes
+    const int64_t up = lo + (n + 1) * step;
+    lo += n * step;
+    hi = up < hi ? up : hi;
+  }
+  return hi;
+}
+
+// What a warp keeps while it works on one head.
 template <int D>
 struct State {
   float o[D / 8][4];      // O: n-tile j holds channels g' D/8 + j; rows g, g + 8
   float m0, m1, l0, l1;   // reference and (this lane's part of the) sum of rows g, g + 8
-  uint32_t u[D / 8][3];   // U of version `uver`: high, middle and low bf16 parts
-  int uver;
 };
 
-// U of head h, version ver, as B operands: n-tile j's column n is channel
-// (n / 2) D/4 + 2j + n % 2, so that a lane's accumulators are its own channels.
+// A lane's K channels are c D/4 ..; of the two code words that they fill at D =
+// 128, lanes with c >= 2 take the second first, so that the four lanes of a key
+// read centroid pieces of different banks.  Channel of position e (0 .. D/4 - 1).
 template <int D>
-__device__ __forceinline__ void load_basis(const RowsArgs& A, int h, int ver, State<D>& st) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const int r = A.Dm.r;
-  const float* U = basis_of(A.v, A.Dm, ver, h);
-#pragma unroll
-  for (int j = 0; j < D / 8; ++j) {
-    const int ch = (g >> 1) * (D / 4) + 2 * j + (g & 1);
-    float x[2];
+__device__ __forceinline__ int k_channel(int c, int e) {
+  return c * (D / 4) + (D == 128 ? e ^ (8 * (c & 2)) : e);
+}
+
+// U of head h, version ver, as B operands: n-tile j's column n is position
+// 2j + n % 2 of the lanes with c = n / 2.
+template <int D>
+__device__ __forceinline__ void stage_basis(const Dims& Dm, const CacheView& v, uint8_t* dst, int h,
+                                            int ver) {
+  const int r = Dm.r;
+  const float* U = basis_of(v, Dm, ver, h);
+  for (int e = threadIdx.x; e < D / 8 * 32; e += blockDim.x) {
+    const int j = e >> 5, g = (e & 31) >> 2, c = e & 3;
+    const float* u = U + (size_t)k_channel<D>(g >> 1, 2 * j + (g & 1)) * r + 2 * c;
+    float x = 2 * c < r ? __ldg(u) : 0.0f, y = 2 * c + 1 < r ? __ldg(u + 1) : 0.0f;
     uint32_t part[3];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) x[e] = 2 * c + e < r ? __ldg(U + (size_t)ch * r + 2 * c + e) : 0.0f;
-#pragma unroll
     for (int k = 0; k < 3; ++k) {
-      part[k] = pack_bf16(x[0], x[1]);
-      x[0] -= __uint_as_float(part[k] << 16);  // exact: the rounding's remainder
-      x[1] -= __uint_as_float(part[k] & 0xffff0000u);
+      part[k] = pack_bf16(x, y);
+      x -= __uint_as_float(part[k] << 16);  // exact: the rounding's remainder
+      y -= __uint_as_float(part[k] & 0xffff0000u);
     }
-#pragma unroll
-    for (int k = 0; k < 3; ++k) st.u[j][k] = part[k];
+    reinterpret_cast<uint4*>(dst)[e] = make_uint4(part[0], part[1], part[2], 0);
   }
-  st.uver = ver;
 }
 
 __device__ __forceinline__ uint32_t i8_pair_bf16(uint32_t two) {
   return pack_bf16(i8_to_f32((int8_t)(two & 0xff)), i8_to_f32((int8_t)(two >> 8)));
 }
 
-// One warp: the 16 keys at k0 of the staged chunk (nval of the chunk's keys are
-// cached; the fields of the others are not used).
+// S_i and M_i of one parameter word (positions 0 .. 3 of a code byte).  Scalar
+// fp32 here: the two-wide forms need their operands in register pairs, and the
+// moves that gather them cost more than they save (1860 against COUNT
+// instructions per 16 keys).
+struct Decode {
+  float s[4], m[4];
+};
+__device__ __forceinline__ Decode decode_of(uint32_t par) {
+  const float mn = h2f((uint16_t)(par & 0xffffu)), sc = h2f((uint16_t)(par >> 16));
+  Decode d;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    d.s[i] = sc * (float)(256 >> (2 * i));
+    d.m[i] = mn - d.s[i];
+  }
+  return d;
+}
+
+// (x & mask of position P) | 1.0f in one instruction; `one` holds 0x3F800000.
+template <int P>
+__device__ __forceinline__ float magic(uint32_t x, uint32_t one) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(x), "n"(3u << (15 + 2 * P)), "r"(one));
+  return __uint_as_float(d);
+}
+__device__ __forceinline__ float magic(uint32_t x, int p, uint32_t one) {
+  return p == 0 ? magic<0>(x, one) : p == 1 ? magic<1>(x, one) : p == 2 ? magic<2>(x, one) : magic<3>(x, one);
+}
+
+// The code byte b of word w at bits 15 .. 22.
+template <int B>
+__device__ __forceinline__ uint32_t code_byte(uint32_t w) {
+  return B == 0 ? w << 15 : B == 1 ? w << 7 : B == 2 ? w >> 1 : w >> 9;
+}
+
+// Rows of the staged tables: 16-byte pieces exchanged by the row number, so that
+// the keys of a warp, whose rows are as good as random, spread over the banks.
 template <int D>
-__device__ __forceinline__ void keys16(const RowsArgs& A, const uint8_t* pk, const uint8_t* smem,
-                                       int h, int k0, int nval, int tabver, State<D>& st) {
-  using L = RLay<D>;
-  constexpr int KCH = D / 4;  // a lane's K channels
-  constexpr int VCH = D / 8;  // a lane's V channels
+__device__ __forceinline__ uint32_t piece_at(int row, int piece) {
+  return (uint32_t)row * (D * 2) + ((uint32_t)(piece ^ (row & 7)) << 4);
+}
+
+// One warp: keys [lo, hi) of the staged 16, all of the staged basis and table
+// version (the fields of other keys are not used).
+template <int D, bool TAB>
+__device__ __forceinline__ void keys16(const RowsArgs& A, const Fields& F, const uint8_t* pk,
+                                       const uint8_t* smem,
+                                       const uint16_t* gk, const uint16_t* gv, int lo, int hi,
+                                       State<D>& st) {
+  using L = RLay<D, NW_ROWS>;
+  using St = Stage<D>;
+  constexpr int KCH = D / 4;       // a lane's K channels
+  constexpr int KW = KCH / 16;     // their code words
+  constexpr int VCH = D / 8;       // a lane's V channels
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const Dims& Dm = A.Dm;
   const int G = Dm.G, ng = Dm.ng, r = Dm.r, ib = Dm.idx_bytes;
-  const uint16_t* tv = reinterpret_cast<const uint16_t*>(pk + L::TV);
-  const uint16_t* cv = reinterpret_cast<const uint16_t*>(pk + L::CV);
-  const uint8_t* tab = smem + L::OFF_TAB;
-  const size_t hoff = (size_t)h * Dm.C * D;
-  const size_t vstride = cent_slot_elems(Dm);
-  // row of a centroid table: staged, or in memory
-  auto centroid = [&](const uint16_t* table, uint32_t staged, uint32_t fields, int k, bool live) {
-    const int idx = !live ? 0
-                    : ib == 1 ? (int)pk[fields + k]
-                              : (int)reinterpret_cast<const uint16_t*>(pk + fields)[k];
-    const int ver = live ? cv[k] : tabver;
-    return ver == tabver && A.tables
-               ? reinterpret_cast<const uint4*>(tab + staged + (uint32_t)idx * (D * 2))
-               : reinterpret_cast<const uint4*>(table + ver * vstride + hoff + (size_t)idx * D);
+  const uint8_t* tk = smem + F.tab;
+  const uint8_t* tvv = tk + Dm.C * D * 2;
+  auto number = [&](uint32_t fields, int k, bool live) {  // centroid (0 of a key not worked on)
+    return !live ? 0 : ib == 1 ? (int)pk[fields + k] : (int)reinterpret_cast<const uint16_t*>(pk + fields)[k];
   };
+
+  uint32_t one;
+  asm volatile("mov.b32 %0, 0x3F800000;" : "=r"(one));
 
   // ---- K' of keys g and g + 8, and S
   float s[2][4];
@@ -213,81 +311,86 @@ __device__ __forceinline__ void keys16(const RowsArgs& A, const uint8_t* pk, con
 #pragma unroll
     for (int e = 0; e < 4; ++e) s[x][e] = 0.0f;
   {
-    const uint4* cp[2];
-    uint32_t code[2][KCH / 16];
-    GroupConst gc[2][KCH / 16];
-    uint64_t cs2[2];
-    uint32_t a[2] = {0, 0};
-    bool same = true;
+    int row[2];
+    float cs[2];
+    uint32_t a[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const int k = k0 + g + 8 * x;
-      const bool live = k < nval;
-      cp[x] = centroid(A.v.cent_k, 0, L::KI, k, live) + c * (KCH / 8);
-#pragma unroll
-      for (int w = 0; w < KCH / 16; ++w) {
-        code[x][w] = reinterpret_cast<const uint32_t*>(pk + L::KC)[k * (D / 16) + c * (KCH / 16) + w];
-        gc[x][w] = group_const(
-            reinterpret_cast<const uint32_t*>(pk + L::KP)[k * ng + (c * KCH + 16 * w) / G]);
-      }
-      cs2[x] = 0;
+      const int k = g + 8 * x;
+      const bool live = k >= lo && k < hi;
+      row[x] = number(F.ki, k, live);
+      cs[x] = 0.0f;
+      a[x] = 0;
       if (r > 0) {
-        const float cs = live ? half_bits_to_f32(reinterpret_cast<const uint16_t*>(pk + L::CS)[k]) : 0.0f;
-        cs2[x] = f2pack(cs, cs);
+        cs[x] = live ? h2f(reinterpret_cast<const uint16_t*>(pk + F.cs)[k]) : 0.0f;
         uint32_t two = 0;
-        if (2 * c < r) two = pk[L::CO + k * r + 2 * c];
-        if (2 * c + 1 < r) two |= (uint32_t)pk[L::CO + k * r + 2 * c + 1] << 8;
+        if (r == MAX_R) {
+          two = reinterpret_cast<const uint16_t*>(pk + F.co)[k * (MAX_R / 2) + c];
+        } else {
+          if (2 * c < r) two = pk[F.co + k * r + 2 * c];
+          if (2 * c + 1 < r) two |= (uint32_t)pk[F.co + k * r + 2 * c + 1] << 8;
+        }
         a[x] = i8_pair_bf16(two);
-        same &= !live || tv[k] == tv[k0];
       }
     }
-    same = __all_sync(0xffffffffu, same);
-    if (r > 0 && same && st.uver != tv[k0]) load_basis<D>(A, h, tv[k0], st);
-    const uint4* qs = reinterpret_cast<const uint4*>(smem + L::OFF_Q);
+    const uint4* us = reinterpret_cast<const uint4*>(smem + L::OFF_U) + lane;
+    const uint4* qs = reinterpret_cast<const uint4*>(smem + L::OFF_Q) + lane;
 #pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {  // a lane's channels 4 ks .. 4 ks + 3
-      uint32_t b[2][2];
+    for (int w = 0; w < KW; ++w) {
+      const int wa = D == 128 ? w ^ (c >> 1) : w;  // the lane's code word
+      uint32_t code[2];
+      Decode gc[2];
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int j = 2 * ks + y;  // channels 2j, 2j + 1
-        float corr[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (r > 0) {
-          if (same) {
-            mma16(corr, a[0], a[1], a[0], a[1], st.u[j][0], st.u[j][1]);
-            mma8(corr, a[0], a[1], st.u[j][2]);
-          } else {  // keys of several basis versions: once per refresh
+      for (int x = 0; x < 2; ++x) {
+        const int k = g + 8 * x;
+        code[x] = reinterpret_cast<const uint32_t*>(pk + St::KC)[k * (D / 16) + c * KW + wa];
+        gc[x] = decode_of(reinterpret_cast<const uint32_t*>(pk + St::KP)[k * ng + (c * KCH + 16 * wa) / G]);
+      }
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const int k = k0 + g + 8 * x;
-              if (k >= nval) continue;
-              const float* U = basis_of(A.v, Dm, tv[k], h) + (size_t)(c * KCH + 2 * j) * r;
-              for (int q = 0; q < r; ++q) {
-                const float f = (float)(int8_t)pk[L::CO + k * r + q];
-                corr[2 * x] = fmaf(__ldg(U + q), f, corr[2 * x]);
-                corr[2 * x + 1] = fmaf(__ldg(U + r + q), f, corr[2 * x + 1]);
-              }
-            }
-          }
-        }
+      for (int hf = 0; hf < 2; ++hf) {  // 8 channels: a piece of the centroid
+        uint4 cw[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          // code pair j of word j / 8: byte (j % 8) / 2, positions 2 (j % 2), + 1
-          const uint32_t w = code[x][j / 8];
-          const int byte = (j % 8) / 2, pos = 2 * (j % 2);
-          const uint32_t at = byte == 0 ? w << 15 : byte == 1 ? w << 7 : byte == 2 ? w >> 1 : w >> 9;
-          const GroupConst& q = gc[x][j / 8];
-          const uint64_t mm = f2pack(magic_code(at, pos), magic_code(at, pos + 1));
-          const uint32_t cw = reinterpret_cast<const uint32_t*>(cp[x])[j];
-          uint64_t v = ffma2(mm, pos == 0 ? q.s01 : q.s23, pos == 0 ? q.m01 : q.m23);
-          v = fadd2(f2pack(__uint_as_float(cw << 16), __uint_as_float(cw & 0xffff0000u)), v);
-          if (r > 0) v = ffma2(f2pack(corr[2 * x], corr[2 * x + 1]), cs2[x], v);
-          b[x][y] = pack_bf16(v);
+          const int piece = c * (KCH / 8) + 2 * wa + hf;
+          cw[x] = TAB ? *reinterpret_cast<const uint4*>(tk + piece_at<D>(row[x], piece))
+                      : __ldg(reinterpret_cast<const uint4*>(gk + (size_t)row[x] * D) + piece);
+        }
+#pragma unroll
+        for (int q4 = 0; q4 < 2; ++q4) {  // 4 channels: a step of 16 over the warp
+          const int ks = 4 * w + 2 * hf + q4;
+          uint32_t b[2][2], bytes[2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            bytes[x] = hf == 0 ? (q4 == 0 ? code_byte<0>(code[x]) : code_byte<1>(code[x]))
+                               : (q4 == 0 ? code_byte<2>(code[x]) : code_byte<3>(code[x]));
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int j = 2 * ks + y;
+            float corr[4];
+            if (r > 0) {
+              const uint4 u = us[j * 32];
+              mma16_new(corr, a[0], a[1], a[0], a[1], u.x, u.y);
+              mma8(corr, a[0], a[1], u.z);
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t at = bytes[x];
+              const uint32_t cb = reinterpret_cast<const uint32_t(&)[4]>(cw[x])[2 * q4 + y];
+              float v0 = __uint_as_float(cb << 16) + fmaf(magic(at, 2 * y, one), gc[x].s[2 * y], gc[x].m[2 * y]);
+              float v1 = __uint_as_float(cb & 0xffff0000u) +
+                         fmaf(magic(at, 2 * y + 1, one), gc[x].s[2 * y + 1], gc[x].m[2 * y + 1]);
+              if (r > 0) {
+                v0 = fmaf(corr[2 * x], cs[x], v0);
+                v1 = fmaf(corr[2 * x + 1], cs[x], v1);
+              }
+              b[x][y] = pack_bf16(v0, v1);
+            }
+          }
+          const uint4 q = qs[ks * 32];  // rows g and g + 8, the same four channels
+          mma16(s[0], q.x, q.y, q.z, q.w, b[0][0], b[0][1]);
+          mma16(s[1], q.x, q.y, q.z, q.w, b[1][0], b[1][1]);
         }
       }
-      // Q rows g and g + 8, the same four channels
-      const uint4 q = qs[ks * 32 + lane];
-      mma16(s[0], q.x, q.z, q.y, q.w, b[0][0], b[0][1]);
-      mma16(s[1], q.x, q.z, q.y, q.w, b[1][0], b[1][1]);
     }
   }
 
@@ -298,7 +401,8 @@ __device__ __forceinline__ void keys16(const RowsArgs& A, const uint8_t* pk, con
     for (int x = 0; x < 2; ++x)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const bool live = k0 + 8 * x + 2 * c + e < nval;
+        const int k = 8 * x + 2 * c + e;
+        const bool live = k >= lo && k < hi;
         s[x][e] = live ? s[x][e] * A.scale_log2 : -INFINITY;
         s[x][2 + e] = live ? s[x][2 + e] * A.scale_log2 : -INFINITY;
       }
@@ -310,7 +414,7 @@ __device__ __forceinline__ void keys16(const RowsArgs& A, const uint8_t* pk, con
         t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, o));
         t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, o));
       }
-      // (some key of the 16 is cached, so the new references are finite)
+      // (some key of the 16 is worked on, so the new references are finite)
       const float n0 = fmaxf(t0, st.m0), n1 = fmaxf(t1, st.m1);
       const float f0 = ex2(st.m0 - n0), f1 = ex2(st.m1 - n1);
       st.m0 = n0;
@@ -341,94 +445,161 @@ __device__ __forceinline__ void keys16(const RowsArgs& A, const uint8_t* pk, con
     p[3] = pack_bf16(w[1][2], w[1][3]);
   }
 
-  // ---- V' of keys 2c, 2c + 1 (pair 0) and 2c + 8, 2c + 9 (pair 1), and O
-  {
-    const uint4* cp[4];
-    uint32_t code[4];
-    uint64_t S[2][4], M[2][4];  // [pair][position in the code byte]
+  // ---- V' of keys 2c, 2c + 1, then of 2c + 8, 2c + 9, and O
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      GroupConst q[2];
+  for (int x = 0; x < 2; ++x) {
+    int row[2];
+    uint32_t code[2];
+    float mn[2], sc[2];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int k = k0 + 2 * c + 8 * x + e;
-        const bool live = k < nval;
-        cp[2 * x + e] = centroid(A.v.cent_v, Dm.C * D * 2, L::VI, k, live) + g * (VCH / 8);
-        const uint8_t* cd = pk + L::VC + k * (D / 4) + g * (VCH / 4);
-        code[2 * x + e] = VCH == 16 ? *reinterpret_cast<const uint32_t*>(cd)
-                                    : *reinterpret_cast<const uint16_t*>(cd);
-        // a key that is not cached: finite (its weight is 0)
-        q[e] = group_const(live ? reinterpret_cast<const uint32_t*>(pk + L::VP)[k * ng + g * VCH / G] : 0u);
-      }
+    for (int e = 0; e < 2; ++e) {
+      const int k = 2 * c + 8 * x + e;
+      const bool live = k >= lo && k < hi;
+      row[e] = number(F.vi, k, live);
+      const uint8_t* cd = pk + St::VC + k * (D / 4) + g * (VCH / 4);
+      code[e] = VCH == 16 ? *reinterpret_cast<const uint32_t*>(cd) : *reinterpret_cast<const uint16_t*>(cd);
+      // a key that is not worked on: finite (its weight is 0)
+      const uint32_t par = live ? reinterpret_cast<const uint32_t*>(pk + F.vp)[k * ng + g * VCH / G] : 0u;
+      mn[e] = h2f((uint16_t)(par & 0xffffu));
+      sc[e] = h2f((uint16_t)(par >> 16));
+    }
+    uint64_t S[4], M[4];  // of both keys, for the position in the code byte
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float a0, a1, b0, b1;
-        f2unpack(e ? q[0].s23 : q[0].s01, a0, a1);
-        f2unpack(e ? q[1].s23 : q[1].s01, b0, b1);
-        S[x][2 * e] = f2pack(a0, b0);
-        S[x][2 * e + 1] = f2pack(a1, b1);
-        f2unpack(e ? q[0].m23 : q[0].m01, a0, a1);
-        f2unpack(e ? q[1].m23 : q[1].m01, b0, b1);
-        M[x][2 * e] = f2pack(a0, b0);
-        M[x][2 * e + 1] = f2pack(a1, b1);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const float f = (float)(256 >> (2 * i));
+      S[i] = fmul2(f2pack(sc[0], sc[1]), f2pack(f, f));
+      M[i] = fsub2(f2pack(mn[0], mn[1]), S[i]);
     }
 #pragma unroll
     for (int j8 = 0; j8 < VCH / 8; ++j8) {
-      uint4 cw[4];
+      uint4 cw[2];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) cw[k] = cp[k][j8];
+      for (int e = 0; e < 2; ++e) {
+        const int piece = g * (VCH / 8) + j8;
+        cw[e] = TAB ? *reinterpret_cast<const uint4*>(tvv + piece_at<D>(row[e], piece))
+                    : __ldg(reinterpret_cast<const uint4*>(gv + (size_t)row[e] * D) + piece);
+      }
+      uint32_t bytes[2];
 #pragma unroll
       for (int jj = 0; jj < 8; ++jj) {
-        const int j = 8 * j8 + jj, byte = j / 4, pos = j % 4;
-        uint32_t b[2];
+        const int j = 8 * j8 + jj;
+        if (jj % 4 == 0) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float mm[2], cc[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t w = code[2 * x + e];
-            const uint32_t at = byte == 0 ? w << 15 : byte == 1 ? w << 7 : byte == 2 ? w >> 1 : w >> 9;
-            mm[e] = magic_code(at, pos);
-            const uint32_t q = reinterpret_cast<const uint32_t(&)[4]>(cw[2 * x + e])[jj / 2];
-            cc[e] = __uint_as_float(jj & 1 ? q & 0xffff0000u : q << 16);
-          }
-          b[x] = pack_bf16(fadd2(f2pack(cc[0], cc[1]), ffma2(f2pack(mm[0], mm[1]), S[x][pos], M[x][pos])));
+          for (int e = 0; e < 2; ++e)
+            bytes[e] = j / 4 == 0   ? code_byte<0>(code[e])
+                       : j / 4 == 1 ? code_byte<1>(code[e])
+                       : j / 4 == 2 ? code_byte<2>(code[e])
+                                    : code_byte<3>(code[e]);
         }
-        mma16(st.o[j], p[0], p[1], p[2], p[3], b[0], b[1]);
+        float mm[2], cc[2], v0, v1;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          mm[e] = magic(bytes[e], j % 4, one);
+          const uint32_t q = reinterpret_cast<const uint32_t(&)[4]>(cw[e])[jj / 2];
+          cc[e] = __uint_as_float(jj & 1 ? q & 0xffff0000u : q << 16);
+        }
+        f2unpack(fadd2(f2pack(cc[0], cc[1]), ffma2(f2pack(mm[0], mm[1]), S[j % 4], M[j % 4])), v0, v1);
+        mma8(st.o[j], p[2 * x], p[2 * x + 1], pack_bf16(v0, v1));
       }
     }
   }
 }
 
+// The head's table rows into shared memory, loads four deep.
 template <int D>
-__global__ void __launch_bounds__(NTHREADS, 1) rows_kernel(const __grid_constant__ RowsArgs A) {
-  using L = RLay<D>;
+__device__ __forceinline__ void stage_tables(const Dims& Dm, uint8_t* d, const uint16_t* gk,
+                                             const uint16_t* gv) {
+  constexpr int P = D / 8;  // pieces per row
+  const uint32_t tb = Dm.C * D * 2;
+  const int n = Dm.C * P, nt = blockDim.x;
+  for (int e0 = threadIdx.x; e0 < n; e0 += 4 * nt) {
+    uint4 a[4], b[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int e = e0 + u * nt < n ? e0 + u * nt : e0;
+      a[u] = __ldg(reinterpret_cast<const uint4*>(gk) + e);
+      b[u] = __ldg(reinterpret_cast<const uint4*>(gv) + e);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int e = e0 + u * nt;
+      if (e >= n) break;
+      const uint32_t at = piece_at<D>(e / P, e % P);
+      *reinterpret_cast<uint4*>(d + at) = a[u];
+      *reinterpret_cast<uint4*>(d + tb + at) = b[u];
+    }
+  }
+}
+
+// All warps of a CTA: tokens [at, tend) of head h, span by span of the same
+// versions, whose basis and tables are staged; one(pk, lo, hi, t, gk, gv) for each
+// tile, warp by warp: keys [lo, hi) of tile t with its fields at pk; gk, gv: the
+// head's tables in memory.
+template <int D, int NW, bool TAB, class One>
+__device__ __forceinline__ void walk(const Dims& Dm, const CacheView& v, const Fields& F, uint8_t* smem,
+                                     int h, int64_t at, int64_t tend, One one) {
+  using L = RLay<D, NW>;
+  const int warp = threadIdx.x >> 5;
+  uint8_t* const ring = smem + L::OFF_ST + warp * NSTAGE * F.stage;
+  const uint32_t ring_at = smem_u32(ring);
+  const Source<D> src = source_of<D>(Dm, F, packed_head(v, Dm, h));
+  int tabver = -1, uver = -1;
+  const uint16_t *gk = nullptr, *gv = nullptr;
+  while (at < tend) {
+    const int uv = v.tokver[at], cvn = v.centver[at];
+    const int64_t to = versions_end(v, at, tend);
+    // a tile on the border of two spans is worked on in both
+    const int64_t first = at / KT + warp, last = (to + KT - 1) / KT;
+#pragma unroll
+    for (int i = 0; i < NSTAGE - 1; ++i) {
+      if (first + i * NW < last) fill_stage<D>(src, Dm.ng, ring_at + i * F.stage, first + i * NW);
+      cp_async_commit();
+    }
+    if (cvn != tabver || uv != uver) {
+      __syncthreads();
+      if (uv != uver && Dm.r > 0) stage_basis<D>(Dm, v, smem + L::OFF_U, h, uv);
+      if (cvn != tabver) {
+        const size_t off = (size_t)cvn * cent_slot_elems(Dm) + (size_t)h * Dm.C * D;
+        gk = v.cent_k + off;
+        gv = v.cent_v + off;
+        if (TAB) stage_tables<D>(Dm, smem + F.tab, gk, gv);
+      }
+      uver = uv;
+      tabver = cvn;
+      __syncthreads();
+    }
+    int s = 0;
+    for (int64_t t = first; t < last; t += NW) {
+      cp_async_wait<NSTAGE - 2>();
+      __syncwarp();  // the tile is there; the stage before it is free
+      const int64_t ahead = t + (NSTAGE - 1) * NW;
+      const int sa = s == 0 ? NSTAGE - 1 : s - 1;
+      if (ahead < last) fill_stage<D>(src, Dm.ng, ring_at + sa * F.stage, ahead);
+      cp_async_commit();
+      const int64_t k0 = t * KT;
+      one(ring + s * F.stage, (int)(at > k0 ? at - k0 : 0), (int)(to - k0 < KT ? to - k0 : KT), t, gk, gv);
+      s = s + 1 == NSTAGE ? 0 : s + 1;
+    }
+    cp_async_wait<0>();
+    __syncwarp();
+    at = to;
+  }
+}
+
+template <int D, bool TAB>
+__global__ void __launch_bounds__(32 * NW_ROWS, 1) rows_kernel(const __grid_constant__ RowsArgs A) {
+  constexpr int NW = NW_ROWS;
+  using L = RLay<D, NW>;
   extern __shared__ __align__(128) uint8_t smem[];
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
-  int* done = reinterpret_cast<int*>(full + NSTAGE);  // warps that have left a stage
-  volatile int* issued = done + NSTAGE;               // copies into it
+  const Dims& Dm = A.Dm;
+  const Fields F = fields_of<D, NW>(Dm);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int64_t x0 = blockIdx.x * A.total / gridDim.x, x1 = (blockIdx.x + 1) * A.total / gridDim.x;
   const int64_t r0 = (int64_t)blockIdx.y * 16;  // first row of this row tile
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < NSTAGE; ++i) {
-      mbar_init(&full[i], 1);
-      done[i] = 0;
-      issued[i] = 0;
-    }
-    fence_mbar_init();
-    fence_proxy_async_smem();
-    for (int i = 0; i < NSTAGE && x0 + i < x1; ++i) fill_stage<D>(A, smem, full, issued, x0 + i, i);
-  }
-  __syncthreads();
-  const Dims& Dm = A.Dm;
   State<D> st;
-  bool ok = true;
-  int n = 0;
   for (int64_t x = x0; x < x1;) {
-    const int h = (int)(x / A.nc);
-    const int64_t head_end = (int64_t)(h + 1) * A.nc;
+    const int h = (int)(x / A.nt);
+    const int64_t head0 = (int64_t)h * A.nt, head_end = head0 + A.nt;
     const int64_t end = head_end < x1 ? head_end : x1;
     // ---- this head's Q rows (operand order: four channels of rows g and g + 8 per lane)
     __syncthreads();  // the last head's tables, O and Q are done with
@@ -440,59 +611,30 @@ __global__ void __launch_bounds__(NTHREADS, 1) rows_kernel(const __grid_constant
         uint2 q = make_uint2(0, 0);
         if (r < A.rows) {
           const int64_t tok = r / A.g;
-          q = __ldg(reinterpret_cast<const uint2*>(
-              A.Q + tok * A.ldq + ((int64_t)h * A.g + (r - tok * A.g)) * D + cc * (D / 4) + 4 * ks));
+          q = __ldg(reinterpret_cast<const uint2*>(A.Q + tok * A.ldq +
+                                                   ((int64_t)h * A.g + (r - tok * A.g)) * D +
+                                                   k_channel<D>(cc, 4 * ks)));
         }
-        *reinterpret_cast<uint2*>(smem + L::OFF_Q + e * 16 + 8 * y) = q;
+        reinterpret_cast<uint32_t*>(smem + L::OFF_Q)[e * 4 + y] = q.x;
+        reinterpret_cast<uint32_t*>(smem + L::OFF_Q)[e * 4 + 2 + y] = q.y;
       }
     }
-    int tabver = -1;
-    st.uver = -1;
     st.m0 = st.m1 = -INFINITY;
     st.l0 = st.l1 = 0.0f;
 #pragma unroll
     for (int j = 0; j < D / 8; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) st.o[j][e] = 0.0f;
-    for (; x < end; ++x, ++n) {
-      const int64_t t0 = (x - (int64_t)h * A.nc) * CH;
-      const int nval = (int)(A.T - t0 < CH ? A.T - t0 : CH);
-      const int s = n % NSTAGE;
-      // after a timeout the warp still meets the others at the barriers
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&full[s], (n / NSTAGE) & 1));
-      const uint8_t* pk = smem + L::OFF_ST + s * L::STAGE;
-      // table version of the chunk's first key, the same for every warp
-      const int ver = ok ? reinterpret_cast<const uint16_t*>(pk + L::CV)[0] : A.v.centver[t0];
-      if (ver != tabver) {
-        __syncthreads();
-        if (A.tables) {
-          const size_t off = (size_t)ver * cent_slot_elems(Dm) + (size_t)h * Dm.C * D;
-          const uint4* sk = reinterpret_cast<const uint4*>(A.v.cent_k + off);
-          const uint4* sv = reinterpret_cast<const uint4*>(A.v.cent_v + off);
-          uint4* d = reinterpret_cast<uint4*>(smem + L::OFF_TAB);
-          const int words = Dm.C * D / 8;
-          for (int e = threadIdx.x; e < words; e += 32 * NW) {
-            d[e] = __ldg(sk + e);
-            d[words + e] = __ldg(sv + e);
-          }
-        }
-        tabver = ver;
-        __syncthreads();
-      }
-      if (ok && 16 * warp < nval) keys16<D>(A, pk, smem, h, 16 * warp, nval, tabver, st);
-      __syncwarp();
-      if (lane == 0) {
-        __threadfence_block();
-        if (atomicAdd(&done[s], 1) == NW - 1) {  // (the others' reads are before their add)
-          done[s] = 0;
-          __threadfence_block();
-          if (ok && x + NSTAGE < x1) fill_stage<D>(A, smem, full, issued, x + NSTAGE, s);
-        }
-      }
-    }
+    const int64_t at = (x - head0) * KT;
+    const int64_t tend = (end - head0) * KT < A.T ? (end - head0) * KT : A.T;
+    walk<D, NW, TAB>(Dm, A.v, F, smem, h, at, tend,
+                     [&](const uint8_t* pk, int lo, int hi, int64_t, const uint16_t* gk, const uint16_t* gv) {
+                       keys16<D, TAB>(A, F, pk, smem, gk, gv, lo, hi, st);
+                     });
+    x = end;
     // ---- the warps' results: maxima and sums, then O over the tables' place
     float* ml = reinterpret_cast<float*>(smem + L::OFF_ML);
-    float* ow = reinterpret_cast<float*>(smem + L::OFF_TAB);
+    float* ow = reinterpret_cast<float*>(smem + F.tab);
 #pragma unroll
     for (int o = 1; o <= 2; o <<= 1) {
       st.l0 += __shfl_xor_sync(0xffffffffu, st.l0, o);
@@ -512,7 +654,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) rows_kernel(const __grid_constant
       for (int e = 0; e < 4; ++e)
         ow[(warp * 16 + g + 8 * (e >> 1)) * D + (2 * c + (e & 1)) * (D / 8) + j] = st.o[j][e];
     __syncthreads();
-    const int slot = (int)(blockIdx.x - cta_of(A, (int64_t)h * A.nc));
+    const int slot = (int)(blockIdx.x - cta_of(A, head0));
     for (int e = threadIdx.x; e < 16 * D; e += 32 * NW) {
       const int row = e / D, ch = e % D;
       const int64_t r = r0 + row;
@@ -539,27 +681,198 @@ __global__ void __launch_bounds__(NTHREADS, 1) rows_kernel(const __grid_constant
       }
     }
   }
-  if (!ok && lane == 0) {
-    timeout_flag();
-    // copies that were issued land before the CTA exits
-    for (int i = 0; i < NSTAGE; ++i)
-      if (issued[i] > 0) mbar_wait(&full[i], (issued[i] - 1) & 1);
+}
+
+// ------------------------------------------------------------------ unpacking
+// K' and V' of heads h0 .. as [head][T][D] bf16, the cache that the
+// reconstruction returns, with the decoding of K' above for both: a lane rebuilds
+// 16 adjacent channels of a key at a time and stores them as one 32-byte sector.
+struct UnpackArgs {
+  Dims Dm;
+  CacheView v;
+  int64_t T, nt, total;  // tokens; tiles per head, in all
+  int h0;
+  uint16_t *K, *V;
+};
+
+__device__ __forceinline__ void store32(uint16_t* dst, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]),
+               "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+template <int D, bool TAB>
+__device__ __forceinline__ void unpack16(const UnpackArgs& A, const Fields& F, const uint8_t* pk,
+                                         const uint8_t* smem, const uint16_t* gk, const uint16_t* gv,
+                                         int lo, int hi, uint16_t* K, uint16_t* V) {
+  using St = Stage<D>;
+  constexpr int KCH = D / 4, KW = KCH / 16;
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const Dims& Dm = A.Dm;
+  const int G = Dm.G, ng = Dm.ng, r = Dm.r, ib = Dm.idx_bytes;
+  const uint8_t* tk = smem + F.tab;
+  const uint8_t* tvv = tk + Dm.C * D * 2;
+  uint32_t one;
+  asm volatile("mov.b32 %0, 0x3F800000;" : "=r"(one));
+  uint32_t a[2] = {0, 0};
+  float cs[2] = {0.0f, 0.0f};
+  bool live[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int k = g + 8 * x;
+    live[x] = k >= lo && k < hi;
+    if (r > 0) {
+      cs[x] = h2f(reinterpret_cast<const uint16_t*>(pk + F.cs)[k]);
+      uint32_t two = 0;
+      if (r == MAX_R) {
+        two = reinterpret_cast<const uint16_t*>(pk + F.co)[k * (MAX_R / 2) + c];
+      } else {
+        if (2 * c < r) two = pk[F.co + k * r + 2 * c];
+        if (2 * c + 1 < r) two |= (uint32_t)pk[F.co + k * r + 2 * c + 1] << 8;
+      }
+      a[x] = i8_pair_bf16(two);
+    }
+  }
+  const uint4* us = reinterpret_cast<const uint4*>(smem + RLay<D, NW_UNPACK>::OFF_U) + lane;
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+    const bool comp = kv == 0 && r > 0;
+    int row[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const uint32_t f = kv ? F.vi : F.ki;
+      row[x] = !live[x] ? 0
+               : ib == 1 ? (int)pk[f + g + 8 * x]
+                         : (int)reinterpret_cast<const uint16_t*>(pk + f)[g + 8 * x];
+    }
+#pragma unroll
+    for (int w = 0; w < KW; ++w) {
+      const int wa = D == 128 ? w ^ (c >> 1) : w;  // the lane's code word
+      uint32_t out[2][8];
+      uint32_t code[2];
+      Decode dc[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int k = g + 8 * x;
+        code[x] = reinterpret_cast<const uint32_t*>(pk + (kv ? St::VC : St::KC))[k * (D / 16) + c * KW + wa];
+        dc[x] = decode_of(
+            reinterpret_cast<const uint32_t*>(pk + (kv ? F.vp : St::KP))[k * ng + (c * KCH + 16 * wa) / G]);
+      }
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        uint4 cw[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int piece = c * (KCH / 8) + 2 * wa + hf;
+          cw[x] = TAB ? *reinterpret_cast<const uint4*>((kv ? tvv : tk) + piece_at<D>(row[x], piece))
+                      : __ldg(reinterpret_cast<const uint4*>((kv ? gv : gk) + (size_t)row[x] * D) + piece);
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {  // pair of channels 2y, 2y + 1 of the piece
+          const int j = 8 * w + 4 * hf + y;
+          float corr[4];
+          if (comp) {
+            const uint4 u = us[j * 32];
+            mma16_new(corr, a[0], a[1], a[0], a[1], u.x, u.y);
+            mma8(corr, a[0], a[1], u.z);
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t at = hf == 0 ? (y < 2 ? code_byte<0>(code[x]) : code_byte<1>(code[x]))
+                                        : (y < 2 ? code_byte<2>(code[x]) : code_byte<3>(code[x]));
+            const int p0 = 2 * (y & 1);
+            const uint32_t cb = reinterpret_cast<const uint32_t(&)[4]>(cw[x])[y];
+            float v0 = __uint_as_float(cb << 16) + fmaf(magic(at, p0, one), dc[x].s[p0], dc[x].m[p0]);
+            float v1 = __uint_as_float(cb & 0xffff0000u) +
+                       fmaf(magic(at, p0 + 1, one), dc[x].s[p0 + 1], dc[x].m[p0 + 1]);
+            if (comp) {
+              v0 = fmaf(corr[2 * x], cs[x], v0);
+              v1 = fmaf(corr[2 * x + 1], cs[x], v1);
+            }
+            out[x][4 * hf + y] = pack_bf16(v0, v1);
+          }
+        }
+      }
+      uint16_t* dst = (kv ? V : K) + c * KCH + 16 * wa;
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (live[x]) store32(dst + (size_t)(g + 8 * x) * D, out[x]);
+    }
   }
 }
 
-template <int D>
-cudaError_t launch_rows(const RowsArgs& a, int grid, int tiles, cudaStream_t s) {
-  using L = RLay<D>;
-  uint32_t tab = a.tables ? 2u * a.Dm.C * D * 2 : 0u;
-  if (tab < L::MERGE) tab = L::MERGE;
-  const int bytes = (int)(L::OFF_TAB + tab);
-  cudaError_t e = cudaFuncSetAttribute(rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+template <int D, bool TAB>
+__global__ void __launch_bounds__(32 * NW_UNPACK, 1) unpack_kernel(const __grid_constant__ UnpackArgs A) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  const Fields F = fields_of<D, NW_UNPACK>(A.Dm);
+  const int64_t x0 = blockIdx.x * A.total / gridDim.x, x1 = (blockIdx.x + 1) * A.total / gridDim.x;
+  for (int64_t x = x0; x < x1;) {
+    const int hr = (int)(x / A.nt);  // head of this call
+    const int64_t head0 = (int64_t)hr * A.nt;
+    const int64_t end = head0 + A.nt < x1 ? head0 + A.nt : x1;
+    const int64_t tend = (end - head0) * KT < A.T ? (end - head0) * KT : A.T;
+    uint16_t* const K = A.K + (size_t)hr * A.T * D;
+    uint16_t* const V = A.V + (size_t)hr * A.T * D;
+    walk<D, NW_UNPACK, TAB>(
+        A.Dm, A.v, F, smem, A.h0 + hr, (x - head0) * KT, tend,
+        [&](const uint8_t* pk, int lo, int hi, int64_t t, const uint16_t* gk, const uint16_t* gv) {
+          const size_t o = (size_t)t * KT * D;
+          unpack16<D, TAB>(A, F, pk, smem, gk, gv, lo, hi, K + o, V + o);
+        });
+    __syncthreads();  // the tables are done with
+    x = end;
+  }
+}
+
+template <class Kernel, class Args>
+cudaError_t launch(Kernel kern, const Args& a, dim3 grid, int threads, uint32_t bytes, cudaStream_t s) {
+  if (bytes > 227 * 1024) return cudaErrorInvalidConfiguration;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   if (e != cudaSuccess) return e;
-  rows_kernel<D><<<dim3((unsigned)grid, (unsigned)tiles), NTHREADS, bytes, s>>>(a);
+  kern<<<grid, threads, bytes, s>>>(a);
   return cudaGetLastError();
 }
 
+template <int D, bool TAB>
+cudaError_t launch_rows(const RowsArgs& a, int grid, int tiles, cudaStream_t s) {
+  uint32_t tab = TAB ? 2u * a.Dm.C * D * 2 : 0u;
+  if (tab < RLay<D, NW_ROWS>::MERGE) tab = RLay<D, NW_ROWS>::MERGE;
+  return launch(rows_kernel<D, TAB>, a, dim3((unsigned)grid, (unsigned)tiles), 32 * NW_ROWS,
+                fields_of<D, NW_ROWS>(a.Dm).tab + tab, s);
+}
+
+template <int D, bool TAB>
+cudaError_t launch_unpack(const UnpackArgs& a, int grid, cudaStream_t s) {
+  const uint32_t tab = TAB ? 2u * a.Dm.C * D * 2 : 0u;
+  return launch(unpack_kernel<D, TAB>, a, dim3((unsigned)grid), 32 * NW_UNPACK,
+                fields_of<D, NW_UNPACK>(a.Dm).tab + tab, s);
+}
+
+// Both centroid tables of a head fit in shared memory beside the rest.
+bool tables_fit(const Dims& D) { return (int64_t)D.C * D.d <= 32768; }
+
 }  // namespace
+
+bool unpack_fast_supported(const Dims& D) { return D.r <= MAX_R; }
+
+cudaError_t launch_unpack_fast(const Dims& D, const CacheView& v, int64_t T, int h0, int heads, uint16_t* K,
+                               uint16_t* V, int sms, cudaStream_t s) {
+  UnpackArgs a = {};
+  a.Dm = D;
+  a.v = v;
+  a.T = T;
+  a.nt = (T + KT - 1) / KT;
+  a.total = a.nt * heads;
+  a.h0 = h0;
+  a.K = K;
+  a.V = V;
+  const int64_t most = (a.total + NW_UNPACK - 1) / NW_UNPACK;  // CTAs with a tile for every warp
+  const int grid = (int)(most < sms ? most : sms);
+  if (D.d == 128)
+    return tables_fit(D) ? launch_unpack<128, true>(a, grid, s) : launch_unpack<128, false>(a, grid, s);
+  return tables_fit(D) ? launch_unpack<64, true>(a, grid, s) : launch_unpack<64, false>(a, grid, s);
+}
 
 // At most this many rows per head run here: up to two 16-row tiles, which decode
 // the history once each.
@@ -567,8 +880,8 @@ bool rows_supported(const Dims& D, int64_t rows) { return D.r <= MAX_R && rows <
 
 RowsPlan rows_plan(const Dims& D, int64_t T, int sms, int most) {
   RowsPlan p;
-  const int64_t nc = (T + CH - 1) / CH, total = nc * D.H;
-  // a head's run of nc chunks meets at most nc grid / total + 2 CTAs' runs
+  const int64_t nt = (T + KT - 1) / KT, total = nt * D.H;
+  // a head's nt tiles meet at most nt grid / total + 2 CTAs' runs
   int64_t grid = sms < total ? sms : total;
   if (grid / D.H + 2 > most) grid = (int64_t)D.H * (most - 2 > 0 ? most - 2 : 1);
   if (grid > total) grid = total;
@@ -594,18 +907,13 @@ cudaError_t launch_rows(const Dims& D, const CacheView& v, int64_t T, const uint
   a.ws_l = ws_l;
   a.nq = nq;
   a.nslot = plan.slots;
-  a.nc = (T + CH - 1) / CH;
-  a.total = a.nc * D.H;
-  a.tables = (int64_t)D.C * D.d <= 32768;
+  a.nt = (T + KT - 1) / KT;
+  a.total = a.nt * D.H;
+  const bool tab = tables_fit(D);
   const int tiles = (int)((a.rows + 15) / 16);
-  return D.d == 128 ? launch_rows<128>(a, plan.grid, tiles, s) : launch_rows<64>(a, plan.grid, tiles, s);
-}
-
-int read_and_clear_rows_timeout() {
-  int v = 0, z = 0;
-  if (cudaMemcpyFromSymbol(&v, g_rows_timeout, sizeof(int)) != cudaSuccess) return -1;
-  if (v) cudaMemcpyToSymbol(g_rows_timeout, &z, sizeof(int));
-  return v;
+  if (D.d == 128)
+    return tab ? launch_rows<128, true>(a, plan.grid, tiles, s) : launch_rows<128, false>(a, plan.grid, tiles, s);
+  return tab ? launch_rows<64, true>(a, plan.grid, tiles, s) : launch_rows<64, false>(a, plan.grid, tiles, s);
 }
 
 }  // namespace qwm

@@ -231,8 +231,12 @@ def test_attention_shared(d, H, gh, T, new, own, page, causal):
 
 @pytest.mark.parametrize("C,G,r,d", [(16, 16, 0, 128), (300, 32, 16, 128), (300, 32, 8, 64), (16, 32, 5, 64)])
 def test_shared_history_is_the_reconstruction(C, G, r, d):
-    """The unpacked history is the bf16 cache that the reconstruction returns, bit for bit: it is read
-    back from the workspace, which ends with it (keys, then values)."""
+    """The unpacked history, read back from the workspace, which ends with it (keys, then values), is the
+    bf16 cache that the reconstruction returns.  Values, and keys without compensation, are equal bit for
+    bit.  The compensation's r products are summed in another order, so before the one rounding a key
+    element may be off by (r + 4) 2^-24 of sum |U c| <= 2 |K'| or so; the rounding then falls the other
+    way, by one step, where the sum lies that near a border between two bf16 values, 2^-7 |K'| apart: for
+    at most 2 (8 + 4) 2^-24 2 / 2^-7 = 4e-4 of the elements."""
     c, Kp, Vp, rows, kv, table, Q, cu, lens = _shared_case(d, 2, 1, 701, (70,), (20,), 16, False, 5, C=C, G=G, r=r)
     full = q.qwm_attention_shared_workspace(c.c, Q.shape[0], 2, 1, 70, 20)[1]
     ws = torch.zeros(full, dtype=torch.uint8, device="cuda")
@@ -240,8 +244,9 @@ def test_shared_history_is_the_reconstruction(C, G, r, d):
     _fine()
     n = 2 * 701 * d
     tail = ws[full - 4 * n:].view(torch.int16)
-    assert torch.equal(tail[:n].view(2, 701, d), Kp.view(torch.int16))
     assert torch.equal(tail[n:].view(2, 701, d), Vp.view(torch.int16))
+    off = (tail[:n].view(2, 701, d).int() - Kp.view(torch.int16).int()).abs()
+    assert off.max() <= (1 if 0 < r <= 8 else 0) and (off > 0).double().mean() <= 4e-4, (off.max(), (off > 0).sum())
 
 
 @pytest.mark.parametrize("C,G,r,d,T,rows", [
