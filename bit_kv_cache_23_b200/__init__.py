@@ -281,17 +281,29 @@ def qwm_device_status() -> int:
 
 
 # ----------------------------------------------------------------- around the cache
-def _rows_ptr(t: torch.Tensor, name: str, like=None, heads=None, dim=None):
-    """(pointer, row distance) of a [n][heads][head_dim] bf16 CUDA tensor whose
-    heads are contiguous within a row; its rows may be strided."""
+# These calls are short (a few microseconds on the GPU for single tokens), so their
+# checks touch each tensor once and launch without a context manager.
+def _not_cuda(t, name, index):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
-    if t.dtype != torch.bfloat16:
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+
+
+def _device_of(t, name) -> int:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        _not_cuda(t, name, -1)
+    return t.get_device()
+
+
+def _rows_ptr(t: torch.Tensor, name: str, index: int, heads=None, dim=None):
+    """(pointer, row distance) of a [n][heads][head_dim] bf16 tensor on cuda:index whose
+    heads are contiguous within a row; its rows may be strided."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != index:
+        _not_cuda(t, name, index)
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if like is not None and t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
     if t.dim() != 3:
         raise ValueError(f"{name} must be [n][heads][head_dim]")
     n, h, d = t.shape
@@ -303,54 +315,59 @@ def _rows_ptr(t: torch.Tensor, name: str, like=None, heads=None, dim=None):
     return t.data_ptr(), (row if n > 1 else max(h * d, 8))
 
 
-def _ints_ptr(t: torch.Tensor, name: str, shape, like):
+def _ints_ptr(t: torch.Tensor, name: str, index: int, *shape):
     """Pointer of a contiguous int32 tensor of this shape (None: any length)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda or t.device != like.device:
-        raise ValueError(f"{name} must be on {like.device}")
-    if t.dtype != torch.int32:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != index:
+        _not_cuda(t, name, index)
+    if t.dtype is not torch.int32:
         raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
     if t.dim() != len(shape) or any(b is not None and a != b for a, b in zip(t.shape, shape)):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def _weight_ptr(w, name, dim, like):
+def _weight_ptr(w, name, index, dim):
     if w is None:
         return None
-    if w.shape != (dim,):
-        raise ValueError(f"{name} must be [{dim}]")
-    if w.device != like.device:
-        raise ValueError(f"{name} is on {w.device}, expected {like.device}")
-    return _dev_ptr(w, name, torch.bfloat16)
+    if not isinstance(w, torch.Tensor) or not w.is_cuda or w.get_device() != index:
+        _not_cuda(w, name, index)
+    if w.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {w.dtype}")
+    if w.shape != (dim,) or not w.is_contiguous():
+        raise ValueError(f"{name} must be [{dim}], contiguous")
+    return w.data_ptr()
 
 
-class _on:
-    """Make `device` current for a call (the library launches on the current
-    device); no work when it already is."""
-
-    def __init__(self, device):
-        self.index = device.index
-
-    def __enter__(self):
-        self.before = torch.cuda.current_device()
-        if self.before != self.index:
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        if self.before != self.index:
-            torch.cuda.set_device(self.before)
+def _raw_stream(stream, index) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _held(stream, *tensors):
-    """Tensors allocated here (on the current stream) and used on `stream`."""
-    if stream is not None and hasattr(stream, "cuda_stream"):
-        for t in tensors:
-            if t is not None and stream != torch.cuda.current_stream(t.device):
-                t.record_stream(stream)
+def _launch(name: str, index: int, *args) -> None:
+    """The library launches on the current device: make it cuda:index for the call."""
+    before = torch.cuda.current_device()
+    if before == index:
+        st = getattr(lib(), name)(*args)
+    else:
+        torch.cuda.set_device(index)
+        try:
+            st = getattr(lib(), name)(*args)
+        finally:
+            torch.cuda.set_device(before)
+    if st != 0:
+        raise QwmError(name, st)
+
+
+def _held(stream, t):
+    """A tensor allocated here (on the current stream) and used on `stream`."""
+    if stream is not None:
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+        t.record_stream(stream)
+    return t
 
 
 def qwm_rope_init(head_dim: int, rot_dim: int, layout: str = "half", theta: float = 10000.0,
@@ -371,16 +388,16 @@ def qwm_rope_init(head_dim: int, rot_dim: int, layout: str = "half", theta: floa
     return r
 
 
-def _pos_ptr(rope, pos, n, like):
+def _pos_ptr(rope, pos, n, index):
     if rope is None:
         if pos is not None:
             raise ValueError("positions without a rotation")
         return None, None
     if pos is None:
         raise ValueError("a rotation needs positions")
-    if pos.dim() == 1 and rope.n_axes == 1:
-        pos = pos[None]
-    return ctypes.addressof(rope), _ints_ptr(pos, "pos", (rope.n_axes, n), like)
+    if rope.n_axes == 1 and isinstance(pos, torch.Tensor) and pos.dim() == 1:
+        return ctypes.addressof(rope), _ints_ptr(pos, "pos", index, n)
+    return ctypes.addressof(rope), _ints_ptr(pos, "pos", index, rope.n_axes, n)
 
 
 def qwm_norm_rope(rope: qwm_rope | None, Q: torch.Tensor | None, K: torch.Tensor | None = None,
@@ -394,33 +411,34 @@ def qwm_norm_rope(rope: qwm_rope | None, Q: torch.Tensor | None, K: torch.Tensor
     x0 = Q if Q is not None else K
     if x0 is None:
         raise ValueError("neither Q nor K given")
-    args, n, d = [], None, None
+    index = _device_of(x0, "Q" if Q is not None else "K")
+    args, outs, n, d = [], [], None, None
     for x, w, o, name in ((Q, q_weight, Q_out, "Q"), (K, k_weight, K_out, "K")):
         if x is None:
             if w is not None or o is not None:
                 raise ValueError(f"{name} is missing")
-            args += [None, 0, 0, None, None, 0]
+            args += (None, 0, 0, None, None, 0)
+            outs.append(None)
             continue
-        p, ld = _rows_ptr(x, name, x0)
-        if n is not None and (x.shape[0] != n or x.shape[2] != d):
+        p, ld = _rows_ptr(x, name, index)
+        shape = x.shape
+        if n is not None and (shape[0] != n or shape[2] != d):
             raise ValueError("Q and K differ in rows or head_dim")
-        n, h, d = x.shape
+        n, h, d = shape
         if o is None:
-            o = torch.empty((n, h, d), dtype=torch.bfloat16, device=x.device)
-            _held(stream, o)
-        elif o.shape != x.shape:
-            raise ValueError(f"{name}_out must have the shape of {name}")
-        po, ldo = _rows_ptr(o, name + "_out", x0)
-        if name == "Q":
-            Q_out = o
+            o = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+            if stream is not None:
+                _held(stream, o)
+            po, ldo = o.data_ptr(), h * d
         else:
-            K_out = o
-        args += [p, ld, h, _weight_ptr(w, name + " weight", d, x0), po, ldo]
-    rp, pp = _pos_ptr(rope, pos, n, x0)
-    with _on(x0.device):
-        _check("qwm_norm_rope", lib().qwm_norm_rope(rp, d, n, *args, pp, n, float(eps),
-                                                    _stream(stream, x0.device)))
-    return Q_out, K_out
+            po, ldo = _rows_ptr(o, name + "_out", index)
+            if o.shape != shape:
+                raise ValueError(f"{name}_out must have the shape of {name}")
+        outs.append(o)
+        args += (p, ld, h, _weight_ptr(w, name + " weight", index, d), po, ldo)
+    rp, pp = _pos_ptr(rope, pos, n, index)
+    _launch("qwm_norm_rope", index, rp, d, n, *args, pp, n, eps, _raw_stream(stream, index))
+    return outs[0], outs[1]
 
 
 def qwm_paged_append(pages: qwm_pages, table: torch.Tensor, cu: torch.Tensor, start: torch.Tensor,
@@ -429,58 +447,73 @@ def qwm_paged_append(pages: qwm_pages, table: torch.Tensor, cu: torch.Tensor, st
                      eps: float = 1e-6, stream=None) -> None:
     """Write the rows cu[b] .. cu[b+1]-1 of K (normed and rotated on the way) and
     V to positions start[b], start[b]+1, ... of sequence b's pages."""
-    kp, ldk = _rows_ptr(K, "K", None, pages.heads, pages.head_dim)
-    vp, ldv = _rows_ptr(V, "V", K, pages.heads, pages.head_dim)
-    if V.shape[0] != K.shape[0]:
+    index = _device_of(K, "K")
+    kp, ldk = _rows_ptr(K, "K", index, pages.heads, pages.head_dim)
+    vp, ldv = _rows_ptr(V, "V", index, pages.heads, pages.head_dim)
+    n = K.shape[0]
+    if V.shape[0] != n:
         raise ValueError("K and V differ in rows")
-    n, n_seq = K.shape[0], table.shape[0]
-    rp, pp = _pos_ptr(rope, pos, n, K)
-    with _on(K.device):
-        _check("qwm_paged_append", lib().qwm_paged_append(
-            ctypes.byref(pages), _ints_ptr(table, "table", (None, None), K), n_seq, table.shape[1],
-            _ints_ptr(cu, "cu", (n_seq + 1,), K), _ints_ptr(start, "start", (n_seq,), K), kp, ldk, vp,
-            ldv, n, rp, pp, n, _weight_ptr(k_weight, "k_weight", pages.head_dim, K), float(eps),
-            _stream(stream, K.device)))
+    tp = _ints_ptr(table, "table", index, None, None)
+    n_seq, width = table.shape
+    rp, pp = _pos_ptr(rope, pos, n, index)
+    _launch("qwm_paged_append", index, pages, tp, n_seq, width, _ints_ptr(cu, "cu", index, n_seq + 1),
+            _ints_ptr(start, "start", index, n_seq), kp, ldk, vp, ldv, n, rp, pp, n,
+            _weight_ptr(k_weight, "k_weight", index, pages.head_dim), eps, _raw_stream(stream, index))
 
 
-def _lse_ptr(lse, n, heads, like):
+def _lse_ptr(lse, n, heads, index):
     if lse is None:
         return None
-    if lse.shape != (n, heads) or lse.device != like.device:
-        raise ValueError(f"lse must be [{n}][{heads}] on {like.device}")
-    return _dev_ptr(lse, "lse", torch.float32)
+    if not isinstance(lse, torch.Tensor) or not lse.is_cuda or lse.get_device() != index:
+        _not_cuda(lse, "lse", index)
+    if lse.dtype is not torch.float32:
+        raise TypeError(f"lse must be torch.float32, got {lse.dtype}")
+    if lse.shape != (n, heads) or not lse.is_contiguous():
+        raise ValueError(f"lse must be [{n}][{heads}], contiguous")
+    return lse.data_ptr()
 
 
-def _out(O, Q, stream):
+def _out(O, Q, index, stream):
     if O is None:
         O = torch.empty(Q.shape, dtype=torch.bfloat16, device=Q.device)
-        _held(stream, O)
-    elif O.shape != Q.shape or O.device != Q.device:
-        raise ValueError("O must have the shape and device of Q")
+        return O if stream is None else _held(stream, O)
+    if not isinstance(O, torch.Tensor) or not O.is_cuda or O.get_device() != index:
+        _not_cuda(O, "O", index)
+    if O.dtype is not torch.bfloat16:
+        raise TypeError(f"O must be torch.bfloat16, got {O.dtype}")
+    if O.shape != Q.shape or not O.is_contiguous():
+        raise ValueError("O must have the shape of Q, contiguous")
     return O
 
 
-def _scratch(workspace, nbytes, like, stream):
-    """The caller's workspace, or one for this call."""
+def _scratch(workspace, sizes, Q, index, stream):
+    """(tensor, pointer, bytes): the caller's workspace, or one for this call of the
+    full size that sizes() gives."""
     if workspace is None:
+        nbytes = sizes()[1]
         if nbytes == 0:
             return None, None, 0
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
-        _held(stream, workspace)
-    elif workspace.device != like.device:
-        raise ValueError(f"workspace must be on {like.device}")
-    p = _dev_ptr(workspace, "workspace")
-    return workspace, p, workspace.numel() * workspace.element_size()
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=Q.device)
+        if stream is not None:
+            _held(stream, workspace)
+        return workspace, workspace.data_ptr(), nbytes
+    if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or workspace.get_device() != index:
+        _not_cuda(workspace, "workspace", index)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _sizes(name, *args) -> tuple[int, int]:
+    least, full = ctypes.c_uint64(0), ctypes.c_uint64(0)
+    _check(name, getattr(lib(), name)(*args, ctypes.byref(least), ctypes.byref(full)))
+    return least.value, full.value
 
 
 def qwm_attention_shared_workspace(cache: qwm_cache, n_q: int, heads_q: int, n_seq: int, max_q: int,
                                    max_kv: int) -> tuple[int, int]:
     """(least, full) workspace bytes of qwm_attention_shared."""
-    least, full = ctypes.c_uint64(0), ctypes.c_uint64(0)
-    _check("qwm_attention_shared_workspace", lib().qwm_attention_shared_workspace(
-        ctypes.byref(cache), n_q, heads_q, n_seq, max_q, max_kv, ctypes.byref(least),
-        ctypes.byref(full)))
-    return least.value, full.value
+    return _sizes("qwm_attention_shared_workspace", cache, n_q, heads_q, n_seq, max_q, max_kv)
 
 
 def qwm_attention_shared(cache: qwm_cache, Q: torch.Tensor, cu: torch.Tensor, max_q: int,
@@ -492,40 +525,32 @@ def qwm_attention_shared(cache: qwm_cache, Q: torch.Tensor, cu: torch.Tensor, ma
     """Attention of the branches (rows cu[b] .. cu[b+1]-1 of Q) over the packed
     history that they share, followed by the first kv_len[b] positions of each
     branch's pages.  max_q, max_kv: upper bounds of a branch's rows and keys."""
-    n, h, d = Q.shape
-    qp, ldq = _rows_ptr(Q, "Q", None, None, cache.cfg.head_dim)
+    index = _device_of(Q, "Q")
+    qp, ldq = _rows_ptr(Q, "Q", index, None, cache.cfg.head_dim)
+    n, h, _ = Q.shape
+    cup = _ints_ptr(cu, "cu", index, None)
     n_seq = cu.shape[0] - 1
-    cup = _ints_ptr(cu, "cu", (None,), Q)
     pg = tp = kp = None
     width = 0
     if pages is not None:
         if table is None or kv_len is None:
             raise ValueError("pages need a table and kv_len")
+        tp = _ints_ptr(table, "table", index, n_seq, None)
+        kp = _ints_ptr(kv_len, "kv_len", index, n_seq)
         pg, width = ctypes.addressof(pages), table.shape[1]
-        tp = _ints_ptr(table, "table", (n_seq, None), Q)
-        kp = _ints_ptr(kv_len, "kv_len", (n_seq,), Q)
-    O = _out(O, Q, stream)
-    lp = _lse_ptr(lse, n, h, Q)
-    full = 0
-    if workspace is None:
-        full = qwm_attention_shared_workspace(cache, n, h, n_seq, max_q, max_kv)[1]
-    ws, wp, wn = _scratch(workspace, full, Q, stream)
-    with _on(Q.device):
-        _check("qwm_attention_shared", lib().qwm_attention_shared(
-            ctypes.byref(cache), qp, ldq, n, h, cup, n_seq, max_q, pg, tp, width, kp, max_kv,
-            int(causal), float(scale), _dev_ptr(O, "O", torch.bfloat16), lp, wp, wn,
-            _stream(stream, Q.device)))
+    O = _out(O, Q, index, stream)
+    lp = _lse_ptr(lse, n, h, index)
+    ws, wp, wn = _scratch(workspace, lambda: qwm_attention_shared_workspace(cache, n, h, n_seq, max_q, max_kv),
+                          Q, index, stream)
+    _launch("qwm_attention_shared", index, cache, qp, ldq, n, h, cup, n_seq, max_q, pg, tp, width, kp,
+            max_kv, int(causal), scale, O.data_ptr(), lp, wp, wn, _raw_stream(stream, index))
     return O
 
 
 def qwm_cross_attention_workspace(heads_q: int, heads_kv: int, head_dim: int, n_q: int, n_seq: int,
                                   max_q: int, max_kv: int) -> tuple[int, int]:
     """(least, full) workspace bytes of qwm_cross_attention."""
-    least, full = ctypes.c_uint64(0), ctypes.c_uint64(0)
-    _check("qwm_cross_attention_workspace", lib().qwm_cross_attention_workspace(
-        heads_q, heads_kv, head_dim, n_q, n_seq, max_q, max_kv, ctypes.byref(least),
-        ctypes.byref(full)))
-    return least.value, full.value
+    return _sizes("qwm_cross_attention_workspace", heads_q, heads_kv, head_dim, n_q, n_seq, max_q, max_kv)
 
 
 def qwm_cross_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu: torch.Tensor,
@@ -535,27 +560,24 @@ def qwm_cross_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu: t
                         stream=None) -> torch.Tensor:
     """Rows cu[b] .. cu[b+1]-1 of Q attend to rows kv_start[b] ..
     kv_start[b]+kv_len[b]-1 of K and V (strided rows allowed)."""
+    index = _device_of(Q, "Q")
+    qp, ldq = _rows_ptr(Q, "Q", index)
     n, h, d = Q.shape
-    qp, ldq = _rows_ptr(Q, "Q")
-    kp, ldk = _rows_ptr(K, "K", Q, None, d)
-    vp, ldv = _rows_ptr(V, "V", Q, K.shape[1], d)
-    if V.shape[0] != K.shape[0]:
+    kp, ldk = _rows_ptr(K, "K", index, None, d)
+    n_kv, hk, _ = K.shape
+    vp, ldv = _rows_ptr(V, "V", index, hk, d)
+    if V.shape[0] != n_kv:
         raise ValueError("K and V differ in rows")
+    cup = _ints_ptr(cu, "cu", index, None)
     n_seq = cu.shape[0] - 1
-    cup = _ints_ptr(cu, "cu", (None,), Q)
-    sp = _ints_ptr(kv_start, "kv_start", (n_seq,), Q)
-    lnp = _ints_ptr(kv_len, "kv_len", (n_seq,), Q)
-    O = _out(O, Q, stream)
-    lp = _lse_ptr(lse, n, h, Q)
-    full = 0
-    if workspace is None:
-        full = qwm_cross_attention_workspace(h, K.shape[1], d, n, n_seq, max_q, max_kv)[1]
-    ws, wp, wn = _scratch(workspace, full, Q, stream)
-    with _on(Q.device):
-        _check("qwm_cross_attention", lib().qwm_cross_attention(
-            qp, ldq, n, h, kp, ldk, vp, ldv, K.shape[0], K.shape[1], d, cup, sp, lnp, n_seq, max_q,
-            max_kv, float(scale), _dev_ptr(O, "O", torch.bfloat16), lp, wp, wn,
-            _stream(stream, Q.device)))
+    sp = _ints_ptr(kv_start, "kv_start", index, n_seq)
+    lnp = _ints_ptr(kv_len, "kv_len", index, n_seq)
+    O = _out(O, Q, index, stream)
+    lp = _lse_ptr(lse, n, h, index)
+    ws, wp, wn = _scratch(workspace, lambda: qwm_cross_attention_workspace(h, hk, d, n, n_seq, max_q, max_kv),
+                          Q, index, stream)
+    _launch("qwm_cross_attention", index, qp, ldq, n, h, kp, ldk, vp, ldv, n_kv, hk, d, cup, sp, lnp, n_seq,
+            max_q, max_kv, scale, O.data_ptr(), lp, wp, wn, _raw_stream(stream, index))
     return O
 
 

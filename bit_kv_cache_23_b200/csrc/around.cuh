@@ -1,6 +1,8 @@
 // around.cuh -- declarations shared by the operators around the packed cache
 // (norm and rotation, paged append, shared-history and cross attention).
 #pragma once
+#include <atomic>
+
 #include "common.cuh"
 
 namespace qwm {
@@ -25,6 +27,20 @@ RowsPlan rows_plan(const Dims& D, int64_t T, int sms, int most);  // at most `mo
 cudaError_t launch_rows(const Dims& D, const CacheView& v, int64_t T, const uint16_t* Q, int64_t ldq,
                         int64_t nq, int Hq, float scale_log2, const RowsPlan& plan, float* ws_o,
                         float* ws_l, cudaStream_t s);
+
+// Raise a kernel's dynamic shared memory limit to the most it may use, once per
+// device (the attribute costs a call about a microsecond).  `done`: one per kernel.
+template <class Kernel>
+cudaError_t allow_smem(Kernel kern, std::atomic<uint64_t>& done, int bytes) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 inline bool aligned_to(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
 

@@ -102,6 +102,7 @@ struct FlashArgs {
   float* lse;          // or null
   int head0;           // first key head of the pass
   int qblocks, nsplit;
+  int o32;             // O is 32-byte aligned
   int part0;           // first partial of this launch; -1: no partials
   float *ws_o, *ws_l;  // [partial][nq][Hq][D], [partial][nq][Hq]
   CUtensorMap k0, v0, k1, v1;
@@ -111,17 +112,26 @@ struct FlashArgs {
 // and one of the g query heads of key head h), key tiles j0 .. j0 + n - 1.
 struct Work {
   int64_t tok0;    // first token row of the sequence
-  int64_t nb;      // its tokens
-  int64_t r0;
+  int nb;          // its tokens
+  int r0;
   int nr;          // rows of this CTA
   int parity;      // 1: one Q tile; the groups take its even and odd key tiles
   int groups;      // active groups (softmax warpgroup and issuing thread)
   int h;
-  int64_t len1;    // own keys
-  int64_t start1;  // first own row (OWN_ROWS)
-  int64_t b;
+  int len1;        // own keys
+  int start1;      // first own row (OWN_ROWS)
+  int b;
   int nt0;         // tiles of the shared keys
   int j0, n, part;
+  // row r's token
+  __device__ __forceinline__ int token(const FlashArgs& A, int r) const {
+    return A.g == 1 ? r : r / A.g;
+  }
+  // own keys that row r sees (causal)
+  __device__ __forceinline__ int seen(const FlashArgs& A, int r) const {
+    const int x = len1 - nb + token(A, r) + 1;
+    return x < 0 ? 0 : x > len1 ? len1 : x;
+  }
   // rows in group p's Q tile
   __device__ __forceinline__ int rows_of(int p) const {
     const int left = nr - (parity ? 0 : p * QT);
@@ -130,52 +140,54 @@ struct Work {
 };
 
 __device__ __forceinline__ bool work_of(const FlashArgs& A, Work& w) {
-  const int qb = blockIdx.x % A.qblocks, split = blockIdx.x / A.qblocks;
+  const int split = A.nsplit == 1 ? 0 : blockIdx.x / A.qblocks, qb = blockIdx.x - split * A.qblocks;
   w.h = A.head0 + blockIdx.y;
   w.b = blockIdx.z;
   w.part = A.part0 + split;
   bool fault = false;
   w.tok0 = 0;
-  w.nb = A.nq;
+  w.nb = (int)A.nq;
   if (A.cu) {
     const int64_t c0 = A.cu[w.b], c1 = A.cu[w.b + 1];
     fault = c0 < 0 || c1 < c0 || c1 > A.nq;
     if (!fault) {
       w.tok0 = c0;
-      w.nb = c1 - c0;
+      w.nb = (int)(c1 - c0);
     } else {
       w.nb = 0;
     }
   }
-  const int64_t rows = (w.nb < A.max_q ? w.nb : A.max_q) * A.g;
-  w.r0 = (int64_t)qb * ROWS;
+  // (the host refuses more than 2^31 - 1 rows, keys or pages' places)
+  const int rows = (w.nb < A.max_q ? w.nb : (int)A.max_q) * A.g;
+  w.r0 = qb * ROWS;
   w.len1 = 0;
   w.start1 = 0;
   if (A.own != OWN_NONE) {
     int64_t len = A.kv_len[w.b];
     int64_t room = A.own == OWN_PAGES ? (int64_t)A.width << A.shift : A.n_kv;
     if (A.own == OWN_ROWS) {
-      w.start1 = A.kv_start[w.b];
-      fault |= w.start1 < 0 || w.start1 > A.n_kv;
-      w.start1 = w.start1 < 0 ? 0 : w.start1 > A.n_kv ? A.n_kv : w.start1;
+      const int64_t start = A.kv_start[w.b];
+      fault |= start < 0 || start > A.n_kv;
+      w.start1 = (int)(start < 0 ? 0 : start > A.n_kv ? A.n_kv : start);
       room -= w.start1;
     }
     fault |= len < 0 || len > room;
     len = len < 0 ? 0 : len > room ? room : len;
-    w.len1 = len < A.max_kv ? len : A.max_kv;
+    w.len1 = (int)(len < A.max_kv ? len : A.max_kv);
   }
   if (fault && threadIdx.x == 0) atomicExch(&g_flash_fault, 1);
   if (w.r0 >= rows) return false;
-  w.nr = (int)(rows - w.r0 < ROWS ? rows - w.r0 : ROWS);
-  int64_t seen = w.len1;
-  if (A.causal) {  // own keys that the CTA's last row sees
-    seen = w.len1 - w.nb + (w.r0 + w.nr - 1) / A.g + 1;
-    seen = seen < 0 ? 0 : seen > w.len1 ? w.len1 : seen;
-  }
+  w.nr = rows - w.r0 < ROWS ? rows - w.r0 : ROWS;
+  const int seen = A.causal ? w.seen(A, w.r0 + w.nr - 1) : w.len1;  // own keys that the last row sees
   w.nt0 = (int)((A.len0 + KT - 1) / KT);
-  const int64_t nt = w.nt0 + (seen + KT - 1) / KT;
-  w.j0 = (int)(split * nt / A.nsplit);
-  w.n = (int)((split + 1) * nt / A.nsplit) - w.j0;
+  const int nt = w.nt0 + (seen + KT - 1) / KT;
+  w.j0 = 0;
+  w.n = nt;
+  if (A.nsplit > 1) {  // even ranges, the first ones a tile longer
+    const int each = nt / A.nsplit, more = nt - each * A.nsplit;
+    w.j0 = split * each + (split < more ? split : more);
+    w.n = each + (split < more);
+  }
   w.parity = w.nr <= QT && w.n > 1;
   w.groups = w.nr > QT || w.parity ? 2 : 1;
   return true;
@@ -246,9 +258,17 @@ __device__ __forceinline__ void weights(float (&s)[64], uint64_t sc2, uint64_t n
 }
 
 // Row r's place among O's rows.
-__device__ __forceinline__ int64_t out_row(const FlashArgs& A, const Work& w, int64_t r) {
-  const int64_t tok = r / A.g;
-  return (w.tok0 + tok) * A.Hq + (int64_t)w.h * A.g + (r - tok * A.g);
+__device__ __forceinline__ int64_t out_row(const FlashArgs& A, const Work& w, int r) {
+  const int tok = w.token(A, r);
+  return (w.tok0 + tok) * A.Hq + (w.h * A.g + (r - tok * A.g));
+}
+
+// 32 bytes, one sector, to a 32-byte aligned address.
+__device__ __forceinline__ void store32(void* dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d,
+                                        uint32_t e, uint32_t f, uint32_t g, uint32_t h) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a), "r"(b),
+               "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h)
+               : "memory");
 }
 
 // One row of O from TMEM, times `inv` (plus, where `more` is set, `w1` times the
@@ -280,17 +300,28 @@ __device__ __forceinline__ void store_row(const FlashArgs& A, const Work& w, boo
     }
     if (!valid) continue;
     if (A.part0 >= 0) {
-      float4* dst = reinterpret_cast<float4*>(A.ws_o + at * D) + 8 * c;
+      float* dst = A.ws_o + at * D + 32 * c;
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+      for (int k = 0; k < 32; k += 8)
+        store32(dst + k, __float_as_uint(o[k]), __float_as_uint(o[k + 1]), __float_as_uint(o[k + 2]),
+                __float_as_uint(o[k + 3]), __float_as_uint(o[k + 4]), __float_as_uint(o[k + 5]),
+                __float_as_uint(o[k + 6]), __float_as_uint(o[k + 7]));
     } else {
-      uint4* dst = reinterpret_cast<uint4*>(A.O + at * D) + 4 * c;
+      uint16_t* dst = A.O + at * D + 32 * c;
+      if (A.o32) {  // O is 32-byte aligned
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        dst[k] = make_uint4(pack_bf16(o[8 * k], o[8 * k + 1]), pack_bf16(o[8 * k + 2], o[8 * k + 3]),
-                            pack_bf16(o[8 * k + 4], o[8 * k + 5]),
-                            pack_bf16(o[8 * k + 6], o[8 * k + 7]));
+        for (int k = 0; k < 32; k += 16)
+          store32(dst + k, pack_bf16(o[k], o[k + 1]), pack_bf16(o[k + 2], o[k + 3]),
+                  pack_bf16(o[k + 4], o[k + 5]), pack_bf16(o[k + 6], o[k + 7]),
+                  pack_bf16(o[k + 8], o[k + 9]), pack_bf16(o[k + 10], o[k + 11]),
+                  pack_bf16(o[k + 12], o[k + 13]), pack_bf16(o[k + 14], o[k + 15]));
+      } else {
+#pragma unroll
+        for (int k = 0; k < 32; k += 8)
+          *reinterpret_cast<uint4*>(dst + k) =
+              make_uint4(pack_bf16(o[k], o[k + 1]), pack_bf16(o[k + 2], o[k + 3]),
+                         pack_bf16(o[k + 4], o[k + 5]), pack_bf16(o[k + 6], o[k + 7]));
+      }
     }
   }
 }
@@ -300,17 +331,27 @@ __device__ __forceinline__ void softmax_role(const FlashArgs& A, uint8_t* smem, 
                                              uint32_t tmem, const Work& w) {
   using L = Lay<D>;
   const int warp = threadIdx.x >> 5, p = warp >> 2, lane = threadIdx.x & 127;
-  {  // Q rows into shared memory, zeros behind the last
-    constexpr int C = D / 8;
-    const int c = threadIdx.x % C;
-    for (int rr = threadIdx.x / C; rr < (w.nr > QT ? 2 : 1) * QT; rr += 256 / C) {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (rr < w.nr) {
-        const int64_t r = w.r0 + rr, tok = r / A.g;
-        v = __ldg(reinterpret_cast<const uint4*>(
-            A.Q + (w.tok0 + tok) * A.ldq + ((int64_t)w.h * A.g + (r - tok * A.g)) * D + 8 * c));
+  {  // Q rows into shared memory, zeros behind the last; eight loads in flight
+    constexpr int C = D / 8, STEP = 256 / C;
+    const int c = threadIdx.x % C, r1 = w.nr > QT ? ROWS : QT;
+    for (int rr0 = threadIdx.x / C; rr0 < r1; rr0 += 8 * STEP) {
+      uint4 v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int rr = rr0 + u * STEP;
+        v[u] = make_uint4(0, 0, 0, 0);
+        if (rr < w.nr) {
+          const int r = w.r0 + rr, tok = w.token(A, r);
+          v[u] = __ldg(reinterpret_cast<const uint4*>(A.Q + (w.tok0 + tok) * A.ldq +
+                                                      (w.h * A.g + (r - tok * A.g)) * D + 8 * c));
+        }
       }
-      *reinterpret_cast<uint4*>(smem + (rr / QT) * L::Q_TILE + sw128_off(rr % QT, c, QT)) = v;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int rr = rr0 + u * STEP;
+        if (rr < r1)
+          *reinterpret_cast<uint4*>(smem + (rr / QT) * L::Q_TILE + sw128_off(rr % QT, c, QT)) = v[u];
+      }
     }
     fence_proxy_async_smem();
     warp_arrive(&bars[L::B_Q]);
@@ -318,12 +359,8 @@ __device__ __forceinline__ void softmax_role(const FlashArgs& A, uint8_t* smem, 
   if (p >= w.groups || 32 * (warp & 3) >= w.rows_of(p)) return;
   const int rr = (w.parity ? 0 : p * QT) + lane;  // row in the CTA
   const bool valid = rr < w.nr;
-  const int64_t r = w.r0 + (valid ? rr : 0);
-  int seen = (int)w.len1;  // own keys that this row sees
-  if (A.causal) {
-    const int64_t x = w.len1 - w.nb + r / A.g + 1;
-    seen = x < 0 ? 0 : x > w.len1 ? (int)w.len1 : (int)x;
-  }
+  const int r = w.r0 + (valid ? rr : 0);
+  const int seen = A.causal ? w.seen(A, r) : w.len1;  // own keys that this row sees
   // tiles with hidden keys: the shared keys' last, if not full, and own ones
   // from the first that some row of the warp does not see whole
   int cut0 = (int)(A.len0 % KT);
@@ -441,27 +478,27 @@ __device__ __forceinline__ void issue_tile(const FlashArgs& A, const Work& w, in
     return;
   }
   const CUtensorMap* m = v ? &A.v1 : &A.k1;
-  const int64_t k0 = (int64_t)(j - w.nt0) * KT;
+  const int k0 = (j - w.nt0) * KT;
   if (A.own == OWN_ROWS) {
 #pragma unroll
     for (int c = 0; c < D / 64; ++c)
-      tma_load_3d(dst + c * BLK, m, 64 * c, w.h, (int)(w.start1 + k0), bar);
+      tma_load_3d(dst + c * BLK, m, 64 * c, w.h, w.start1 + k0, bar);
     return;
   }
   const int psize = 1 << A.shift, rows = psize < KT ? psize : KT;
-  const int32_t* table = A.table + w.b * A.width;
+  const int32_t* table = A.table + (int64_t)w.b * A.width;
   for (int r = 0; r < KT; r += rows) {
     // pages behind the end, and page numbers outside the pool, arrive as zeros
-    int64_t page = A.n_pages;
+    int page = (int)A.n_pages;
     if (k0 + r < w.len1) {
       const int32_t at = __ldg(table + ((k0 + r) >> A.shift));
       if (at >= 0 && at < A.n_pages) page = at;
       else atomicExch(&g_flash_fault, 1);
     }
-    const int y = (w.h << A.shift) + (int)((k0 + r) & (psize - 1));
+    const int y = (w.h << A.shift) + ((k0 + r) & (psize - 1));
 #pragma unroll
     for (int c = 0; c < D / 64; ++c)
-      tma_load_3d(dst + c * BLK + r * 128, m, 64 * c, y, (int)page, bar);
+      tma_load_3d(dst + c * BLK + r * 128, m, 64 * c, y, page, bar);
   }
 }
 
@@ -481,7 +518,7 @@ __device__ __forceinline__ void load_role(const FlashArgs& A, uint8_t* smem, uin
       break;
     }
     const int j = w.j0 + e / 2;
-    const int64_t left = j < w.nt0 ? KT : w.len1 - (int64_t)(j - w.nt0) * KT;
+    const int left = j < w.nt0 ? KT : w.len1 - (j - w.nt0) * KT;
     const uint32_t dst = base + L::OFF_KV + slot * L::ENT;
     // V rows behind the end are overwritten before the tile is handed on
     const bool wipe = (e & 1) && left < KT;
@@ -494,7 +531,7 @@ __device__ __forceinline__ void load_role(const FlashArgs& A, uint8_t* smem, uin
     if (wipe) {
       if (!warp_wait(bar, rag++ & 1)) { ok = false; ++e; break; }
       constexpr int C = D / 8;
-      for (int x = (int)left * C + lane; x < KT * C; x += 32)
+      for (int x = left * C + lane; x < KT * C; x += 32)
         *reinterpret_cast<uint4*>(smem + L::OFF_KV + slot * L::ENT + sw128_off(x / C, x % C, KT)) =
             make_uint4(0, 0, 0, 0);
       fence_proxy_async_smem();
@@ -570,8 +607,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) flash_kernel(const __grid_constan
   if (w.n == 0) {  // no keys in this range
     const int rr = threadIdx.x;
     for (int e = rr; e < w.nr * (D / 8); e += NTHREADS) {
-      const int64_t r = w.r0 + e / (D / 8), tok = r / A.g;
-      const int64_t row = (w.tok0 + tok) * A.Hq + (int64_t)w.h * A.g + (r - tok * A.g);
+      const int64_t row = out_row(A, w, w.r0 + e / (D / 8));
       const int c = e % (D / 8);
       if (A.part0 >= 0) {
         const size_t at = (size_t)w.part * A.nq * A.Hq + row;
@@ -873,8 +909,8 @@ bool map_3d(CUtensorMap* m, const void* base, int D, int64_t n1, int64_t ld1, in
 
 template <int D>
 cudaError_t launch_flash(const FlashArgs& a, int heads, int64_t n_seq, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(flash_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)Lay<D>::SMEM);
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_smem(flash_kernel<D>, allowed, (int)Lay<D>::SMEM);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((int64_t)a.qblocks * a.nsplit), (unsigned)heads, (unsigned)n_seq);
   flash_kernel<D><<<grid, NTHREADS, Lay<D>::SMEM, s>>>(a);
@@ -942,9 +978,9 @@ SharedPlan plan_shared(const Dims& D, int64_t T, int Hq, int64_t n_q, int64_t n_
   return p;
 }
 
-bool lengths_ok(int64_t n_q, int64_t n_seq, int64_t max_q, int64_t max_kv) {
-  return n_q >= 0 && n_q <= kMaxGridX && n_seq >= 1 && n_seq <= 65535 && max_q >= 0 &&
-         max_q <= kMaxGridX && max_kv >= 0 && max_kv <= kMaxGridX;
+bool lengths_ok(int64_t n_q, int g, int64_t n_seq, int64_t max_q, int64_t max_kv) {
+  return n_q >= 0 && n_q * g <= kMaxGridX - ROWS && n_seq >= 1 && n_seq <= 65535 && max_q >= 0 &&
+         max_q <= kMaxGridX && max_kv >= 0 && max_kv <= kMaxGridX - KT;
 }
 
 }  // namespace
@@ -971,8 +1007,8 @@ extern "C" qwm_status qwm_attention_shared_workspace(const qwm_cache* c, int64_t
                                                      int32_t heads_q, int64_t n_seq, int64_t max_q,
                                                      int64_t max_kv, uint64_t* least,
                                                      uint64_t* full) {
-  if (!cache_ok(c) || !least || !full || !lengths_ok(n_q, n_seq, max_q, max_kv) || heads_q < 1 ||
-      heads_q > 65535 || heads_q % c->cfg.heads)
+  if (!cache_ok(c) || c->len > kMaxGridX - KT || !least || !full || heads_q < 1 || heads_q > 65535 || heads_q % c->cfg.heads ||
+      !lengths_ok(n_q, heads_q / c->cfg.heads, n_seq, max_q, max_kv))
     return QWM_ERR_INVALID_ARG;
   const Dims D = dims_of(&c->cfg);
   const SharedPlan p = plan_shared(D, c->len, heads_q, n_q, n_seq, max_q, max_kv);
@@ -1027,6 +1063,7 @@ extern "C" qwm_status qwm_attention_shared(const qwm_cache* c, const void* Q, in
   a.max_q = max_q;
   a.scale_log2 = (scale > 0.0f ? scale : 1.0f / sqrtf((float)D.d)) * 1.4426950408889634f;
   a.O = (uint16_t*)O;
+  a.o32 = aligned_to(O, 32);
   a.lse = lse;
   a.ws_o = (float*)workspace;
   a.ws_l = a.ws_o + (size_t)plan.np * n_q * heads_q * D.d;
@@ -1112,8 +1149,9 @@ extern "C" qwm_status qwm_cross_attention_workspace(int32_t heads_q, int32_t hea
                                                     int32_t head_dim, int64_t n_q, int64_t n_seq,
                                                     int64_t max_q, int64_t max_kv, uint64_t* least,
                                                     uint64_t* full) {
-  if (!least || !full || !lengths_ok(n_q, n_seq, max_q, max_kv) || heads_kv < 1 || heads_q < 1 ||
-      heads_q > 65535 || heads_q % heads_kv || (head_dim != 64 && head_dim != 128))
+  if (!least || !full || heads_kv < 1 || heads_q < 1 || heads_q > 65535 || heads_q % heads_kv ||
+      (head_dim != 64 && head_dim != 128) ||
+      !lengths_ok(n_q, heads_q / heads_kv, n_seq, max_q, max_kv))
     return QWM_ERR_INVALID_ARG;
   const int64_t mq = max_q < n_q ? max_q : n_q;
   const int64_t units = (mq * (heads_q / heads_kv) + ROWS - 1) / ROWS * heads_kv * n_seq;
@@ -1134,7 +1172,7 @@ extern "C" qwm_status qwm_cross_attention(const void* Q, int64_t ldq, int64_t n_
   const qwm_status st = qwm_cross_attention_workspace(heads_q, heads_kv, head_dim, n_q, n_seq, max_q,
                                                       max_kv, &least, &full);
   if (st != QWM_OK) return st;
-  if (!cu || !kv_start || !kv_len || (n_q > 0 && (!Q || !O)) || n_kv < 0 ||
+  if (!cu || !kv_start || !kv_len || (n_q > 0 && (!Q || !O)) || n_kv < 0 || n_kv > kMaxGridX ||
       (n_kv > 0 && max_kv > 0 && (!K || !V)) || ldq < (int64_t)heads_q * head_dim || ldq % 8 ||
       ldk < (int64_t)heads_kv * head_dim || ldk % 8 || ldv < (int64_t)heads_kv * head_dim || ldv % 8)
     return QWM_ERR_INVALID_ARG;
@@ -1164,6 +1202,7 @@ extern "C" qwm_status qwm_cross_attention(const void* Q, int64_t ldq, int64_t n_
   a.max_kv = max_kv;
   a.scale_log2 = (scale > 0.0f ? scale : 1.0f / sqrtf((float)head_dim)) * 1.4426950408889634f;
   a.O = (uint16_t*)O;
+  a.o32 = aligned_to(O, 32);
   a.lse = lse;
   a.qblocks = (int)((mq * g + ROWS - 1) / ROWS);
   a.nsplit = 1;

@@ -824,29 +824,31 @@ __global__ void __launch_bounds__(32 * NW_UNPACK, 1) unpack_kernel(const __grid_
   }
 }
 
-template <class Kernel, class Args>
-cudaError_t launch(Kernel kern, const Args& a, dim3 grid, int threads, uint32_t bytes, cudaStream_t s) {
-  if (bytes > 227 * 1024) return cudaErrorInvalidConfiguration;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e != cudaSuccess) return e;
-  kern<<<grid, threads, bytes, s>>>(a);
-  return cudaGetLastError();
-}
+constexpr uint32_t kMostSmem = 227 * 1024;
 
 template <int D, bool TAB>
 cudaError_t launch_rows(const RowsArgs& a, int grid, int tiles, cudaStream_t s) {
   uint32_t tab = TAB ? 2u * a.Dm.C * D * 2 : 0u;
   if (tab < RLay<D, NW_ROWS>::MERGE) tab = RLay<D, NW_ROWS>::MERGE;
-  return launch(rows_kernel<D, TAB>, a, dim3((unsigned)grid, (unsigned)tiles), 32 * NW_ROWS,
-                fields_of<D, NW_ROWS>(a.Dm).tab + tab, s);
+  const uint32_t bytes = fields_of<D, NW_ROWS>(a.Dm).tab + tab;
+  if (bytes > kMostSmem) return cudaErrorInvalidConfiguration;
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_smem(rows_kernel<D, TAB>, allowed, (int)kMostSmem);
+  if (e != cudaSuccess) return e;
+  rows_kernel<D, TAB><<<dim3((unsigned)grid, (unsigned)tiles), 32 * NW_ROWS, bytes, s>>>(a);
+  return cudaGetLastError();
 }
 
 template <int D, bool TAB>
 cudaError_t launch_unpack(const UnpackArgs& a, int grid, cudaStream_t s) {
   const uint32_t tab = TAB ? 2u * a.Dm.C * D * 2 : 0u;
-  return launch(unpack_kernel<D, TAB>, a, dim3((unsigned)grid), 32 * NW_UNPACK,
-                fields_of<D, NW_UNPACK>(a.Dm).tab + tab, s);
+  const uint32_t bytes = fields_of<D, NW_UNPACK>(a.Dm).tab + tab;
+  if (bytes > kMostSmem) return cudaErrorInvalidConfiguration;
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_smem(unpack_kernel<D, TAB>, allowed, (int)kMostSmem);
+  if (e != cudaSuccess) return e;
+  unpack_kernel<D, TAB><<<(unsigned)grid, 32 * NW_UNPACK, bytes, s>>>(a);
+  return cudaGetLastError();
 }
 
 // Both centroid tables of a head fit in shared memory beside the rest.

@@ -6,19 +6,29 @@
 //   (a, b) -> gain (a cos t - b sin t, a sin t + b cos t),  t = pos freq.
 //
 // Bound by memory: every element is read once and written once, 4 bytes per
-// element and about 10 fp32 operations.  A head's row lies in D/8 adjacent
-// lanes, 16 bytes each, so the mean is a butterfly over those lanes and the
-// partner of a half-layout pair comes from another lane by shuffles; a lane
-// keeps its channels' cosines, sines and weights in registers over the rows of
-// one token.
+// element; but at 6.5 TB/s an SM has only about 6 operations for each, so the
+// arithmetic is kept short: with pairs (a, b), weights and turn fold into four
+// factors per pair and token, a' = inv (a A1 - b A2), b' = inv (b B1 + a B2), two
+// pairs to an instruction.  A lane holds whole pairs: four of an interleaved
+// 16-byte chunk, or the eight of the two partner chunks of the half layout (with
+// the partner in another lane, shuffles and a second unpacking made the
+// operations the bound).  The mean is a butterfly over a row's lanes.
+//
+// One warp serves a token's query or key heads (or, with few tokens, a slice of
+// them) by itself: no barrier ties its latencies (the angles, a page's place) to
+// other warps', and its next rows are on the way while it works on these.
+// Measured: the 480p frame (1560 x 80 heads x 128, normed and rotated) 10.9 us,
+// 5.9 TB/s; 9361 x 48 heads in the half layout 42.6 us, 5.4 TB/s; a paged append
+// of 5072 x 12 heads 16.6 us, 3.8 TB/s.  A block per token took 18.3, 102 and 44 us.
 //
 // Angles are formed in fp64 and reduced to (-pi, pi] before the fp32 sincosf:
-// in fp32 a position near 10^6 would be off by 0.06 rad.  One thread computes
-// each (token, pair) once for all heads of the block's tokens, through shared
-// memory, which keeps the fp64 work at 1 / heads of the elements.
+// in fp32 a position near 10^6 would be off by 0.06 rad.  A lane computes one or
+// two pairs for all of the warp's rows, through shared memory, which keeps the
+// fp64 work at 1 / heads of the elements.
 #include <math.h>
 
 #include "around.cuh"
+#include "tc.cuh"
 
 namespace qwm {
 
@@ -28,9 +38,8 @@ namespace {
 __device__ int g_index_fault;
 
 constexpr int32_t kRopeMagic = 0x51575250;  // "QWRP"
-constexpr int NT = 256;                     // threads per block
-constexpr int UNROLL = 4;                   // rows in flight per lane
-constexpr int MAX_TB = 4;                   // tokens per block at most
+constexpr int NT = 128;      // threads per block; 5 blocks per SM (102 registers) did better than 4 or 6
+constexpr int UNROLL = 4;    // 16-byte pieces per lane and step; as many again are on the way
 
 struct Side {
   const uint16_t* x;  // rows, ld apart
@@ -44,7 +53,9 @@ struct RopeArgs {
   Side s[2];  // queries and keys; paged: keys and values
   const int32_t* pos;
   int64_t ldpos, n;
-  int tb;    // tokens per block: 1, 2 or 4
+  int64_t units;         // (token, side, slice) of all
+  int slices0, slices;   // of the first side, of both, per token
+  int per_slice;         // heads
   int pairs, end0, end1;  // pairs; first pair behind axis 0 and axis 1
   float gain, eps;
   // paged
@@ -56,19 +67,42 @@ struct RopeArgs {
 
 enum { ROT_NONE = 0, ROT_HALF = 1, ROT_INTER = 2 };
 
-__device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
+__device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
   return r;
+}
+
+// The pairs of a lane, a and b, from its NC chunks of 8 channels and back: pair e
+// is channels 2e, 2e + 1 of the chunk (NC = 1), or channel e of both (NC = 2).
+template <int NC>
+__device__ __forceinline__ void pairs_of(const uint4 (&v)[NC], float (&a)[4 * NC], float (&b)[4 * NC]) {
+  const uint32_t(&x)[4] = reinterpret_cast<const uint32_t(&)[4]>(v[0]);
+  const uint32_t(&y)[4] = reinterpret_cast<const uint32_t(&)[4]>(v[NC - 1]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (NC == 1) {
+      a[i] = low(x[i]);
+      b[i] = high(x[i]);
+    } else {
+      a[2 * i] = low(x[i]);
+      a[2 * i + 1] = high(x[i]);
+      b[2 * i] = low(y[i]);
+      b[2 * i + 1] = high(y[i]);
+    }
+  }
+}
+template <int NC>
+__device__ __forceinline__ void chunks_of(const float (&a)[4 * NC], const float (&b)[4 * NC], uint4 (&v)[NC]) {
+  if constexpr (NC == 1) {
+    v[0] = make_uint4(pack2(a[0], b[0]), pack2(a[1], b[1]), pack2(a[2], b[2]), pack2(a[3], b[3]));
+  } else {
+    v[0] = make_uint4(pack2(a[0], a[1]), pack2(a[2], a[3]), pack2(a[4], a[5]), pack2(a[6], a[7]));
+    v[1] = make_uint4(pack2(b[0], b[1]), pack2(b[2], b[3]), pack2(b[4], b[5]), pack2(b[6], b[7]));
+  }
 }
 
 // Cosine and sine of pos * freq.  k = the nearest whole number of turns; the
@@ -80,149 +114,191 @@ __device__ __forceinline__ float2 turn(int pos, double freq, float gain) {
   double r = fma(k, -6.283185307179586, a);
   r = fma(k, -2.4492935982947064e-16, r);
   float s, c;
-  sincosf((float)r, &s, &c);
+  sincospif((float)(r * 0.3183098861837907), &s, &c);
   return make_float2(c * gain, s * gain);
 }
 
-// Place of position p of sequence b in a pool, as an element offset of head 0,
-// or -1 for a page outside the pool or the table.
+// Place of row t's position in the pools, as an element offset of head 0, or -1:
+// a row of no sequence, or a page outside the pool or the table.  One warp; the
+// sequence is the last that begins at or before t, found by 32 probes at a time.
 __device__ __forceinline__ int64_t place_of(const RopeArgs& A, int64_t t, int D) {
-  // the last sequence that begins at or before row t
-  int64_t lo = 0, hi = A.n_seq;  // cu[lo] <= t < cu[hi], where rows are owned
-  if (t >= A.cu[A.n_seq] || t < A.cu[0]) return -1;  // behind the last sequence: left alone
+  const int lane = threadIdx.x & 31;
+  int64_t lo = -1, hi = A.n_seq + 1;  // cu[lo] <= t < cu[hi]
   while (hi - lo > 1) {
-    const int64_t mid = (lo + hi) >> 1;
-    if (A.cu[mid] <= t) lo = mid;
-    else hi = mid;
+    const int64_t step = (hi - lo + 31) / 32, x = lo + (lane + 1) * step;
+    const unsigned below = __ballot_sync(0xffffffffu, x < hi && __ldg(A.cu + x) <= t);
+    const int n = below == 0xffffffffu ? 32 : __ffs(~below) - 1;  // the leading probes
+    const int64_t up = lo + (n + 1) * step;
+    lo += n * step;
+    hi = up < hi ? up : hi;
   }
-  const int64_t p = (int64_t)A.start[lo] + (t - A.cu[lo]);
+  if (lo < 0 || lo >= A.n_seq) return -1;
+  const int64_t p = (int64_t)__ldg(A.start + lo) + (t - __ldg(A.cu + lo));
   const int64_t col = p >> A.shift;
   int64_t page = -1;
-  if (p >= 0 && col < A.width) page = A.table[lo * A.width + col];
+  if (p >= 0 && col < A.width) page = __ldg(A.table + lo * A.width + col);
   if (page < 0 || page >= A.n_pages) {
-    atomicExch(&g_index_fault, 1);
+    if (lane == 0) atomicExch(&g_index_fault, 1);
     return -1;
   }
   return (((page * A.s[0].heads) << A.shift) + (p & ((1 << A.shift) - 1))) * D;
 }
 
 template <int D, int ROT, bool PAGED>
-__global__ void __launch_bounds__(NT) norm_rope_kernel(const __grid_constant__ RopeArgs A) {
-  constexpr int L = D / 8;        // lanes per row
-  constexpr int GROUPS = NT / L;  // rows per block and step
-  __shared__ float2 cs[ROT ? MAX_TB * QWM_ROPE_MAX_PAIRS : 1];
-  __shared__ int64_t place[MAX_TB];
-  const int64_t t0 = (int64_t)blockIdx.x * A.tb;
-  if (ROT) {
-    for (int e = threadIdx.x; e < A.tb * A.pairs; e += NT) {
-      const int tl = e / A.pairs, i = e - tl * A.pairs;
-      if (t0 + tl < A.n) {
-        const int axis = (i >= A.end0) + (i >= A.end1);
-        cs[tl * QWM_ROPE_MAX_PAIRS + i] =
-            turn(__ldg(A.pos + axis * A.ldpos + t0 + tl), A.freq[i], A.gain);
+__global__ void __launch_bounds__(NT, 5) norm_rope_kernel(const __grid_constant__ RopeArgs A) {
+  using namespace tc;
+  constexpr int NC = ROT == ROT_HALF ? 2 : 1;  // chunks of a lane
+  constexpr int NP = 4 * NC;                   // pairs of a lane
+  constexpr int L = D / (8 * NC);              // lanes per row
+  constexpr int ROWS = 32 / L;                 // rows per warp at once
+  constexpr int U = UNROLL / NC;               // of them in a step
+  constexpr int STEP = ROWS * U;
+  __shared__ float2 cs_all[ROT ? NT / 32 * QWM_ROPE_MAX_PAIRS : 1];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int64_t unit = (int64_t)blockIdx.x * (NT / 32) + warp;
+  if (unit >= A.units) return;
+  const int64_t t = (uint32_t)unit / (uint32_t)A.slices;  // (the host keeps units in 32 bits)
+  const int slice = (int)(unit - t * A.slices), side = slice >= A.slices0;
+  const Side& S = A.s[side];
+  const int h0 = (side ? slice - A.slices0 : slice) * A.per_slice;
+  const int h1 = h0 + A.per_slice < S.heads ? h0 + A.per_slice : S.heads;
+  const bool values = PAGED && side == 1;  // copied as they are
+  const int c = lane % L, row = lane / L;
+  // the lane's chunks: c; or partners c and c + half / 8, and neighbours behind them
+  const int nr = ROT == ROT_HALF ? A.pairs / 8 : 0;
+  int at[NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) at[i] = 8 * (NC == 1 ? c : c < nr ? c + i * nr : 2 * c + i);
+  const uint16_t* const xt = S.x + t * S.ld;
+  auto load = [&](uint4 (&v)[U][NC], int h) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        v[u][i] = make_uint4(0, 0, 0, 0);
+        if (h + row + u * ROWS < h1)
+          v[u][i] = *reinterpret_cast<const uint4*>(xt + (int64_t)(h + row + u * ROWS) * D + at[i]);
       }
+  };
+  uint4 now[U][NC];
+  load(now, h0);
+  float2* cs = cs_all + (ROT ? warp * QWM_ROPE_MAX_PAIRS : 0);
+  if (ROT && !values) {
+    for (int i = lane; i < A.pairs; i += 32) {
+      const int axis = (i >= A.end0) + (i >= A.end1);
+      cs[i] = turn(__ldg(A.pos + axis * A.ldpos + t), A.freq[i], A.gain);
     }
   }
-  if (PAGED && threadIdx.x < A.tb)
-    place[threadIdx.x] = t0 + threadIdx.x < A.n ? place_of(A, t0 + threadIdx.x, D) : -1;
-  __syncthreads();
+  int64_t place = 0;
+  if (PAGED) {
+    place = place_of(A, t, D);
+    if (place < 0) return;
+  }
+  __syncwarp();
 
-  const int c = threadIdx.x % L;  // this lane's 8 channels: 8c .. 8c+7
-  const int grp = threadIdx.x / L;
-  const int tl = grp % A.tb, h0 = grp / A.tb, step = GROUPS / A.tb;
-  const int64_t t = t0 + tl;
-  const bool live = t < A.n && (!PAGED || place[tl] >= 0);
-  const int half = A.pairs / 8;  // chunks of half the rotated channels
-  const bool turns = ROT && c < 2 * half;
-  // the lane that holds the partners of a half-layout pair
-  const int partner = ROT == ROT_HALF && turns ? (c < half ? c + half : c - half) : c;
-  float co[ROT == ROT_HALF ? 8 : 4], si[ROT == ROT_HALF ? 8 : 4];
-  if (ROT) {
-    constexpr int NP = ROT == ROT_HALF ? 8 : 4;
-    const int first = ROT == ROT_HALF ? 8 * (c < half ? c : c - half) : 4 * c;
+  const bool turns = ROT && NP * c < A.pairs;
+  const int64_t oh = PAGED ? (int64_t)D << A.shift : D;  // from head to head
+  const bool norm = !values && S.w != nullptr;
+  uint64_t a1[NP / 2], a2[NP / 2], b1[NP / 2], b2[NP / 2];  // the factors, by twos
+  if (!values && (ROT || norm)) {
+    float wa[NP], wb[NP];
 #pragma unroll
-    for (int e = 0; e < NP; ++e) {
-      float2 v = make_float2(1.0f, 0.0f);
-      if (turns && live) v = cs[tl * QWM_ROPE_MAX_PAIRS + first + e];
-      co[e] = v.x;
-      si[e] = (ROT == ROT_HALF && c < half) ? -v.y : v.y;
+    for (int e = 0; e < NP; ++e) wa[e] = wb[e] = 1.0f;
+    if (norm) {
+      uint4 w[NC];
+#pragma unroll
+      for (int i = 0; i < NC; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(S.w + at[i]));
+      pairs_of<NC>(w, wa, wb);
+    }
+#pragma unroll
+    for (int e = 0; e < NP; e += 2) {
+      float2 x = make_float2(1.0f, 0.0f), y = x;
+      if (turns) {
+        x = cs[NP * c + e];
+        y = cs[NP * c + e + 1];
+      }
+      a1[e / 2] = f2pack(wa[e] * x.x, wa[e + 1] * y.x);
+      a2[e / 2] = f2pack(-wb[e] * x.y, -wb[e + 1] * y.y);
+      b1[e / 2] = f2pack(wb[e] * x.x, wb[e + 1] * y.x);
+      b2[e / 2] = f2pack(wa[e] * x.y, wa[e + 1] * y.y);
     }
   }
-#pragma unroll 1
-  for (int side = 0; side < 2; ++side) {
-    const Side& S = A.s[side];
-    const bool values = PAGED && side == 1;  // copied as they are
-    float w[8], pw[ROT == ROT_HALF ? 8 : 1];
-    const bool norm = S.w != nullptr;
-    if (norm) {
-      unpack8(__ldg(reinterpret_cast<const uint4*>(S.w) + c), w);
-      if constexpr (ROT == ROT_HALF)
-        unpack8(__ldg(reinterpret_cast<const uint4*>(S.w) + partner), pw);
-    }
-    const uint16_t* xt = S.x + t * S.ld + 8 * c;
-    uint16_t* ot = S.out + 8 * c + (PAGED ? place[tl] : t * S.ldo);
-    const int64_t oh = PAGED ? (int64_t)D << A.shift : D;  // from head to head
-    for (int hb = h0; hb - h0 < S.heads; hb += step * UNROLL) {
-      uint4 raw[UNROLL];
+  uint16_t* const ot = S.out + (PAGED ? place : t * S.ldo);
+  for (int h = h0; h < h1; h += STEP) {
+    uint4 next[U][NC];
+    load(next, h + STEP);
 #pragma unroll
-      for (int u = 0; u < UNROLL; ++u) {
-        const int h = hb + u * step;
-        raw[u] = make_uint4(0, 0, 0, 0);
-        if (live && h < S.heads) raw[u] = *reinterpret_cast<const uint4*>(xt + (int64_t)h * D);
-      }
+    for (int u = 0; u < U; ++u) {
+      if (!values && (ROT || norm)) {
+        float a[NP], b[NP];
+        pairs_of<NC>(now[u], a, b);
+        uint64_t inv2 = f2pack(1.0f, 1.0f);
+        if (norm) {
+          uint64_t sq = 0;
 #pragma unroll
-      for (int u = 0; u < UNROLL; ++u) {
-        const int h = hb + u * step;
-        uint4 res = raw[u];
-        if (!values && (ROT || norm)) {
-          float v[8];
-          unpack8(raw[u], v);
-          float inv = 1.0f;
-          if (norm) {
-            float ss = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
-#pragma unroll
-            for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o, L);
-            inv = rsqrtf(ss * (1.0f / D) + A.eps);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = v[e] * inv * w[e];
+          for (int e = 0; e < NP; e += 2) {
+            const uint64_t x = f2pack(a[e], a[e + 1]), y = f2pack(b[e], b[e + 1]);
+            sq = ffma2(x, x, sq);
+            sq = ffma2(y, y, sq);
           }
-          if constexpr (ROT == ROT_HALF) {
-            uint4 pr;
-            pr.x = __shfl_sync(0xffffffffu, raw[u].x, partner, L);
-            pr.y = __shfl_sync(0xffffffffu, raw[u].y, partner, L);
-            pr.z = __shfl_sync(0xffffffffu, raw[u].z, partner, L);
-            pr.w = __shfl_sync(0xffffffffu, raw[u].w, partner, L);
-            float p[8];
-            unpack8(pr, p);
-            if (norm) {
+          float s0, s1;
+          f2unpack(sq, s0, s1);
+          float ss = s0 + s1;
 #pragma unroll
-              for (int e = 0; e < 8; ++e) p[e] = p[e] * inv * pw[e];
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = turns ? fmaf(p[e], si[e], v[e] * co[e]) : v[e];
-          }
-          if constexpr (ROT == ROT_INTER) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float a = v[2 * e], b = v[2 * e + 1];
-              v[2 * e] = turns ? fmaf(-b, si[e], a * co[e]) : a;
-              v[2 * e + 1] = turns ? fmaf(a, si[e], b * co[e]) : b;
-            }
-          }
-          res = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]),
-                           pack2(v[6], v[7]));
+          for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o, L);
+          const float inv = rsqrtf(ss * (1.0f / D) + A.eps);
+          inv2 = f2pack(inv, inv);
         }
-        if (live && h < S.heads) *reinterpret_cast<uint4*>(ot + h * oh) = res;
+#pragma unroll
+        for (int e = 0; e < NP; e += 2) {
+          const uint64_t x = f2pack(a[e], a[e + 1]), y = f2pack(b[e], b[e + 1]);
+          uint64_t p = fmul2(x, a1[e / 2]), q = fmul2(y, b1[e / 2]);
+          if (ROT) {
+            p = ffma2(y, a2[e / 2], p);
+            q = ffma2(x, b2[e / 2], q);
+          }
+          if (norm) {
+            p = fmul2(p, inv2);
+            q = fmul2(q, inv2);
+          }
+          f2unpack(p, a[e], a[e + 1]);
+          f2unpack(q, b[e], b[e + 1]);
+        }
+        chunks_of<NC>(a, b, now[u]);
+      }
+      if (h + row + u * ROWS < h1) {
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+          *reinterpret_cast<uint4*>(ot + (h + row + u * ROWS) * oh + at[i]) = now[u][i];
       }
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < NC; ++i) now[u][i] = next[u][i];
+  }
+}
+
+// A warp per token and side keeps the angles' share small; with few tokens the
+// heads are sliced, down to a step of rows, until 16 warps per SM have work.
+template <int D>
+void set_units(RopeArgs& a) {
+  const int step = 32 / (D / 8) * UNROLL;
+  for (int per = 64;; per /= 2) {
+    a.per_slice = per;
+    a.slices0 = (a.s[0].heads + per - 1) / per;
+    a.slices = a.slices0 + (a.s[1].heads + per - 1) / per;
+    a.units = a.n * a.slices;
+    if (per <= step || a.units >= 148 * 16) return;
   }
 }
 
 template <int D, bool PAGED>
-cudaError_t launch(const RopeArgs& a, int rot, cudaStream_t s) {
-  const unsigned grid = (unsigned)((a.n + a.tb - 1) / a.tb);
+cudaError_t launch(RopeArgs& a, int rot, cudaStream_t s) {
+  set_units<D>(a);
+  const int64_t blocks = (a.units + NT / 32 - 1) / (NT / 32);
+  if (a.units > (int64_t(1) << 31) - 1) return cudaErrorInvalidConfiguration;
+  const unsigned grid = (unsigned)blocks;
   if (rot == ROT_NONE) norm_rope_kernel<D, ROT_NONE, PAGED><<<grid, NT, 0, s>>>(a);
   else if (rot == ROT_HALF) norm_rope_kernel<D, ROT_HALF, PAGED><<<grid, NT, 0, s>>>(a);
   else norm_rope_kernel<D, ROT_INTER, PAGED><<<grid, NT, 0, s>>>(a);
@@ -249,10 +325,6 @@ void set_rope(RopeArgs& a, const qwm_rope* r) {
 int rot_of(const qwm_rope* r) {
   return !r ? ROT_NONE : r->layout == QWM_ROPE_HALF ? ROT_HALF : ROT_INTER;
 }
-
-// Tokens per block: with few tokens one each, so that they spread over the SMs;
-// with many, four, so that one fp64 angle per thread covers the block's pairs.
-int tokens_per_block(int64_t n) { return n >= 4096 ? 4 : n >= 1024 ? 2 : 1; }
 
 }  // namespace
 
@@ -354,7 +426,6 @@ extern "C" qwm_status qwm_norm_rope(const qwm_rope* rope, int32_t head_dim, int6
   a.ldpos = ldpos;
   a.n = n;
   a.eps = eps;
-  a.tb = tokens_per_block(n);
   if (rope) set_rope(a, rope);
   const cudaError_t e = head_dim == 128 ? launch<128, false>(a, rot_of(rope), (cudaStream_t)stream)
                                         : launch<64, false>(a, rot_of(rope), (cudaStream_t)stream);
@@ -386,7 +457,6 @@ extern "C" qwm_status qwm_paged_append(const qwm_pages* p, const int32_t* table,
   a.ldpos = ldpos;
   a.n = n;
   a.eps = eps;
-  a.tb = tokens_per_block(n);
   a.table = table;
   a.cu = cu;
   a.start = start;
