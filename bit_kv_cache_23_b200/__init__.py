@@ -281,63 +281,66 @@ def qwm_device_status() -> int:
 
 
 # ----------------------------------------------------------------- around the cache
-# These calls are short (a few microseconds on the GPU for single tokens), so their
-# checks touch each tensor once and launch without a context manager.
-def _not_cuda(t, name, index):
+# These calls are short (a few microseconds on the GPU for single tokens), so a
+# tensor that is in order passes one combined test; what is wrong with another is
+# found out afterwards.
+_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+
+
+def _refuse(t, name, index, dtype, shape):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
-    raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} has shape {tuple(t.shape)} and strides {t.stride()}, expected {shape}, contiguous")
 
 
 def _device_of(t, name) -> int:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        _not_cuda(t, name, -1)
+        _refuse(t, name, None, None, None)
     return t.get_device()
 
 
 def _rows_ptr(t: torch.Tensor, name: str, index: int, heads=None, dim=None):
     """(pointer, row distance) of a [n][heads][head_dim] bf16 tensor on cuda:index whose
     heads are contiguous within a row; its rows may be strided."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != index:
-        _not_cuda(t, name, index)
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [n][heads][head_dim]")
+    if not isinstance(t, torch.Tensor) or t.dtype is not _BF16 or t.get_device() != index or t.dim() != 3:
+        _refuse(t, name, index, _BF16, "[n][heads][head_dim]")
     n, h, d = t.shape
     if (heads is not None and h != heads) or (dim is not None and d != dim):
         raise ValueError(f"{name} has heads x head_dim = {h} x {d}, expected {heads} x {dim}")
     row, head, one = t.stride()
-    if (one != 1 and d > 1) or (h > 1 and head != d):
+    if (one != 1 and d > 1) or (head != d and h > 1):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
     return t.data_ptr(), (row if n > 1 else max(h * d, 8))
 
 
-def _ints_ptr(t: torch.Tensor, name: str, index: int, *shape):
-    """Pointer of a contiguous int32 tensor of this shape (None: any length)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != index:
-        _not_cuda(t, name, index)
-    if t.dtype is not torch.int32:
-        raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
-    if t.dim() != len(shape) or any(b is not None and a != b for a, b in zip(t.shape, shape)):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+def _vec_ptr(t, name, index, dtype, n=None):
+    """Pointer of a contiguous vector of n (None: any number) on cuda:index."""
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index or t.dim() != 1
+            or (n is not None and t.shape[0] != n) or not t.is_contiguous()):
+        _refuse(t, name, index, dtype, f"[{'n' if n is None else n}]")
     return t.data_ptr()
 
 
-def _weight_ptr(w, name, index, dim):
-    if w is None:
-        return None
-    if not isinstance(w, torch.Tensor) or not w.is_cuda or w.get_device() != index:
-        _not_cuda(w, name, index)
-    if w.dtype is not torch.bfloat16:
-        raise TypeError(f"{name} must be torch.bfloat16, got {w.dtype}")
-    if w.shape != (dim,) or not w.is_contiguous():
-        raise ValueError(f"{name} must be [{dim}], contiguous")
-    return w.data_ptr()
+def _mat_ptr(t, name, index, dtype, n=None, m=None):
+    """Pointer of a contiguous matrix [n][m] (None: any number) on cuda:index."""
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index or t.dim() != 2
+            or (n is not None and t.shape[0] != n) or (m is not None and t.shape[1] != m)
+            or not t.is_contiguous()):
+        _refuse(t, name, index, dtype, f"[{'n' if n is None else n}][{'m' if m is None else m}]")
+    return t.data_ptr()
+
+
+def _new(shape, x, stream):
+    """A contiguous bf16 tensor beside x, allocated on the current stream and, where
+    another one is given, used there."""
+    o = x.new_empty(shape)
+    return o if stream is None else _held(stream, o)
 
 
 def _raw_stream(stream, index) -> int:
@@ -396,8 +399,8 @@ def _pos_ptr(rope, pos, n, index):
     if pos is None:
         raise ValueError("a rotation needs positions")
     if rope.n_axes == 1 and isinstance(pos, torch.Tensor) and pos.dim() == 1:
-        return ctypes.addressof(rope), _ints_ptr(pos, "pos", index, n)
-    return ctypes.addressof(rope), _ints_ptr(pos, "pos", index, rope.n_axes, n)
+        return ctypes.addressof(rope), _vec_ptr(pos, "pos", index, _I32, n)
+    return ctypes.addressof(rope), _mat_ptr(pos, "pos", index, _I32, rope.n_axes, n)
 
 
 def qwm_norm_rope(rope: qwm_rope | None, Q: torch.Tensor | None, K: torch.Tensor | None = None,
@@ -426,16 +429,15 @@ def qwm_norm_rope(rope: qwm_rope | None, Q: torch.Tensor | None, K: torch.Tensor
             raise ValueError("Q and K differ in rows or head_dim")
         n, h, d = shape
         if o is None:
-            o = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
-            if stream is not None:
-                _held(stream, o)
-            po, ldo = o.data_ptr(), h * d
+            o = _new(shape, x, stream)
+            po, ldo = o.data_ptr(), max(h * d, 8)
         else:
             po, ldo = _rows_ptr(o, name + "_out", index)
             if o.shape != shape:
                 raise ValueError(f"{name}_out must have the shape of {name}")
         outs.append(o)
-        args += (p, ld, h, _weight_ptr(w, name + " weight", index, d), po, ldo)
+        wp = None if w is None else _vec_ptr(w, name + " weight", index, _BF16, d)
+        args += (p, ld, h, wp, po, ldo)
     rp, pp = _pos_ptr(rope, pos, n, index)
     _launch("qwm_norm_rope", index, rp, d, n, *args, pp, n, eps, _raw_stream(stream, index))
     return outs[0], outs[1]
@@ -453,36 +455,25 @@ def qwm_paged_append(pages: qwm_pages, table: torch.Tensor, cu: torch.Tensor, st
     n = K.shape[0]
     if V.shape[0] != n:
         raise ValueError("K and V differ in rows")
-    tp = _ints_ptr(table, "table", index, None, None)
+    tp = _mat_ptr(table, "table", index, _I32)
     n_seq, width = table.shape
     rp, pp = _pos_ptr(rope, pos, n, index)
-    _launch("qwm_paged_append", index, pages, tp, n_seq, width, _ints_ptr(cu, "cu", index, n_seq + 1),
-            _ints_ptr(start, "start", index, n_seq), kp, ldk, vp, ldv, n, rp, pp, n,
-            _weight_ptr(k_weight, "k_weight", index, pages.head_dim), eps, _raw_stream(stream, index))
+    wp = None if k_weight is None else _vec_ptr(k_weight, "k_weight", index, _BF16, pages.head_dim)
+    _launch("qwm_paged_append", index, pages, tp, n_seq, width, _vec_ptr(cu, "cu", index, _I32, n_seq + 1),
+            _vec_ptr(start, "start", index, _I32, n_seq), kp, ldk, vp, ldv, n, rp, pp, n, wp, eps,
+            _raw_stream(stream, index))
 
 
 def _lse_ptr(lse, n, heads, index):
-    if lse is None:
-        return None
-    if not isinstance(lse, torch.Tensor) or not lse.is_cuda or lse.get_device() != index:
-        _not_cuda(lse, "lse", index)
-    if lse.dtype is not torch.float32:
-        raise TypeError(f"lse must be torch.float32, got {lse.dtype}")
-    if lse.shape != (n, heads) or not lse.is_contiguous():
-        raise ValueError(f"lse must be [{n}][{heads}], contiguous")
-    return lse.data_ptr()
+    return None if lse is None else _mat_ptr(lse, "lse", index, _F32, n, heads)
 
 
 def _out(O, Q, index, stream):
     if O is None:
-        O = torch.empty(Q.shape, dtype=torch.bfloat16, device=Q.device)
-        return O if stream is None else _held(stream, O)
-    if not isinstance(O, torch.Tensor) or not O.is_cuda or O.get_device() != index:
-        _not_cuda(O, "O", index)
-    if O.dtype is not torch.bfloat16:
-        raise TypeError(f"O must be torch.bfloat16, got {O.dtype}")
-    if O.shape != Q.shape or not O.is_contiguous():
-        raise ValueError("O must have the shape of Q, contiguous")
+        return _new(Q.shape, Q, stream)
+    if (not isinstance(O, torch.Tensor) or O.dtype is not _BF16 or O.get_device() != index
+            or O.shape != Q.shape or not O.is_contiguous()):
+        _refuse(O, "O", index, _BF16, f"{tuple(Q.shape)} as Q has")
     return O
 
 
@@ -497,10 +488,9 @@ def _scratch(workspace, sizes, Q, index, stream):
         if stream is not None:
             _held(stream, workspace)
         return workspace, workspace.data_ptr(), nbytes
-    if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or workspace.get_device() != index:
-        _not_cuda(workspace, "workspace", index)
-    if not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
+    if (not isinstance(workspace, torch.Tensor) or workspace.get_device() != index
+            or not workspace.is_contiguous()):
+        _refuse(workspace, "workspace", index, getattr(workspace, "dtype", None), "any shape")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -528,15 +518,15 @@ def qwm_attention_shared(cache: qwm_cache, Q: torch.Tensor, cu: torch.Tensor, ma
     index = _device_of(Q, "Q")
     qp, ldq = _rows_ptr(Q, "Q", index, None, cache.cfg.head_dim)
     n, h, _ = Q.shape
-    cup = _ints_ptr(cu, "cu", index, None)
+    cup = _vec_ptr(cu, "cu", index, _I32)
     n_seq = cu.shape[0] - 1
     pg = tp = kp = None
     width = 0
     if pages is not None:
         if table is None or kv_len is None:
             raise ValueError("pages need a table and kv_len")
-        tp = _ints_ptr(table, "table", index, n_seq, None)
-        kp = _ints_ptr(kv_len, "kv_len", index, n_seq)
+        tp = _mat_ptr(table, "table", index, _I32, n_seq)
+        kp = _vec_ptr(kv_len, "kv_len", index, _I32, n_seq)
         pg, width = ctypes.addressof(pages), table.shape[1]
     O = _out(O, Q, index, stream)
     lp = _lse_ptr(lse, n, h, index)
@@ -568,10 +558,10 @@ def qwm_cross_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu: t
     vp, ldv = _rows_ptr(V, "V", index, hk, d)
     if V.shape[0] != n_kv:
         raise ValueError("K and V differ in rows")
-    cup = _ints_ptr(cu, "cu", index, None)
+    cup = _vec_ptr(cu, "cu", index, _I32)
     n_seq = cu.shape[0] - 1
-    sp = _ints_ptr(kv_start, "kv_start", index, n_seq)
-    lnp = _ints_ptr(kv_len, "kv_len", index, n_seq)
+    sp = _vec_ptr(kv_start, "kv_start", index, _I32, n_seq)
+    lnp = _vec_ptr(kv_len, "kv_len", index, _I32, n_seq)
     O = _out(O, Q, index, stream)
     lp = _lse_ptr(lse, n, h, index)
     ws, wp, wn = _scratch(workspace, lambda: qwm_cross_attention_workspace(h, hk, d, n, n_seq, max_q, max_kv),
