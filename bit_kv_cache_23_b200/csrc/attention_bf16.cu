@@ -47,25 +47,29 @@ __device__ int g_flash_fault;  // a length, offset or page number was clamped
 
 constexpr int KT = 64;           // keys per tile
 constexpr int QT = 128;          // query rows per Q tile (TMEM lanes)
-constexpr int ROWS = 2 * QT;     // query rows per CTA
-constexpr int NTHREADS = 352;
-constexpr int W_LOAD = 8, W_MMA = 9;
 
-template <int D>
+// NG: groups per CTA.  Two, of a Q tile each, read every K and V tile once for 256
+// rows, which long key ranges need (at 128 rows the L2 cache would have to deliver
+// 16 TB/s); with one, two CTAs share an SM, and one's beginning and end hide
+// behind the other.
+template <int D, int NG>
 struct Lay {
+  static constexpr int ROWS = NG * QT;            // query rows per CTA
+  static constexpr int W_LOAD = 4 * NG, W_MMA = W_LOAD + 1, NTHREADS = 32 * (W_MMA + NG);
+  static constexpr uint32_t COLS = NG * 256;      // TMEM: [group][2] S, then [group] O
   static constexpr uint32_t Q_TILE = QT * D * 2;  // [D / 64 column blocks][128 rows][128 B]
   static constexpr uint32_t ENT = KT * D * 2;     // one K or V tile, [D / 64][64 rows][128 B]
   // Ring entries (K, V, K, V, ...), of an even number of tiles: when the groups
   // take even and odd tiles, each slot then serves one group, which sees every
   // phase of the slot's barrier.  (Copies land out of order; a group that waits
   // for a slot's next phase but one finds the parity of the phase before.)
-  static constexpr int NST = D == 128 ? 8 : 16;
+  static constexpr int NST = NG * (D == 128 ? 4 : 8);
   static_assert(NST % 4 == 0, "an even number of K and V tiles");
-  static constexpr uint32_t OFF_KV = 2 * Q_TILE;
+  static constexpr uint32_t OFF_KV = NG * Q_TILE;
   static constexpr uint32_t OFF_BAR = OFF_KV + NST * ENT;
   static constexpr int B_FULL = 0,        // loader -> MMA
                        B_EMPTY = NST,     // MMA commits -> loader
-                       B_Q = 2 * NST,     // softmax warps: Q is in shared memory
+                       B_Q = 2 * NST,     // Q is in shared memory
                        B_S = B_Q + 1,     // [group][buffer] commit of Q K^T -> softmax
                        B_P = B_S + 4,     // [group][buffer] softmax -> MMA
                        B_PV = B_P + 4,    // [group] commit of P V -> softmax
@@ -77,7 +81,8 @@ struct Lay {
   static constexpr uint32_t OFF_LSE = OFF_BAR + NBAR * 8 + 16;
   static constexpr uint32_t SMEM = OFF_LSE + QT * 4 + 1024;
 };
-static_assert(Lay<128>::SMEM <= 227 * 1024 && Lay<64>::SMEM <= 227 * 1024, "shared memory");
+static_assert(Lay<128, 2>::SMEM <= 227 * 1024 && Lay<64, 2>::SMEM <= 227 * 1024, "shared memory");
+static_assert(Lay<128, 1>::SMEM <= 113 * 1024 && Lay<64, 1>::SMEM <= 113 * 1024, "shared memory");
 
 enum { OWN_NONE = 0, OWN_ROWS = 1, OWN_PAGES = 2 };
 
@@ -105,7 +110,8 @@ struct FlashArgs {
   int o32;             // O is 32-byte aligned
   int part0;           // first partial of this launch; -1: no partials
   float *ws_o, *ws_l;  // [partial][nq][Hq][D], [partial][nq][Hq]
-  CUtensorMap k0, v0, k1, v1;
+  int qtma;            // Q rows come through the map (g divides 128)
+  CUtensorMap q, k0, v0, k1, v1;
 };
 
 // What one CTA does: rows r0 .. r0 + nr - 1 of sequence b (a row is a token
@@ -139,7 +145,9 @@ struct Work {
   }
 };
 
+template <int NG>
 __device__ __forceinline__ bool work_of(const FlashArgs& A, Work& w) {
+  constexpr int ROWS = NG * QT;
   const int split = A.nsplit == 1 ? 0 : blockIdx.x / A.qblocks, qb = blockIdx.x - split * A.qblocks;
   w.h = A.head0 + blockIdx.y;
   w.b = blockIdx.z;
@@ -188,7 +196,7 @@ __device__ __forceinline__ bool work_of(const FlashArgs& A, Work& w) {
     w.j0 = split * each + (split < more ? split : more);
     w.n = each + (split < more);
   }
-  w.parity = w.nr <= QT && w.n > 1;
+  w.parity = NG == 2 && w.nr <= QT && w.n > 1;
   w.groups = w.nr > QT || w.parity ? 2 : 1;
   return true;
 }
@@ -326,14 +334,14 @@ __device__ __forceinline__ void store_row(const FlashArgs& A, const Work& w, boo
   }
 }
 
-template <int D>
+template <int D, int NG>
 __device__ __forceinline__ void softmax_role(const FlashArgs& A, uint8_t* smem, uint64_t* bars,
                                              uint32_t tmem, const Work& w) {
-  using L = Lay<D>;
+  using L = Lay<D, NG>;
   const int warp = threadIdx.x >> 5, p = warp >> 2, lane = threadIdx.x & 127;
-  {  // Q rows into shared memory, zeros behind the last; eight loads in flight
-    constexpr int C = D / 8, STEP = 256 / C;
-    const int c = threadIdx.x % C, r1 = w.nr > QT ? ROWS : QT;
+  if (!A.qtma) {  // Q rows into shared memory, zeros behind the last; eight loads in flight
+    constexpr int C = D / 8, STEP = 32 * L::W_LOAD / C;
+    const int c = threadIdx.x % C, r1 = w.nr > QT ? L::ROWS : QT;
     for (int rr0 = threadIdx.x / C; rr0 < r1; rr0 += 8 * STEP) {
       uint4 v[8];
 #pragma unroll
@@ -367,7 +375,7 @@ __device__ __forceinline__ void softmax_role(const FlashArgs& A, uint8_t* smem, 
   if (cut0 == 0) cut0 = KT;
   const int whole = w.nt0 + __reduce_min_sync(0xffffffffu, seen) / KT;
   const uint32_t lane0 = (uint32_t)(32 * (warp & 3)) << 16;
-  const uint32_t ts0 = tmem + lane0 + 128 * p, to = tmem + lane0 + 256 + 128 * p;
+  const uint32_t ts0 = tmem + lane0 + 128 * p, to = tmem + lane0 + 128 * (NG + p);
   float m_used = -INFINITY;
   uint64_t l2[2] = {0, 0};  // running row sum, as pairs of partial sums
   const uint64_t sc2 = f2pack(A.scale_log2, A.scale_log2);
@@ -503,14 +511,28 @@ __device__ __forceinline__ void issue_tile(const FlashArgs& A, const Work& w, in
 }
 
 // One warp; entry 2t holds K of tile t, entry 2t + 1 its V.
-template <int D>
+template <int D, int NG>
 __device__ __forceinline__ void load_role(const FlashArgs& A, uint8_t* smem, uint64_t* bars,
                                           const Work& w) {
-  using L = Lay<D>;
+  using L = Lay<D, NG>;
   const int lane = threadIdx.x & 31;
   const uint32_t base = smem_u32(smem);
   bool ok = true;
   int rag = 0, e = 0;
+  if (A.qtma) {
+    // boxes of 64 channels, the key head's g query heads and 128 / g tokens; rows of
+    // no row of this CTA are computed with and not stored
+    if (lane == 0) {
+      const int tiles = w.nr > QT ? 2 : 1;
+      mbar_arrive_expect_tx(&bars[L::B_Q], tiles * L::Q_TILE);
+      for (int p = 0; p < tiles; ++p)
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_3d(base + p * L::Q_TILE + c * (QT * 128), &A.q, 64 * c, w.h * A.g,
+                      (int)w.tok0 + w.token(A, w.r0 + p * QT), &bars[L::B_Q]);
+    }
+    __syncwarp();
+  }
   for (; e < 2 * w.n; ++e) {
     const int slot = e % L::NST;
     if (e >= L::NST && !warp_wait(&bars[L::B_EMPTY + slot], ((e / L::NST) - 1) & 1)) {
@@ -539,6 +561,7 @@ __device__ __forceinline__ void load_role(const FlashArgs& A, uint8_t* smem, uin
     }
   }
   // every box issued has landed before the CTA may exit
+  if (A.qtma && !warp_wait(&bars[L::B_Q], 0)) ok = false;
   for (int k = e > L::NST ? e - L::NST : 0; k < e; ++k)
     if (!warp_wait(&bars[L::B_FULL + k % L::NST], (k / L::NST) & 1)) ok = false;
   if (!ok && lane == 0) timeout_flag();
@@ -548,10 +571,10 @@ __device__ __forceinline__ void load_role(const FlashArgs& A, uint8_t* smem, uin
 // One thread per group: two tiles' S = Q K^T ahead, then for each tile O += P V
 // and S of the tile after the next, into the buffer that P occupied (the tensor
 // core works in issue order).  A commit tells when all before it is complete.
-template <int D>
+template <int D, int NG>
 __device__ __forceinline__ void mma_role(uint8_t* smem, uint64_t* bars, uint32_t tmem,
                                          const Work& w, int p) {
-  using L = Lay<D>;
+  using L = Lay<D, NG>;
   constexpr uint32_t IDQ = idesc_bf16(QT, KT, false, false);
   constexpr uint32_t IDP = idesc_bf16(QT, D, false, true);
   const uint32_t base = smem_u32(smem);
@@ -559,7 +582,7 @@ __device__ __forceinline__ void mma_role(uint8_t* smem, uint64_t* bars, uint32_t
   const uint64_t kd = desc_sw128(base + L::OFF_KV, 16, 1024);
   // V: channels are the contiguous dimension; its 64-channel blocks lie KT * 128 bytes apart
   const uint64_t vd = desc_sw128(base + L::OFF_KV, KT * 128, 1024);
-  const uint32_t ts0 = tmem + 128 * p, to = tmem + 256 + 128 * p;
+  const uint32_t ts0 = tmem + 128 * p, to = tmem + 128 * (NG + p);
   const int step = 1 + w.parity;
   auto full = [&](int e) { return mbar_wait(&bars[L::B_FULL + e % L::NST], (e / L::NST) & 1); };
   auto scores = [&](int t, int i) {  // S of tile t, the group's i-th
@@ -598,15 +621,16 @@ __device__ __forceinline__ void mma_role(uint8_t* smem, uint64_t* bars, uint32_t
   if (!ok) timeout_flag();
 }
 
-template <int D>
-__global__ void __launch_bounds__(NTHREADS, 1) flash_kernel(const __grid_constant__ FlashArgs A) {
-  using L = Lay<D>;
+template <int D, int NG>
+__global__ void __launch_bounds__(Lay<D, NG>::NTHREADS, 3 - NG)
+    flash_kernel(const __grid_constant__ FlashArgs A) {
+  using L = Lay<D, NG>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Work w;
-  if (!work_of(A, w)) return;
+  if (!work_of<NG>(A, w)) return;
   if (w.n == 0) {  // no keys in this range
     const int rr = threadIdx.x;
-    for (int e = rr; e < w.nr * (D / 8); e += NTHREADS) {
+    for (int e = rr; e < w.nr * (D / 8); e += L::NTHREADS) {
       const int64_t row = out_row(A, w, w.r0 + e / (D / 8));
       const int c = e % (D / 8);
       if (A.part0 >= 0) {
@@ -630,7 +654,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) flash_kernel(const __grid_constan
       mbar_init(&bars[L::B_FULL + i], 1);
       mbar_init(&bars[L::B_EMPTY + i], w.parity ? 1 : w.groups);
     }
-    mbar_init(&bars[L::B_Q], 8);
+    mbar_init(&bars[L::B_Q], A.qtma ? 1 : L::W_LOAD);
     for (int i = 0; i < 2; ++i) {
       const int warps = i < w.groups ? (w.rows_of(i) + 31) / 32 : 1;
       for (int b = 0; b < 2; ++b) {
@@ -645,28 +669,28 @@ __global__ void __launch_bounds__(NTHREADS, 1) flash_kernel(const __grid_constan
     mbar_init(&bars[L::B_RAG], 1);
     fence_mbar_init();
   }
-  if (warp == W_MMA) {
-    tmem_alloc(holder, 512);
+  if (warp == L::W_MMA) {
+    tmem_alloc(holder, L::COLS);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *holder;
-  if (warp < W_LOAD) {
-    softmax_role<D>(A, smem, bars, tmem, w);
-  } else if (warp < W_MMA) {
-    load_role<D>(A, smem, bars, w);
+  if (warp < L::W_LOAD) {
+    softmax_role<D, NG>(A, smem, bars, tmem, w);
+  } else if (warp < L::W_MMA) {
+    load_role<D, NG>(A, smem, bars, w);
   } else {
-    const int p = warp - W_MMA;
-    if ((threadIdx.x & 31) == 0 && p < w.groups) mma_role<D>(smem, bars, tmem, w, p);
+    const int p = warp - L::W_MMA;
+    if ((threadIdx.x & 31) == 0 && p < w.groups) mma_role<D, NG>(smem, bars, tmem, w, p);
     __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == W_MMA) {
+  if (warp == L::W_MMA) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, L::COLS);
   }
 }
 
@@ -858,20 +882,34 @@ int device_sms() {
   return cache[dev];
 }
 
-// Key ranges for `units` CTAs over `ntile` tiles each: the count that minimizes
-// (rounds of CTAs on the GPU) x (tiles per range + a fixed cost of 8 tiles).
-int choose_split(int64_t units, int64_t ntile, int most) {
-  const int64_t slots = device_sms();
-  int best = 1;
+// How a launch divides its work: groups per CTA, row blocks per sequence, key
+// ranges per row block.
+struct Blocks {
+  int ng, qblocks, nsplit;
+};
+
+// rows: of a sequence; units: sequences times key heads; ntile: key tiles; most:
+// key ranges at most.  The key ranges are the count that minimizes (rounds of CTAs
+// on the GPU) x (tiles per range + a fixed cost of FIX tiles).
+Blocks blocks_of(int64_t rows, int64_t units, int64_t ntile, int most) {
+  Blocks b;
+#ifdef NGF
+  b.ng = NGF;
+#else
+  b.ng = ntile >= 40 && rows > QT ? 2 : 1;
+#endif
+  b.qblocks = (int)((rows + b.ng * QT - 1) / (b.ng * QT));
+  const int64_t ctas = units * b.qblocks, slots = (int64_t)device_sms() * (3 - b.ng);
+  b.nsplit = 1;
   double bestc = 1e300;
   for (int s = 1; s <= most && s * 4 <= (ntile > 4 ? ntile : 4); ++s) {
-    const double c = (double)((units * s + slots - 1) / slots) * ((double)ntile / s + 8.0);
+    const double c = (double)((ctas * s + slots - 1) / slots) * ((double)ntile / s + 8.0);
     if (c < bestc * 0.98) {
       bestc = c;
-      best = s;
+      b.nsplit = s;
     }
   }
-  return best;
+  return b;
 }
 
 // The driver's encoder of tensor maps (no link to the driver library).
@@ -907,18 +945,28 @@ bool map_3d(CUtensorMap* m, const void* base, int D, int64_t n1, int64_t ld1, in
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+// Q's map, where whole tokens make up a Q tile.
+bool map_q(FlashArgs& a, int D) {
+  a.qtma = QT % a.g == 0;
+  return !a.qtma || map_3d(&a.q, a.Q, D, a.Hq, D, a.nq, a.ldq, a.g, QT / a.g);
+}
+
+template <int D, int NG>
 cudaError_t launch_flash(const FlashArgs& a, int heads, int64_t n_seq, cudaStream_t s) {
+  using L = Lay<D, NG>;
   static std::atomic<uint64_t> allowed{0};
-  const cudaError_t e = allow_smem(flash_kernel<D>, allowed, (int)Lay<D>::SMEM);
+  const cudaError_t e = allow_smem(flash_kernel<D, NG>, allowed, (int)L::SMEM);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((int64_t)a.qblocks * a.nsplit), (unsigned)heads, (unsigned)n_seq);
-  flash_kernel<D><<<grid, NTHREADS, Lay<D>::SMEM, s>>>(a);
+  flash_kernel<D, NG><<<grid, L::NTHREADS, L::SMEM, s>>>(a);
   return cudaGetLastError();
 }
 
-cudaError_t launch_flash(int D, const FlashArgs& a, int heads, int64_t n_seq, cudaStream_t s) {
-  return D == 128 ? launch_flash<128>(a, heads, n_seq, s) : launch_flash<64>(a, heads, n_seq, s);
+cudaError_t launch_flash(int D, const FlashArgs& a, const Blocks& b, int heads, int64_t n_seq,
+                         cudaStream_t s) {
+  if (D == 128)
+    return b.ng == 2 ? launch_flash<128, 2>(a, heads, n_seq, s) : launch_flash<128, 1>(a, heads, n_seq, s);
+  return b.ng == 2 ? launch_flash<64, 2>(a, heads, n_seq, s) : launch_flash<64, 1>(a, heads, n_seq, s);
 }
 
 cudaError_t launch_merge(int D, const FlashArgs& a, int np, const int32_t* cu, int64_t n_seq,
@@ -979,7 +1027,7 @@ SharedPlan plan_shared(const Dims& D, int64_t T, int Hq, int64_t n_q, int64_t n_
 }
 
 bool lengths_ok(int64_t n_q, int g, int64_t n_seq, int64_t max_q, int64_t max_kv) {
-  return n_q >= 0 && n_q * g <= kMaxGridX - ROWS && n_seq >= 1 && n_seq <= 65535 && max_q >= 0 &&
+  return n_q >= 0 && n_q * g <= kMaxGridX - 2 * QT && n_seq >= 1 && n_seq <= 65535 && max_q >= 0 &&
          max_q <= kMaxGridX && max_kv >= 0 && max_kv <= kMaxGridX - KT;
 }
 
@@ -1067,6 +1115,7 @@ extern "C" qwm_status qwm_attention_shared(const qwm_cache* c, const void* Q, in
   a.lse = lse;
   a.ws_o = (float*)workspace;
   a.ws_l = a.ws_o + (size_t)plan.np * n_q * heads_q * D.d;
+  if (!map_q(a, D.d)) return QWM_ERR_CUDA;
   uint8_t* scratch = (uint8_t*)workspace + partial_bytes(plan.np, n_q, heads_q, D.d);
   // the branches' own keys
   FlashArgs own = a;
@@ -1088,7 +1137,6 @@ extern "C" qwm_status qwm_attention_shared(const qwm_cache* c, const void* Q, in
     own.shift = page_shift(pages);
     own.pool_heads = pages->heads;
   }
-  own.qblocks = (int)((mq * g + ROWS - 1) / ROWS);
   // heads per pass: what the workspace holds unpacked
   const uint64_t head = plan.rows ? 0 : (uint64_t)T * D.d * 4;
   int hp = D.H;
@@ -1101,28 +1149,32 @@ extern "C" qwm_status qwm_attention_shared(const qwm_cache* c, const void* Q, in
   hp = (D.H + passes - 1) / passes;
   const int64_t tiles0 = (T + KT - 1) / KT, tiles1 = (max_kv + KT - 1) / KT;
   int np = 0;
+  Blocks ba = {}, bo = {};
+  const auto set = [](FlashArgs& f, const Blocks& b) {
+    f.qblocks = b.qblocks;
+    f.nsplit = b.nsplit;
+  };
   if (plan.joined) {
-    const int ns = plan.np < 2 ? 1
-                               : choose_split((int64_t)own.qblocks * hp * n_seq, tiles0 + tiles1, plan.np);
-    own.nsplit = ns;
-    own.part0 = ns > 1 ? 0 : -1;
-    np = ns > 1 ? ns : 0;
+    bo = blocks_of(mq * g, hp * n_seq, tiles0 + tiles1, plan.np < 2 ? 1 : plan.np);
+    set(own, bo);
+    own.part0 = bo.nsplit > 1 ? 0 : -1;
+    np = bo.nsplit > 1 ? bo.nsplit : 0;
   } else {
-    const int ns1 = pages && max_kv > 0 ? choose_split((int64_t)own.qblocks * D.H * n_seq, tiles1, plan.np / 2) : 0;
+    if (pages && max_kv > 0) bo = blocks_of(mq * g, D.H * n_seq, tiles1, plan.np / 2);
+    set(own, bo);
     if (plan.rows) {
-      const RowsPlan rp = rows_plan(D, T, device_sms(), plan.np - ns1);
+      const RowsPlan rp = rows_plan(D, T, device_sms(), plan.np - bo.nsplit);
       a.nsplit = rp.slots;
       if (launch_rows(D, v, T, a.Q, ldq, n_q, heads_q, a.scale_log2, rp, a.ws_o, a.ws_l, s) != cudaSuccess)
         return QWM_ERR_CUDA;
     } else {
-      a.qblocks = (int)((n_q * g + ROWS - 1) / ROWS);
       a.max_q = n_q;
-      a.nsplit = choose_split((int64_t)a.qblocks * hp, tiles0, plan.np - ns1);
+      ba = blocks_of(n_q * g, hp, tiles0, plan.np - bo.nsplit);
+      set(a, ba);
     }
     a.part0 = 0;
     own.part0 = a.nsplit;
-    own.nsplit = ns1;
-    np = a.nsplit + ns1;
+    np = a.nsplit + bo.nsplit;
   }
   FlashArgs& with0 = plan.joined ? own : a;
   for (int h0 = 0; h0 < D.H && !plan.rows; h0 += hp) {
@@ -1137,9 +1189,9 @@ extern "C" qwm_status qwm_attention_shared(const qwm_cache* c, const void* Q, in
         return QWM_ERR_CUDA;
     }
     with0.head0 = h0;
-    if (launch_flash(D.d, with0, nh, plan.joined ? n_seq : 1, s) != cudaSuccess) return QWM_ERR_CUDA;
+    if (launch_flash(D.d, with0, plan.joined ? bo : ba, nh, plan.joined ? n_seq : 1, s) != cudaSuccess) return QWM_ERR_CUDA;
   }
-  if (!plan.joined && own.nsplit > 0 && launch_flash(D.d, own, D.H, n_seq, s) != cudaSuccess)
+  if (!plan.joined && own.nsplit > 0 && launch_flash(D.d, own, bo, D.H, n_seq, s) != cudaSuccess)
     return QWM_ERR_CUDA;
   if (np > 0 && launch_merge(D.d, a, np, cu, n_seq, max_q, s) != cudaSuccess) return QWM_ERR_CUDA;
   return QWM_OK;
@@ -1154,8 +1206,9 @@ extern "C" qwm_status qwm_cross_attention_workspace(int32_t heads_q, int32_t hea
       !lengths_ok(n_q, heads_q / heads_kv, n_seq, max_q, max_kv))
     return QWM_ERR_INVALID_ARG;
   const int64_t mq = max_q < n_q ? max_q : n_q;
-  const int64_t units = (mq * (heads_q / heads_kv) + ROWS - 1) / ROWS * heads_kv * n_seq;
-  const int np = choose_split(units, (max_kv + KT - 1) / KT, partials_of(n_q, heads_q, head_dim));
+  const int np = blocks_of(mq * (heads_q / heads_kv), heads_kv * n_seq, (max_kv + KT - 1) / KT,
+                           partials_of(n_q, heads_q, head_dim))
+                     .nsplit;
   *least = 0;
   *full = np > 1 ? partial_bytes(np, n_q, heads_q, head_dim) : 0;
   return QWM_OK;
@@ -1189,6 +1242,7 @@ extern "C" qwm_status qwm_cross_attention(const void* Q, int64_t ldq, int64_t n_
   a.nq = n_q;
   a.Hq = heads_q;
   a.g = g;
+  if (!map_q(a, head_dim)) return QWM_ERR_CUDA;
   a.cu = cu;
   a.max_q = max_q;
   a.own = OWN_ROWS;
@@ -1204,19 +1258,19 @@ extern "C" qwm_status qwm_cross_attention(const void* Q, int64_t ldq, int64_t n_
   a.O = (uint16_t*)O;
   a.o32 = aligned_to(O, 32);
   a.lse = lse;
-  a.qblocks = (int)((mq * g + ROWS - 1) / ROWS);
-  a.nsplit = 1;
+  const bool parts = full > 0 && workspace && workspace_bytes >= full;
+  const Blocks b = blocks_of(mq * g, heads_kv * n_seq, (max_kv + KT - 1) / KT,
+                             parts ? partials_of(n_q, heads_q, head_dim) : 1);
+  a.qblocks = b.qblocks;
+  a.nsplit = b.nsplit;
   a.part0 = -1;
-  if (full > 0 && workspace && workspace_bytes >= full) {
-    const int np = choose_split((int64_t)a.qblocks * heads_kv * n_seq, (max_kv + KT - 1) / KT,
-                                partials_of(n_q, heads_q, head_dim));
-    a.nsplit = np;
+  if (parts) {
     a.part0 = 0;
     a.ws_o = (float*)workspace;
-    a.ws_l = a.ws_o + (size_t)np * n_q * heads_q * head_dim;
+    a.ws_l = a.ws_o + (size_t)b.nsplit * n_q * heads_q * head_dim;
   }
   const cudaStream_t s = (cudaStream_t)stream;
-  if (launch_flash(head_dim, a, heads_kv, n_seq, s) != cudaSuccess) return QWM_ERR_CUDA;
+  if (launch_flash(head_dim, a, b, heads_kv, n_seq, s) != cudaSuccess) return QWM_ERR_CUDA;
   if (a.nsplit > 1 && launch_merge(head_dim, a, a.nsplit, cu, n_seq, max_q, s) != cudaSuccess)
     return QWM_ERR_CUDA;
   return QWM_OK;
