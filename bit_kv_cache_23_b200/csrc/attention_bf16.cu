@@ -8,20 +8,20 @@
 //   S = Q K^T,  m = running row maximum,  P = 2^(scale log2e S - m),
 //   l = sum P,  O = sum P V,  out = O / l,  lse = ln 2 (m + log2 l).
 //
-// One CTA serves up to 256 query rows of one key head (two 128-row Q tiles; the
-// query heads that share the key head are rows too) over a range of 64-key
-// tiles; nothing but Q, K, V and the result crosses HBM.  With too few row
-// blocks to fill the GPU the key range is split; each range gives a normalized
-// fp32 partial and its log-sum-exp, which a last kernel merges.
+// One CTA serves up to 128 query rows of one key head (the query heads that share
+// the key head are rows too) over a range of 64-key tiles; nothing but Q, K, V and
+// the result crosses HBM.  With too few row blocks to fill the GPU the key range is
+// split; each range gives a normalized fp32 partial and its log-sum-exp, which a
+// last kernel merges.
 //
-// 352 threads: warps 0-7 softmax (one row per thread; warpgroup p serves group
-// p), warp 8 the loader, warps 9 and 10 one issuing thread per group.  A group
-// is one of the two Q tiles or, when there is only one, its even or its odd key
-// tiles (joined at the end through shared memory).  Each group has two score
-// buffers in TMEM, so that Q K^T of the next tiles runs while the softmax works
-// on this one, and neither softmax group ever waits for a product it has just
-// asked for: with one buffer of 128 keys both groups waited together and then
-// shared the exponential unit, 5000 clocks per 128 keys of 256 rows.
+// 192 threads: warps 0-3 softmax (one row per thread), warp 4 the loader, warp 5
+// the issuing thread.  Two score buffers in TMEM let Q K^T of the next tiles run
+// while the softmax works on this one.  Two CTAs share an SM: one's products run
+// while the other has the exponential unit, and one's beginning and end hide
+// behind the other's tiles.  (One CTA of 256 rows, with each K and V tile read
+// once for two such groups, took 8 to 18 % longer up to 2048 keys, the same at
+// 4096, and 5 % less at 8192: the groups fall into step, both waiting for
+// products and then both for the exponential unit.)
 //
 // K and V tiles go through one ring of TMA boxes in the 128-byte-swizzled layout
 // that the MMA descriptors read (one box per 64 channels and, for pages, per
@@ -48,41 +48,28 @@ __device__ int g_flash_fault;  // a length, offset or page number was clamped
 constexpr int KT = 64;           // keys per tile
 constexpr int QT = 128;          // query rows per Q tile (TMEM lanes)
 
-// NG: groups per CTA.  Two, of a Q tile each, read every K and V tile once for 256
-// rows, which long key ranges need (at 128 rows the L2 cache would have to deliver
-// 16 TB/s); with one, two CTAs share an SM, and one's beginning and end hide
-// behind the other.
-template <int D, int NG>
+constexpr int W_LOAD = 4, W_MMA = 5, NTHREADS = 192;
+constexpr uint32_t COLS = 256;   // TMEM: S, S, O
+
+template <int D>
 struct Lay {
-  static constexpr int ROWS = NG * QT;            // query rows per CTA
-  static constexpr int W_LOAD = 4 * NG, W_MMA = W_LOAD + 1, NTHREADS = 32 * (W_MMA + NG);
-  static constexpr uint32_t COLS = NG * 256;      // TMEM: [group][2] S, then [group] O
   static constexpr uint32_t Q_TILE = QT * D * 2;  // [D / 64 column blocks][128 rows][128 B]
   static constexpr uint32_t ENT = KT * D * 2;     // one K or V tile, [D / 64][64 rows][128 B]
-  // Ring entries (K, V, K, V, ...), of an even number of tiles: when the groups
-  // take even and odd tiles, each slot then serves one group, which sees every
-  // phase of the slot's barrier.  (Copies land out of order; a group that waits
-  // for a slot's next phase but one finds the parity of the phase before.)
-  static constexpr int NST = NG * (D == 128 ? 4 : 8);
-  static_assert(NST % 4 == 0, "an even number of K and V tiles");
-  static constexpr uint32_t OFF_KV = NG * Q_TILE;
+  static constexpr int NST = D == 128 ? 4 : 8;    // ring entries (K, V, K, V, ...)
+  static constexpr uint32_t OFF_KV = Q_TILE;
   static constexpr uint32_t OFF_BAR = OFF_KV + NST * ENT;
   static constexpr int B_FULL = 0,        // loader -> MMA
                        B_EMPTY = NST,     // MMA commits -> loader
                        B_Q = 2 * NST,     // Q is in shared memory
-                       B_S = B_Q + 1,     // [group][buffer] commit of Q K^T -> softmax
-                       B_P = B_S + 4,     // [group][buffer] softmax -> MMA
-                       B_PV = B_P + 4,    // [group] commit of P V -> softmax
-                       B_O = B_PV + 2,    // [group] commit of the last P V -> softmax
-                       B_DONE = B_O + 2,  // [group] drain before exit
-                       B_M = B_DONE + 2,  // odd tiles' result in shared memory
-                       B_RAG = B_M + 1,   // a ragged V tile has landed -> loader
+                       B_S = B_Q + 1,     // [buffer] commit of Q K^T -> softmax
+                       B_P = B_S + 2,     // [buffer] softmax -> MMA
+                       B_PV = B_P + 2,    // commit of P V -> softmax
+                       B_DONE = B_PV + 1, // drain before exit
+                       B_RAG = B_DONE + 1,  // a ragged V tile has landed -> loader
                        NBAR = B_RAG + 1;
-  static constexpr uint32_t OFF_LSE = OFF_BAR + NBAR * 8 + 16;
-  static constexpr uint32_t SMEM = OFF_LSE + QT * 4 + 1024;
+  static constexpr uint32_t SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
 };
-static_assert(Lay<128, 2>::SMEM <= 227 * 1024 && Lay<64, 2>::SMEM <= 227 * 1024, "shared memory");
-static_assert(Lay<128, 1>::SMEM <= 113 * 1024 && Lay<64, 1>::SMEM <= 113 * 1024, "shared memory");
+static_assert(Lay<128>::SMEM <= 113 * 1024 && Lay<64>::SMEM <= 113 * 1024, "two CTAs per SM");
 
 enum { OWN_NONE = 0, OWN_ROWS = 1, OWN_PAGES = 2 };
 
@@ -121,8 +108,6 @@ struct Work {
   int nb;          // its tokens
   int r0;
   int nr;          // rows of this CTA
-  int parity;      // 1: one Q tile; the groups take its even and odd key tiles
-  int groups;      // active groups (softmax warpgroup and issuing thread)
   int h;
   int len1;        // own keys
   int start1;      // first own row (OWN_ROWS)
@@ -138,16 +123,9 @@ struct Work {
     const int x = len1 - nb + token(A, r) + 1;
     return x < 0 ? 0 : x > len1 ? len1 : x;
   }
-  // rows in group p's Q tile
-  __device__ __forceinline__ int rows_of(int p) const {
-    const int left = nr - (parity ? 0 : p * QT);
-    return left < QT ? left : QT;
-  }
 };
 
-template <int NG>
 __device__ __forceinline__ bool work_of(const FlashArgs& A, Work& w) {
-  constexpr int ROWS = NG * QT;
   const int split = A.nsplit == 1 ? 0 : blockIdx.x / A.qblocks, qb = blockIdx.x - split * A.qblocks;
   w.h = A.head0 + blockIdx.y;
   w.b = blockIdx.z;
@@ -167,7 +145,7 @@ __device__ __forceinline__ bool work_of(const FlashArgs& A, Work& w) {
   }
   // (the host refuses more than 2^31 - 1 rows, keys or pages' places)
   const int rows = (w.nb < A.max_q ? w.nb : (int)A.max_q) * A.g;
-  w.r0 = qb * ROWS;
+  w.r0 = qb * QT;
   w.len1 = 0;
   w.start1 = 0;
   if (A.own != OWN_NONE) {
@@ -185,7 +163,7 @@ __device__ __forceinline__ bool work_of(const FlashArgs& A, Work& w) {
   }
   if (fault && threadIdx.x == 0) atomicExch(&g_flash_fault, 1);
   if (w.r0 >= rows) return false;
-  w.nr = rows - w.r0 < ROWS ? rows - w.r0 : ROWS;
+  w.nr = rows - w.r0 < QT ? rows - w.r0 : QT;
   const int seen = A.causal ? w.seen(A, w.r0 + w.nr - 1) : w.len1;  // own keys that the last row sees
   w.nt0 = (int)((A.len0 + KT - 1) / KT);
   const int nt = w.nt0 + (seen + KT - 1) / KT;
@@ -196,8 +174,6 @@ __device__ __forceinline__ bool work_of(const FlashArgs& A, Work& w) {
     w.j0 = split * each + (split < more ? split : more);
     w.n = each + (split < more);
   }
-  w.parity = NG == 2 && w.nr <= QT && w.n > 1;
-  w.groups = w.nr > QT || w.parity ? 2 : 1;
   return true;
 }
 
@@ -279,12 +255,10 @@ __device__ __forceinline__ void store32(void* dst, uint32_t a, uint32_t b, uint3
                : "memory");
 }
 
-// One row of O from TMEM, times `inv` (plus, where `more` is set, `w1` times the
-// other group's row in shared memory), to O or to this CTA's partial.
+// One row of O from TMEM, times `inv`, to O or to this CTA's partial.
 template <int D>
 __device__ __forceinline__ void store_row(const FlashArgs& A, const Work& w, bool valid, int64_t row,
-                                          uint32_t to, float inv, float lse, const float4* more,
-                                          int swz, float w1) {
+                                          uint32_t to, float inv, float lse) {
   const size_t at = A.part0 >= 0 ? (size_t)w.part * A.nq * A.Hq + row : (size_t)row;
   if (valid) {
     if (A.part0 >= 0) A.ws_l[at] = lse;
@@ -296,16 +270,6 @@ __device__ __forceinline__ void store_row(const FlashArgs& A, const Work& w, boo
     tmem_ld32(to + c * 32, o);
 #pragma unroll
     for (int e = 0; e < 32; ++e) o[e] *= inv;
-    if (more) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float4 x = more[(8 * c + k) ^ swz];
-        o[4 * k] = fmaf(w1, x.x, o[4 * k]);
-        o[4 * k + 1] = fmaf(w1, x.y, o[4 * k + 1]);
-        o[4 * k + 2] = fmaf(w1, x.z, o[4 * k + 2]);
-        o[4 * k + 3] = fmaf(w1, x.w, o[4 * k + 3]);
-      }
-    }
     if (!valid) continue;
     if (A.part0 >= 0) {
       float* dst = A.ws_o + at * D + 32 * c;
@@ -334,15 +298,15 @@ __device__ __forceinline__ void store_row(const FlashArgs& A, const Work& w, boo
   }
 }
 
-template <int D, int NG>
+template <int D>
 __device__ __forceinline__ void softmax_role(const FlashArgs& A, uint8_t* smem, uint64_t* bars,
                                              uint32_t tmem, const Work& w) {
-  using L = Lay<D, NG>;
-  const int warp = threadIdx.x >> 5, p = warp >> 2, lane = threadIdx.x & 127;
+  using L = Lay<D>;
+  const int warp = threadIdx.x >> 5;
   if (!A.qtma) {  // Q rows into shared memory, zeros behind the last; eight loads in flight
-    constexpr int C = D / 8, STEP = 32 * L::W_LOAD / C;
-    const int c = threadIdx.x % C, r1 = w.nr > QT ? L::ROWS : QT;
-    for (int rr0 = threadIdx.x / C; rr0 < r1; rr0 += 8 * STEP) {
+    constexpr int C = D / 8, STEP = QT / C;
+    const int c = threadIdx.x % C;
+    for (int rr0 = threadIdx.x / C; rr0 < QT; rr0 += 8 * STEP) {
       uint4 v[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
@@ -357,15 +321,14 @@ __device__ __forceinline__ void softmax_role(const FlashArgs& A, uint8_t* smem, 
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         const int rr = rr0 + u * STEP;
-        if (rr < r1)
-          *reinterpret_cast<uint4*>(smem + (rr / QT) * L::Q_TILE + sw128_off(rr % QT, c, QT)) = v[u];
+        if (rr < QT) *reinterpret_cast<uint4*>(smem + sw128_off(rr, c, QT)) = v[u];
       }
     }
     fence_proxy_async_smem();
     warp_arrive(&bars[L::B_Q]);
   }
-  if (p >= w.groups || 32 * (warp & 3) >= w.rows_of(p)) return;
-  const int rr = (w.parity ? 0 : p * QT) + lane;  // row in the CTA
+  if (32 * warp >= w.nr) return;
+  const int rr = threadIdx.x;  // row in the CTA and TMEM lane
   const bool valid = rr < w.nr;
   const int r = w.r0 + (valid ? rr : 0);
   const int seen = A.causal ? w.seen(A, r) : w.len1;  // own keys that this row sees
@@ -374,17 +337,15 @@ __device__ __forceinline__ void softmax_role(const FlashArgs& A, uint8_t* smem, 
   int cut0 = (int)(A.len0 % KT);
   if (cut0 == 0) cut0 = KT;
   const int whole = w.nt0 + __reduce_min_sync(0xffffffffu, seen) / KT;
-  const uint32_t lane0 = (uint32_t)(32 * (warp & 3)) << 16;
-  const uint32_t ts0 = tmem + lane0 + 128 * p, to = tmem + lane0 + 128 * (NG + p);
+  const uint32_t ts0 = tmem + ((uint32_t)(32 * warp) << 16), to = ts0 + 128;
   float m_used = -INFINITY;
   uint64_t l2[2] = {0, 0};  // running row sum, as pairs of partial sums
   const uint64_t sc2 = f2pack(A.scale_log2, A.scale_log2);
   bool ok = true;
-  int i = 0;
-  for (int t = w.parity ? p : 0; t < w.n; t += 1 + w.parity, ++i) {
-    const int j = w.j0 + t;
+  for (int i = 0; i < w.n; ++i) {
+    const int j = w.j0 + i;
     const uint32_t ts = ts0 + 64 * (i & 1);
-    if (!warp_wait(&bars[L::B_S + 2 * p + (i & 1)], (i >> 1) & 1)) { ok = false; break; }
+    if (!warp_wait(&bars[L::B_S + (i & 1)], (i >> 1) & 1)) { ok = false; break; }
     tc_fence_after();
     float s[64];
     tmem_ld64(ts, s);
@@ -400,7 +361,7 @@ __device__ __forceinline__ void softmax_role(const FlashArgs& A, uint8_t* smem, 
       m_used = m_row;
     } else if (__any_sync(0xffffffffu, need)) {
       // O is at rest once the last product with P is complete (this tile's waits for P)
-      if (!warp_wait(&bars[L::B_PV + p], (i - 1) & 1)) { ok = false; break; }
+      if (!warp_wait(&bars[L::B_PV], (i - 1) & 1)) { ok = false; break; }
       tc_fence_after();
       const float f = need ? ex2(m_used - m_row) : 1.0f;
 #pragma unroll 1
@@ -422,11 +383,9 @@ __device__ __forceinline__ void softmax_role(const FlashArgs& A, uint8_t* smem, 
     weights(s, sc2, nm2, l2, ts);
     tmem_wait_st();
     tc_fence_before();
-    warp_arrive(&bars[L::B_P + 2 * p + (i & 1)]);
+    warp_arrive(&bars[L::B_P + (i & 1)]);
   }
-  if (ok) ok = warp_wait(&bars[L::B_O + p], 0);
-  // the groups of a parity pair meet: shared memory is free once both are done
-  if (ok && w.parity) ok = warp_wait(&bars[L::B_O + 1 - p], 0);
+  if (ok) ok = warp_wait(&bars[L::B_PV], (w.n - 1) & 1);
   if (!ok) {
     if ((threadIdx.x & 31) == 0) timeout_flag();
     return;
@@ -435,40 +394,8 @@ __device__ __forceinline__ void softmax_role(const FlashArgs& A, uint8_t* smem, 
   float la, lb;
   f2unpack(fadd2(l2[0], l2[1]), la, lb);
   const float l = la + lb;
-  float inv = l > 0.0f ? 1.0f / l : 0.0f;
-  float lse = l > 0.0f ? (m_used + log2f(l)) * 0.6931471805599453f : -INFINITY;
-  const int swz = lane & (D / 4 - 1);  // spreads the rows over the banks
-  float4* mine = reinterpret_cast<float4*>(smem) + lane * (D / 4);
-  float* lses = reinterpret_cast<float*>(smem + L::OFF_LSE);
-  float w1 = 0.0f;
-  if (w.parity) {
-    if (p == 1) {
-#pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        float o[32];
-        tmem_ld32(to + c * 32, o);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mine[(8 * c + k) ^ swz] = make_float4(o[4 * k] * inv, o[4 * k + 1] * inv,
-                                                o[4 * k + 2] * inv, o[4 * k + 3] * inv);
-      }
-      lses[lane] = lse;
-      warp_arrive(&bars[L::B_M]);
-      return;
-    }
-    if (!warp_wait(&bars[L::B_M], 0)) {
-      if ((threadIdx.x & 31) == 0) timeout_flag();
-      return;
-    }
-    const float lse1 = lses[lane], top = fmaxf(lse, lse1);
-    if (top > -INFINITY) {
-      const float a = expf(lse - top), b = expf(lse1 - top), den = 1.0f / (a + b);
-      inv *= a * den;
-      w1 = b * den;
-      lse = top + logf(a + b);
-    }
-  }
-  store_row<D>(A, w, valid, out_row(A, w, r), to, inv, lse, w.parity ? mine : nullptr, swz, w1);
+  store_row<D>(A, w, valid, out_row(A, w, r), to, l > 0.0f ? 1.0f / l : 0.0f,
+               l > 0.0f ? (m_used + log2f(l)) * 0.6931471805599453f : -INFINITY);
 }
 
 // ------------------------------------------------------------------ loader role
@@ -511,10 +438,10 @@ __device__ __forceinline__ void issue_tile(const FlashArgs& A, const Work& w, in
 }
 
 // One warp; entry 2t holds K of tile t, entry 2t + 1 its V.
-template <int D, int NG>
+template <int D>
 __device__ __forceinline__ void load_role(const FlashArgs& A, uint8_t* smem, uint64_t* bars,
                                           const Work& w) {
-  using L = Lay<D, NG>;
+  using L = Lay<D>;
   const int lane = threadIdx.x & 31;
   const uint32_t base = smem_u32(smem);
   bool ok = true;
@@ -523,13 +450,11 @@ __device__ __forceinline__ void load_role(const FlashArgs& A, uint8_t* smem, uin
     // boxes of 64 channels, the key head's g query heads and 128 / g tokens; rows of
     // no row of this CTA are computed with and not stored
     if (lane == 0) {
-      const int tiles = w.nr > QT ? 2 : 1;
-      mbar_arrive_expect_tx(&bars[L::B_Q], tiles * L::Q_TILE);
-      for (int p = 0; p < tiles; ++p)
+      mbar_arrive_expect_tx(&bars[L::B_Q], L::Q_TILE);
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c)
-          tma_load_3d(base + p * L::Q_TILE + c * (QT * 128), &A.q, 64 * c, w.h * A.g,
-                      (int)w.tok0 + w.token(A, w.r0 + p * QT), &bars[L::B_Q]);
+      for (int c = 0; c < D / 64; ++c)
+        tma_load_3d(base + c * (QT * 128), &A.q, 64 * c, w.h * A.g, (int)w.tok0 + w.token(A, w.r0),
+                    &bars[L::B_Q]);
     }
     __syncwarp();
   }
@@ -568,24 +493,22 @@ __device__ __forceinline__ void load_role(const FlashArgs& A, uint8_t* smem, uin
 }
 
 // ------------------------------------------------------------------ MMA role
-// One thread per group: two tiles' S = Q K^T ahead, then for each tile O += P V
-// and S of the tile after the next, into the buffer that P occupied (the tensor
-// core works in issue order).  A commit tells when all before it is complete.
-template <int D, int NG>
+// One thread: two tiles' S = Q K^T ahead, then for each tile O += P V and S of the
+// tile after the next, into the buffer that P occupied (the tensor core works in
+// issue order).  A commit tells when all before it is complete.
+template <int D>
 __device__ __forceinline__ void mma_role(uint8_t* smem, uint64_t* bars, uint32_t tmem,
-                                         const Work& w, int p) {
-  using L = Lay<D, NG>;
+                                         const Work& w) {
+  using L = Lay<D>;
   constexpr uint32_t IDQ = idesc_bf16(QT, KT, false, false);
   constexpr uint32_t IDP = idesc_bf16(QT, D, false, true);
   const uint32_t base = smem_u32(smem);
-  const uint64_t qd = desc_sw128(base + (w.parity ? 0 : p * L::Q_TILE), 16, 1024);
+  const uint64_t qd = desc_sw128(base, 16, 1024);
   const uint64_t kd = desc_sw128(base + L::OFF_KV, 16, 1024);
   // V: channels are the contiguous dimension; its 64-channel blocks lie KT * 128 bytes apart
   const uint64_t vd = desc_sw128(base + L::OFF_KV, KT * 128, 1024);
-  const uint32_t ts0 = tmem + 128 * p, to = tmem + 128 * (NG + p);
-  const int step = 1 + w.parity;
   auto full = [&](int e) { return mbar_wait(&bars[L::B_FULL + e % L::NST], (e / L::NST) & 1); };
-  auto scores = [&](int t, int i) {  // S of tile t, the group's i-th
+  auto scores = [&](int t) {  // S of tile t
     if (!full(2 * t)) return false;
     tc_fence_after();
     const int slot = 2 * t % L::NST;
@@ -593,44 +516,42 @@ __device__ __forceinline__ void mma_role(uint8_t* smem, uint64_t* bars, uint32_t
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
       const uint32_t in = (k & 3) * 32;
-      mma_bf16_ss(ts0 + 64 * (i & 1), qd + (((k >> 2) * (QT * 128) + in) >> 4),
+      mma_bf16_ss(tmem + 64 * (t & 1), qd + (((k >> 2) * (QT * 128) + in) >> 4),
                   k0 + (((k >> 2) * (KT * 128) + in) >> 4), IDQ, k > 0);
     }
-    mma_commit(&bars[L::B_S + 2 * p + (i & 1)]);
+    mma_commit(&bars[L::B_S + (t & 1)]);
     mma_commit(&bars[L::B_EMPTY + slot]);
     return true;
   };
-  int t = w.parity ? p : 0;
-  bool ok = mbar_wait(&bars[L::B_Q], 0) && scores(t, 0) && (t + step >= w.n || scores(t + step, 1));
-  for (int i = 0; ok && t < w.n; t += step, ++i) {
+  bool ok = mbar_wait(&bars[L::B_Q], 0) && scores(0) && (w.n < 2 || scores(1));
+  for (int t = 0; ok && t < w.n; ++t) {
     const int slot = (2 * t + 1) % L::NST;
-    ok = full(2 * t + 1) && mbar_wait(&bars[L::B_P + 2 * p + (i & 1)], (i >> 1) & 1);
+    ok = full(2 * t + 1) && mbar_wait(&bars[L::B_P + (t & 1)], (t >> 1) & 1);
     if (!ok) break;
     tc_fence_after();
     const uint64_t v0 = vd + ((slot * L::ENT) >> 4);
 #pragma unroll
     for (int k = 0; k < KT / 16; ++k)
-      mma_bf16_ts(to, ts0 + 64 * (i & 1) + 8 * k, v0 + ((k * 16 * 128) >> 4), IDP,
-                  (i > 0 || k > 0) ? 1u : 0u);
-    mma_commit(&bars[t + step < w.n ? L::B_PV + p : L::B_O + p]);
+      mma_bf16_ts(tmem + 128, tmem + 64 * (t & 1) + 8 * k, v0 + ((k * 16 * 128) >> 4), IDP,
+                  (t > 0 || k > 0) ? 1u : 0u);
+    mma_commit(&bars[L::B_PV]);
     mma_commit(&bars[L::B_EMPTY + slot]);
-    if (t + 2 * step < w.n) ok = scores(t + 2 * step, i + 2);
+    if (t + 2 < w.n) ok = scores(t + 2);
   }
-  mma_commit(&bars[L::B_DONE + p]);
-  if (!mbar_wait(&bars[L::B_DONE + p], 0)) ok = false;
+  mma_commit(&bars[L::B_DONE]);
+  if (!mbar_wait(&bars[L::B_DONE], 0)) ok = false;
   if (!ok) timeout_flag();
 }
 
-template <int D, int NG>
-__global__ void __launch_bounds__(Lay<D, NG>::NTHREADS, 3 - NG)
-    flash_kernel(const __grid_constant__ FlashArgs A) {
-  using L = Lay<D, NG>;
+template <int D>
+__global__ void __launch_bounds__(NTHREADS, 2) flash_kernel(const __grid_constant__ FlashArgs A) {
+  using L = Lay<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Work w;
-  if (!work_of<NG>(A, w)) return;
+  if (!work_of(A, w)) return;
   if (w.n == 0) {  // no keys in this range
     const int rr = threadIdx.x;
-    for (int e = rr; e < w.nr * (D / 8); e += L::NTHREADS) {
+    for (int e = rr; e < w.nr * (D / 8); e += NTHREADS) {
       const int64_t row = out_row(A, w, w.r0 + e / (D / 8));
       const int c = e % (D / 8);
       if (A.part0 >= 0) {
@@ -652,45 +573,39 @@ __global__ void __launch_bounds__(Lay<D, NG>::NTHREADS, 3 - NG)
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::NST; ++i) {
       mbar_init(&bars[L::B_FULL + i], 1);
-      mbar_init(&bars[L::B_EMPTY + i], w.parity ? 1 : w.groups);
+      mbar_init(&bars[L::B_EMPTY + i], 1);
     }
-    mbar_init(&bars[L::B_Q], A.qtma ? 1 : L::W_LOAD);
-    for (int i = 0; i < 2; ++i) {
-      const int warps = i < w.groups ? (w.rows_of(i) + 31) / 32 : 1;
-      for (int b = 0; b < 2; ++b) {
-        mbar_init(&bars[L::B_S + 2 * i + b], 1);
-        mbar_init(&bars[L::B_P + 2 * i + b], warps);
-      }
-      mbar_init(&bars[L::B_PV + i], 1);
-      mbar_init(&bars[L::B_O + i], 1);
-      mbar_init(&bars[L::B_DONE + i], 1);
+    mbar_init(&bars[L::B_Q], A.qtma ? 1 : W_LOAD);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&bars[L::B_S + b], 1);
+      mbar_init(&bars[L::B_P + b], (w.nr + 31) / 32);
     }
-    mbar_init(&bars[L::B_M], (w.nr + 31) / 32);
+    mbar_init(&bars[L::B_PV], 1);
+    mbar_init(&bars[L::B_DONE], 1);
     mbar_init(&bars[L::B_RAG], 1);
     fence_mbar_init();
   }
-  if (warp == L::W_MMA) {
-    tmem_alloc(holder, L::COLS);
+  if (warp == W_MMA) {
+    tmem_alloc(holder, COLS);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *holder;
-  if (warp < L::W_LOAD) {
-    softmax_role<D, NG>(A, smem, bars, tmem, w);
-  } else if (warp < L::W_MMA) {
-    load_role<D, NG>(A, smem, bars, w);
+  if (warp < W_LOAD) {
+    softmax_role<D>(A, smem, bars, tmem, w);
+  } else if (warp < W_MMA) {
+    load_role<D>(A, smem, bars, w);
   } else {
-    const int p = warp - L::W_MMA;
-    if ((threadIdx.x & 31) == 0 && p < w.groups) mma_role<D, NG>(smem, bars, tmem, w, p);
+    if ((threadIdx.x & 31) == 0) mma_role<D>(smem, bars, tmem, w);
     __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == L::W_MMA) {
+  if (warp == W_MMA) {
     tc_fence_after();
-    tmem_dealloc(tmem, L::COLS);
+    tmem_dealloc(tmem, COLS);
   }
 }
 
@@ -882,24 +797,18 @@ int device_sms() {
   return cache[dev];
 }
 
-// How a launch divides its work: groups per CTA, row blocks per sequence, key
-// ranges per row block.
+// How a launch divides its work: row blocks per sequence, key ranges per row block.
 struct Blocks {
-  int ng, qblocks, nsplit;
+  int qblocks, nsplit;
 };
 
 // rows: of a sequence; units: sequences times key heads; ntile: key tiles; most:
 // key ranges at most.  The key ranges are the count that minimizes (rounds of CTAs
-// on the GPU) x (tiles per range + a fixed cost of FIX tiles).
+// on the GPU) x (tiles per range + a fixed cost of 8 tiles).
 Blocks blocks_of(int64_t rows, int64_t units, int64_t ntile, int most) {
   Blocks b;
-#ifdef NGF
-  b.ng = NGF;
-#else
-  b.ng = ntile >= 40 && rows > QT ? 2 : 1;
-#endif
-  b.qblocks = (int)((rows + b.ng * QT - 1) / (b.ng * QT));
-  const int64_t ctas = units * b.qblocks, slots = (int64_t)device_sms() * (3 - b.ng);
+  b.qblocks = (int)((rows + QT - 1) / QT);
+  const int64_t ctas = units * b.qblocks, slots = 2 * (int64_t)device_sms();
   b.nsplit = 1;
   double bestc = 1e300;
   for (int s = 1; s <= most && s * 4 <= (ntile > 4 ? ntile : 4); ++s) {
@@ -951,22 +860,18 @@ bool map_q(FlashArgs& a, int D) {
   return !a.qtma || map_3d(&a.q, a.Q, D, a.Hq, D, a.nq, a.ldq, a.g, QT / a.g);
 }
 
-template <int D, int NG>
+template <int D>
 cudaError_t launch_flash(const FlashArgs& a, int heads, int64_t n_seq, cudaStream_t s) {
-  using L = Lay<D, NG>;
   static std::atomic<uint64_t> allowed{0};
-  const cudaError_t e = allow_smem(flash_kernel<D, NG>, allowed, (int)L::SMEM);
+  const cudaError_t e = allow_smem(flash_kernel<D>, allowed, (int)Lay<D>::SMEM);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((int64_t)a.qblocks * a.nsplit), (unsigned)heads, (unsigned)n_seq);
-  flash_kernel<D, NG><<<grid, L::NTHREADS, L::SMEM, s>>>(a);
+  flash_kernel<D><<<grid, NTHREADS, Lay<D>::SMEM, s>>>(a);
   return cudaGetLastError();
 }
 
-cudaError_t launch_flash(int D, const FlashArgs& a, const Blocks& b, int heads, int64_t n_seq,
-                         cudaStream_t s) {
-  if (D == 128)
-    return b.ng == 2 ? launch_flash<128, 2>(a, heads, n_seq, s) : launch_flash<128, 1>(a, heads, n_seq, s);
-  return b.ng == 2 ? launch_flash<64, 2>(a, heads, n_seq, s) : launch_flash<64, 1>(a, heads, n_seq, s);
+cudaError_t launch_flash(int D, const FlashArgs& a, int heads, int64_t n_seq, cudaStream_t s) {
+  return D == 128 ? launch_flash<128>(a, heads, n_seq, s) : launch_flash<64>(a, heads, n_seq, s);
 }
 
 cudaError_t launch_merge(int D, const FlashArgs& a, int np, const int32_t* cu, int64_t n_seq,
@@ -1027,7 +932,7 @@ SharedPlan plan_shared(const Dims& D, int64_t T, int Hq, int64_t n_q, int64_t n_
 }
 
 bool lengths_ok(int64_t n_q, int g, int64_t n_seq, int64_t max_q, int64_t max_kv) {
-  return n_q >= 0 && n_q * g <= kMaxGridX - 2 * QT && n_seq >= 1 && n_seq <= 65535 && max_q >= 0 &&
+  return n_q >= 0 && n_q * g <= kMaxGridX - QT && n_seq >= 1 && n_seq <= 65535 && max_q >= 0 &&
          max_q <= kMaxGridX && max_kv >= 0 && max_kv <= kMaxGridX - KT;
 }
 
@@ -1149,7 +1054,7 @@ extern "C" qwm_status qwm_attention_shared(const qwm_cache* c, const void* Q, in
   hp = (D.H + passes - 1) / passes;
   const int64_t tiles0 = (T + KT - 1) / KT, tiles1 = (max_kv + KT - 1) / KT;
   int np = 0;
-  Blocks ba = {}, bo = {};
+  Blocks bo = {};
   const auto set = [](FlashArgs& f, const Blocks& b) {
     f.qblocks = b.qblocks;
     f.nsplit = b.nsplit;
@@ -1169,8 +1074,7 @@ extern "C" qwm_status qwm_attention_shared(const qwm_cache* c, const void* Q, in
         return QWM_ERR_CUDA;
     } else {
       a.max_q = n_q;
-      ba = blocks_of(n_q * g, hp, tiles0, plan.np - bo.nsplit);
-      set(a, ba);
+      set(a, blocks_of(n_q * g, hp, tiles0, plan.np - bo.nsplit));
     }
     a.part0 = 0;
     own.part0 = a.nsplit;
@@ -1189,9 +1093,9 @@ extern "C" qwm_status qwm_attention_shared(const qwm_cache* c, const void* Q, in
         return QWM_ERR_CUDA;
     }
     with0.head0 = h0;
-    if (launch_flash(D.d, with0, plan.joined ? bo : ba, nh, plan.joined ? n_seq : 1, s) != cudaSuccess) return QWM_ERR_CUDA;
+    if (launch_flash(D.d, with0, nh, plan.joined ? n_seq : 1, s) != cudaSuccess) return QWM_ERR_CUDA;
   }
-  if (!plan.joined && own.nsplit > 0 && launch_flash(D.d, own, bo, D.H, n_seq, s) != cudaSuccess)
+  if (!plan.joined && own.nsplit > 0 && launch_flash(D.d, own, D.H, n_seq, s) != cudaSuccess)
     return QWM_ERR_CUDA;
   if (np > 0 && launch_merge(D.d, a, np, cu, n_seq, max_q, s) != cudaSuccess) return QWM_ERR_CUDA;
   return QWM_OK;
@@ -1270,7 +1174,7 @@ extern "C" qwm_status qwm_cross_attention(const void* Q, int64_t ldq, int64_t n_
     a.ws_l = a.ws_o + (size_t)b.nsplit * n_q * heads_q * head_dim;
   }
   const cudaStream_t s = (cudaStream_t)stream;
-  if (launch_flash(head_dim, a, b, heads_kv, n_seq, s) != cudaSuccess) return QWM_ERR_CUDA;
+  if (launch_flash(head_dim, a, heads_kv, n_seq, s) != cudaSuccess) return QWM_ERR_CUDA;
   if (a.nsplit > 1 && launch_merge(head_dim, a, a.nsplit, cu, n_seq, max_q, s) != cudaSuccess)
     return QWM_ERR_CUDA;
   return QWM_OK;
