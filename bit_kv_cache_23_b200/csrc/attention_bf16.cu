@@ -55,16 +55,17 @@ template <int D>
 struct Lay {
   static constexpr uint32_t Q_TILE = QT * D * 2;  // [D / 64 column blocks][128 rows][128 B]
   static constexpr uint32_t ENT = KT * D * 2;     // one K or V tile, [D / 64][64 rows][128 B]
-  static constexpr int NST = D == 128 ? 4 : 8;    // ring entries (K, V, K, V, ...)
-  static constexpr uint32_t OFF_KV = Q_TILE;
-  static constexpr uint32_t OFF_BAR = OFF_KV + NST * ENT;
-  static constexpr int B_FULL = 0,        // loader -> MMA
-                       B_EMPTY = NST,     // MMA commits -> loader
-                       B_Q = 2 * NST,     // Q is in shared memory
-                       B_S = B_Q + 1,     // [buffer] commit of Q K^T -> softmax
-                       B_P = B_S + 2,     // [buffer] softmax -> MMA
-                       B_PV = B_P + 2,    // commit of P V -> softmax
-                       B_DONE = B_PV + 1, // drain before exit
+  static constexpr uint32_t OFF_K = Q_TILE, OFF_V = OFF_K + 2 * ENT;  // two tiles of each
+  static constexpr uint32_t OFF_BAR = OFF_V + 2 * ENT;
+  // Tile t uses places and barriers t & 1.  Few barriers, for each commit costs the
+  // issuing thread time: S is also what frees K's place, P V what frees V's.
+  static constexpr int B_K = 0,           // loader -> MMA
+                       B_V = B_K + 2,
+                       B_S = B_V + 2,     // commit of Q K^T -> softmax, loader
+                       B_P = B_S + 2,     // softmax -> MMA
+                       B_PV = B_P + 2,    // commit of P V -> softmax, loader
+                       B_Q = B_PV + 2,    // Q is in shared memory
+                       B_DONE = B_Q + 1, // drain before exit
                        B_RAG = B_DONE + 1,  // a ragged V tile has landed -> loader
                        NBAR = B_RAG + 1;
   static constexpr uint32_t SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
@@ -361,7 +362,7 @@ __device__ __forceinline__ void softmax_role(const FlashArgs& A, uint8_t* smem, 
       m_used = m_row;
     } else if (__any_sync(0xffffffffu, need)) {
       // O is at rest once the last product with P is complete (this tile's waits for P)
-      if (!warp_wait(&bars[L::B_PV], (i - 1) & 1)) { ok = false; break; }
+      if (!warp_wait(&bars[L::B_PV + ((i - 1) & 1)], ((i - 1) >> 1) & 1)) { ok = false; break; }
       tc_fence_after();
       const float f = need ? ex2(m_used - m_row) : 1.0f;
 #pragma unroll 1
@@ -385,7 +386,7 @@ __device__ __forceinline__ void softmax_role(const FlashArgs& A, uint8_t* smem, 
     tc_fence_before();
     warp_arrive(&bars[L::B_P + (i & 1)]);
   }
-  if (ok) ok = warp_wait(&bars[L::B_PV], (w.n - 1) & 1);
+  if (ok) ok = warp_wait(&bars[L::B_PV + ((w.n - 1) & 1)], ((w.n - 1) >> 1) & 1);
   if (!ok) {
     if ((threadIdx.x & 31) == 0) timeout_flag();
     return;
@@ -399,8 +400,8 @@ __device__ __forceinline__ void softmax_role(const FlashArgs& A, uint8_t* smem, 
 }
 
 // ------------------------------------------------------------------ loader role
-// The boxes of K (v = 0) or V (v = 1) rows of key tile j into the ring entry at
-// `dst`, ENT bytes in all; one thread.
+// The boxes of K (v = 0) or V (v = 1) rows of key tile j to `dst`, ENT bytes
+// in all; one thread.
 template <int D>
 __device__ __forceinline__ void issue_tile(const FlashArgs& A, const Work& w, int j, int v,
                                            uint32_t dst, uint64_t* bar) {
@@ -437,7 +438,7 @@ __device__ __forceinline__ void issue_tile(const FlashArgs& A, const Work& w, in
   }
 }
 
-// One warp; entry 2t holds K of tile t, entry 2t + 1 its V.
+// One warp: K and V of the tiles in turn.
 template <int D>
 __device__ __forceinline__ void load_role(const FlashArgs& A, uint8_t* smem, uint64_t* bars,
                                           const Work& w) {
@@ -445,7 +446,7 @@ __device__ __forceinline__ void load_role(const FlashArgs& A, uint8_t* smem, uin
   const int lane = threadIdx.x & 31;
   const uint32_t base = smem_u32(smem);
   bool ok = true;
-  int rag = 0, e = 0;
+  int rag = 0, e = 0;  // e = 2 t: K of tile t; e = 2 t + 1: its V
   if (A.qtma) {
     // boxes of 64 channels, the key head's g query heads and 128 / g tokens; rows of
     // no row of this CTA are computed with and not stored
@@ -459,36 +460,37 @@ __device__ __forceinline__ void load_role(const FlashArgs& A, uint8_t* smem, uin
     __syncwarp();
   }
   for (; e < 2 * w.n; ++e) {
-    const int slot = e % L::NST;
-    if (e >= L::NST && !warp_wait(&bars[L::B_EMPTY + slot], ((e / L::NST) - 1) & 1)) {
+    const int t = e >> 1, v = e & 1, at = t & 1;
+    if (t >= 2 && !warp_wait(&bars[(v ? L::B_PV : L::B_S) + at], ((t >> 1) - 1) & 1)) {
       ok = false;
       break;
     }
-    const int j = w.j0 + e / 2;
+    const int j = w.j0 + t;
     const int left = j < w.nt0 ? KT : w.len1 - (j - w.nt0) * KT;
-    const uint32_t dst = base + L::OFF_KV + slot * L::ENT;
+    const uint32_t off = (v ? L::OFF_V : L::OFF_K) + at * L::ENT, dst = base + off;
+    uint64_t* const full = &bars[(v ? L::B_V : L::B_K) + at];
     // V rows behind the end are overwritten before the tile is handed on
-    const bool wipe = (e & 1) && left < KT;
-    uint64_t* bar = &bars[wipe ? L::B_RAG : L::B_FULL + slot];
+    const bool wipe = v && left < KT;
+    uint64_t* bar = wipe ? &bars[L::B_RAG] : full;
     if (lane == 0) {
       mbar_arrive_expect_tx(bar, L::ENT);
-      issue_tile<D>(A, w, j, e & 1, dst, bar);
+      issue_tile<D>(A, w, j, v, dst, bar);
     }
     __syncwarp();
     if (wipe) {
       if (!warp_wait(bar, rag++ & 1)) { ok = false; ++e; break; }
       constexpr int C = D / 8;
       for (int x = left * C + lane; x < KT * C; x += 32)
-        *reinterpret_cast<uint4*>(smem + L::OFF_KV + slot * L::ENT + sw128_off(x / C, x % C, KT)) =
+        *reinterpret_cast<uint4*>(smem + off + sw128_off(x / C, x % C, KT)) =
             make_uint4(0, 0, 0, 0);
       fence_proxy_async_smem();
-      warp_arrive(&bars[L::B_FULL + slot]);
+      warp_arrive(full);
     }
   }
   // every box issued has landed before the CTA may exit
   if (A.qtma && !warp_wait(&bars[L::B_Q], 0)) ok = false;
-  for (int k = e > L::NST ? e - L::NST : 0; k < e; ++k)
-    if (!warp_wait(&bars[L::B_FULL + k % L::NST], (k / L::NST) & 1)) ok = false;
+  for (int k = e > 4 ? e - 4 : 0; k < e; ++k)
+    if (!warp_wait(&bars[(k & 1 ? L::B_V : L::B_K) + ((k >> 1) & 1)], (k >> 2) & 1)) ok = false;
   if (!ok && lane == 0) timeout_flag();
 }
 
@@ -504,15 +506,11 @@ __device__ __forceinline__ void mma_role(uint8_t* smem, uint64_t* bars, uint32_t
   constexpr uint32_t IDP = idesc_bf16(QT, D, false, true);
   const uint32_t base = smem_u32(smem);
   const uint64_t qd = desc_sw128(base, 16, 1024);
-  const uint64_t kd = desc_sw128(base + L::OFF_KV, 16, 1024);
+  const uint64_t kd = desc_sw128(base + L::OFF_K, 16, 1024);
   // V: channels are the contiguous dimension; its 64-channel blocks lie KT * 128 bytes apart
-  const uint64_t vd = desc_sw128(base + L::OFF_KV, KT * 128, 1024);
-  auto full = [&](int e) { return mbar_wait(&bars[L::B_FULL + e % L::NST], (e / L::NST) & 1); };
-  auto scores = [&](int t) {  // S of tile t
-    if (!full(2 * t)) return false;
-    tc_fence_after();
-    const int slot = 2 * t % L::NST;
-    const uint64_t k0 = kd + ((slot * L::ENT) >> 4);
+  const uint64_t vd = desc_sw128(base + L::OFF_V, KT * 128, 1024);
+  auto scores = [&](int t) {  // S of tile t, whose K is there
+    const uint64_t k0 = kd + (((t & 1) * L::ENT) >> 4);
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
       const uint32_t in = (k & 3) * 32;
@@ -520,23 +518,36 @@ __device__ __forceinline__ void mma_role(uint8_t* smem, uint64_t* bars, uint32_t
                   k0 + (((k >> 2) * (KT * 128) + in) >> 4), IDQ, k > 0);
     }
     mma_commit(&bars[L::B_S + (t & 1)]);
-    mma_commit(&bars[L::B_EMPTY + slot]);
-    return true;
   };
-  bool ok = mbar_wait(&bars[L::B_Q], 0) && scores(0) && (w.n < 2 || scores(1));
-  for (int t = 0; ok && t < w.n; ++t) {
-    const int slot = (2 * t + 1) % L::NST;
-    ok = full(2 * t + 1) && mbar_wait(&bars[L::B_P + (t & 1)], (t >> 1) & 1);
+  bool ok = mbar_wait(&bars[L::B_Q], 0);
+  for (int t = 0; ok && t < 2 && t < w.n; ++t) {
+    ok = mbar_wait(&bars[L::B_K + t], 0);
     if (!ok) break;
     tc_fence_after();
-    const uint64_t v0 = vd + ((slot * L::ENT) >> 4);
+    scores(t);
+  }
+  for (int t = 0; ok && t < w.n; ++t) {
+    const int at = t & 1;
+    const uint32_t phase = (t >> 1) & 1;
+    // (a test only: P V must not wait for a later key tile)
+    const bool there = t + 2 < w.n && mbar_test(&bars[L::B_K + at], phase ^ 1);
+    ok = mbar_wait(&bars[L::B_V + at], phase) && mbar_wait(&bars[L::B_P + at], phase);
+    if (!ok) break;
+    tc_fence_after();
+    const uint64_t v0 = vd + ((at * L::ENT) >> 4);
 #pragma unroll
     for (int k = 0; k < KT / 16; ++k)
-      mma_bf16_ts(tmem + 128, tmem + 64 * (t & 1) + 8 * k, v0 + ((k * 16 * 128) >> 4), IDP,
+      mma_bf16_ts(tmem + 128, tmem + 64 * at + 8 * k, v0 + ((k * 16 * 128) >> 4), IDP,
                   (t > 0 || k > 0) ? 1u : 0u);
-    mma_commit(&bars[L::B_PV]);
-    mma_commit(&bars[L::B_EMPTY + slot]);
-    if (t + 2 < w.n) ok = scores(t + 2);
+    mma_commit(&bars[L::B_PV + at]);
+    if (t + 2 < w.n) {
+      if (!there) {
+        ok = mbar_wait(&bars[L::B_K + at], phase ^ 1);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      scores(t + 2);
+    }
   }
   mma_commit(&bars[L::B_DONE]);
   if (!mbar_wait(&bars[L::B_DONE], 0)) ok = false;
@@ -571,16 +582,14 @@ __global__ void __launch_bounds__(NTHREADS, 2) flash_kernel(const __grid_constan
   uint32_t* holder = reinterpret_cast<uint32_t*>(smem + L::OFF_BAR + L::NBAR * 8);
   const int warp = threadIdx.x / 32;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < L::NST; ++i) {
-      mbar_init(&bars[L::B_FULL + i], 1);
-      mbar_init(&bars[L::B_EMPTY + i], 1);
-    }
     mbar_init(&bars[L::B_Q], A.qtma ? 1 : W_LOAD);
     for (int b = 0; b < 2; ++b) {
+      mbar_init(&bars[L::B_K + b], 1);
+      mbar_init(&bars[L::B_V + b], 1);
       mbar_init(&bars[L::B_S + b], 1);
       mbar_init(&bars[L::B_P + b], (w.nr + 31) / 32);
+      mbar_init(&bars[L::B_PV + b], 1);
     }
-    mbar_init(&bars[L::B_PV], 1);
     mbar_init(&bars[L::B_DONE], 1);
     mbar_init(&bars[L::B_RAG], 1);
     fence_mbar_init();
