@@ -633,17 +633,23 @@ __global__ void __launch_bounds__(256) merge_kernel(const float* __restrict__ ws
   if (row >= rows) return;
   const int lane = threadIdx.x & 31;
   const int64_t t = row / Hq;
-  int64_t lo = 0, hi = n_seq;
-  if (t >= __ldg(cu + n_seq) || t < __ldg(cu)) return;
+  // the last sequence that begins at or before t, 32 probes at a time
+  int64_t lo = -1, hi = n_seq + 1;
   while (hi - lo > 1) {
-    const int64_t mid = (lo + hi) >> 1;
-    if (__ldg(cu + mid) <= t) lo = mid;
-    else hi = mid;
+    const int64_t step = (hi - lo + 31) / 32, x = lo + (lane + 1) * step;
+    const unsigned below = __ballot_sync(0xffffffffu, x < hi && __ldg(cu + x) <= t);
+    const int n = below == 0xffffffffu ? 32 : __ffs(~below) - 1;  // the leading probes
+    const int64_t up = lo + (n + 1) * step;
+    lo += n * step;
+    hi = up < hi ? up : hi;
   }
+  if (lo < 0 || lo >= n_seq) return;
   const int64_t c0 = __ldg(cu + lo), c1 = __ldg(cu + lo + 1);
   if (t - c0 >= max_q || c0 < 0 || c1 > nq || c1 <= t) return;
-  float L = -INFINITY;
-  for (int c = lane; c < np; c += 32) L = fmaxf(L, __ldg(ws_l + (size_t)c * rows + row));
+  // (at most 64 partials: two of their weights per lane)
+  float l0 = lane < np ? __ldg(ws_l + (size_t)lane * rows + row) : -INFINITY;
+  float l1 = lane + 32 < np ? __ldg(ws_l + (size_t)(lane + 32) * rows + row) : -INFINITY;
+  float L = fmaxf(l0, l1);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) L = fmaxf(L, __shfl_xor_sync(0xffffffffu, L, o));
   constexpr int V = D / 32;
@@ -651,14 +657,16 @@ __global__ void __launch_bounds__(256) merge_kernel(const float* __restrict__ ws
 #pragma unroll
   for (int e = 0; e < V; ++e) acc[e] = 0.0f;
   if (L > -INFINITY) {
+    const float w0 = expf(l0 - L), w1 = expf(l1 - L);
+#pragma unroll 4
     for (int c = 0; c < np; ++c) {
-      const float wt = expf(__ldg(ws_l + (size_t)c * rows + row) - L);
-      if (wt == 0.0f) continue;  // (an empty partial's values are not written)
+      const float wt = __shfl_sync(0xffffffffu, c < 32 ? w0 : w1, c & 31);
       const float* o = ws_o + ((size_t)c * rows + row) * D + V * lane;
       den += wt;
 #pragma unroll
       for (int e = 0; e < V; e += 2) {
-        const float2 x = __ldg(reinterpret_cast<const float2*>(o + e));
+        float2 x = make_float2(0.0f, 0.0f);
+        if (wt != 0.0f) x = __ldg(reinterpret_cast<const float2*>(o + e));  // (an empty partial's values are not written)
         acc[e] = fmaf(wt, x.x, acc[e]);
         acc[e + 1] = fmaf(wt, x.y, acc[e + 1]);
       }

@@ -294,7 +294,8 @@ __device__ __forceinline__ void keys16(const RowsArgs& A, const Fields& F, const
   constexpr int VCH = D / 8;       // a lane's V channels
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const Dims& Dm = A.Dm;
-  const int G = Dm.G, ng = Dm.ng, r = Dm.r, ib = Dm.idx_bytes;
+  const int gs = Dm.G == 16 ? 4 : 5;  // log2 of the group size
+  const int ng = Dm.ng, r = Dm.r, ib = Dm.idx_bytes;
   const uint8_t* tk = smem + F.tab;
   const uint8_t* tvv = tk + Dm.C * D * 2;
   auto number = [&](uint32_t fields, int k, bool live) {  // centroid (0 of a key not worked on)
@@ -344,7 +345,7 @@ __device__ __forceinline__ void keys16(const RowsArgs& A, const Fields& F, const
       for (int x = 0; x < 2; ++x) {
         const int k = g + 8 * x;
         code[x] = reinterpret_cast<const uint32_t*>(pk + St::KC)[k * (D / 16) + c * KW + wa];
-        gc[x] = decode_of(reinterpret_cast<const uint32_t*>(pk + St::KP)[k * ng + (c * KCH + 16 * wa) / G]);
+        gc[x] = decode_of(reinterpret_cast<const uint32_t*>(pk + St::KP)[k * ng + ((c * KCH + 16 * wa) >> gs)]);
       }
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {  // 8 channels: a piece of the centroid
@@ -459,7 +460,7 @@ __device__ __forceinline__ void keys16(const RowsArgs& A, const Fields& F, const
       const uint8_t* cd = pk + St::VC + k * (D / 4) + g * (VCH / 4);
       code[e] = VCH == 16 ? *reinterpret_cast<const uint32_t*>(cd) : *reinterpret_cast<const uint16_t*>(cd);
       // a key that is not worked on: finite (its weight is 0)
-      const uint32_t par = live ? reinterpret_cast<const uint32_t*>(pk + F.vp)[k * ng + g * VCH / G] : 0u;
+      const uint32_t par = live ? reinterpret_cast<const uint32_t*>(pk + F.vp)[k * ng + (g * VCH >> gs)] : 0u;
       mn[e] = h2f((uint16_t)(par & 0xffffu));
       sc[e] = h2f((uint16_t)(par >> 16));
     }
@@ -709,7 +710,8 @@ __device__ __forceinline__ void unpack16(const UnpackArgs& A, const Fields& F, c
   constexpr int KCH = D / 4, KW = KCH / 16;
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const Dims& Dm = A.Dm;
-  const int G = Dm.G, ng = Dm.ng, r = Dm.r, ib = Dm.idx_bytes;
+  const int gs = Dm.G == 16 ? 4 : 5;  // log2 of the group size
+  const int ng = Dm.ng, r = Dm.r, ib = Dm.idx_bytes;
   const uint8_t* tk = smem + F.tab;
   const uint8_t* tvv = tk + Dm.C * D * 2;
   uint32_t one;
@@ -756,7 +758,7 @@ __device__ __forceinline__ void unpack16(const UnpackArgs& A, const Fields& F, c
         const int k = g + 8 * x;
         code[x] = reinterpret_cast<const uint32_t*>(pk + (kv ? St::VC : St::KC))[k * (D / 16) + c * KW + wa];
         dc[x] = decode_of(
-            reinterpret_cast<const uint32_t*>(pk + (kv ? F.vp : St::KP))[k * ng + (c * KCH + 16 * wa) / G]);
+            reinterpret_cast<const uint32_t*>(pk + (kv ? F.vp : St::KP))[k * ng + ((c * KCH + 16 * wa) >> gs)]);
       }
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
