@@ -660,6 +660,8 @@ class QuantKVCache:
                          stream=None):
         if Q.device != self.buffers["k_codes"].device:
             raise ValueError(f"Q is on {Q.device}, the cache on {self.device}")
+        if pages is not None and pages.K.device != Q.device:
+            raise ValueError(f"Q is on {Q.device}, the pages on {pages.K.device}")
         return qwm_attention_shared(self.c, Q, cu, max_q, pages.pages if pages else None, table,
                                     kv_len, max_kv, causal, O, lse, scale, workspace, stream)
 

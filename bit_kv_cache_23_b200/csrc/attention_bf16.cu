@@ -72,6 +72,8 @@ struct Lay {
 };
 static_assert(Lay<128>::SMEM <= 113 * 1024 && Lay<64>::SMEM <= 113 * 1024, "two CTAs per SM");
 
+constexpr int kMostKeys = (1 << 30);  // of a sequence, rows alike: sums of both stay in 31 bits
+
 enum { OWN_NONE = 0, OWN_ROWS = 1, OWN_PAGES = 2 };
 
 struct FlashArgs {
@@ -110,7 +112,8 @@ struct Work {
   int r0;
   int nr;          // rows of this CTA
   int h;
-  int len1;        // own keys
+  int len1;        // own keys that are read (at most max_kv)
+  int len;         // own keys of the sequence
   int start1;      // first own row (OWN_ROWS)
   int b;
   int nt0;         // tiles of the shared keys
@@ -121,7 +124,7 @@ struct Work {
   }
   // own keys that row r sees (causal)
   __device__ __forceinline__ int seen(const FlashArgs& A, int r) const {
-    const int x = len1 - nb + token(A, r) + 1;
+    const int x = len - nb + token(A, r) + 1;
     return x < 0 ? 0 : x > len1 ? len1 : x;
   }
 };
@@ -147,7 +150,7 @@ __device__ __forceinline__ bool work_of(const FlashArgs& A, Work& w) {
   // (the host refuses more than 2^31 - 1 rows, keys or pages' places)
   const int rows = (w.nb < A.max_q ? w.nb : (int)A.max_q) * A.g;
   w.r0 = qb * QT;
-  w.len1 = 0;
+  w.len = w.len1 = 0;
   w.start1 = 0;
   if (A.own != OWN_NONE) {
     int64_t len = A.kv_len[w.b];
@@ -160,6 +163,7 @@ __device__ __forceinline__ bool work_of(const FlashArgs& A, Work& w) {
     }
     fault |= len < 0 || len > room;
     len = len < 0 ? 0 : len > room ? room : len;
+    w.len = (int)(len < kMostKeys ? len : kMostKeys);
     w.len1 = (int)(len < A.max_kv ? len : A.max_kv);
   }
   if (fault && threadIdx.x == 0) atomicExch(&g_flash_fault, 1);
@@ -948,9 +952,9 @@ SharedPlan plan_shared(const Dims& D, int64_t T, int Hq, int64_t n_q, int64_t n_
   return p;
 }
 
-bool lengths_ok(int64_t n_q, int g, int64_t n_seq, int64_t max_q, int64_t max_kv) {
-  return n_q >= 0 && n_q * g <= kMaxGridX - QT && n_seq >= 1 && n_seq <= 65535 && max_q >= 0 &&
-         max_q <= kMaxGridX && max_kv >= 0 && max_kv <= kMaxGridX - KT;
+bool lengths_ok(int64_t n_q, int g, int Hq, int64_t n_seq, int64_t max_q, int64_t max_kv) {
+  return n_q >= 0 && n_q * g <= kMostKeys && n_q * Hq <= 8 * kMaxGridX && n_seq >= 1 && n_seq <= 65535 &&
+         max_q >= 0 && max_q <= kMaxGridX && max_kv >= 0 && max_kv <= kMostKeys;
 }
 
 }  // namespace
@@ -977,9 +981,11 @@ extern "C" qwm_status qwm_attention_shared_workspace(const qwm_cache* c, int64_t
                                                      int32_t heads_q, int64_t n_seq, int64_t max_q,
                                                      int64_t max_kv, uint64_t* least,
                                                      uint64_t* full) {
-  if (!cache_ok(c) || c->len > kMaxGridX - KT || !least || !full || heads_q < 1 || heads_q > 65535 || heads_q % c->cfg.heads ||
-      !lengths_ok(n_q, heads_q / c->cfg.heads, n_seq, max_q, max_kv))
+  if (!cache_ok(c) || c->len > kMostKeys || !least || !full || heads_q < 1 || heads_q > 65535 || heads_q % c->cfg.heads ||
+      !lengths_ok(n_q, heads_q / c->cfg.heads, heads_q, n_seq, max_q, max_kv))
     return QWM_ERR_INVALID_ARG;
+  *least = *full = 0;
+  if (n_q == 0 || max_q == 0) return QWM_OK;
   const Dims D = dims_of(&c->cfg);
   const SharedPlan p = plan_shared(D, c->len, heads_q, n_q, n_seq, max_q, max_kv);
   const uint64_t head = p.rows ? 0 : (uint64_t)c->len * D.d * 4;
@@ -1124,7 +1130,7 @@ extern "C" qwm_status qwm_cross_attention_workspace(int32_t heads_q, int32_t hea
                                                     uint64_t* full) {
   if (!least || !full || heads_kv < 1 || heads_q < 1 || heads_q > 65535 || heads_q % heads_kv ||
       (head_dim != 64 && head_dim != 128) ||
-      !lengths_ok(n_q, heads_q / heads_kv, n_seq, max_q, max_kv))
+      !lengths_ok(n_q, heads_q / heads_kv, heads_q, n_seq, max_q, max_kv))
     return QWM_ERR_INVALID_ARG;
   const int64_t mq = max_q < n_q ? max_q : n_q;
   const int np = blocks_of(mq * (heads_q / heads_kv), heads_kv * n_seq, (max_kv + KT - 1) / KT,
@@ -1146,7 +1152,7 @@ extern "C" qwm_status qwm_cross_attention(const void* Q, int64_t ldq, int64_t n_
   const qwm_status st = qwm_cross_attention_workspace(heads_q, heads_kv, head_dim, n_q, n_seq, max_q,
                                                       max_kv, &least, &full);
   if (st != QWM_OK) return st;
-  if (!cu || !kv_start || !kv_len || (n_q > 0 && (!Q || !O)) || n_kv < 0 || n_kv > kMaxGridX ||
+  if (!cu || !kv_start || !kv_len || (n_q > 0 && (!Q || !O)) || n_kv < 0 || n_kv > kMostKeys ||
       (n_kv > 0 && max_kv > 0 && (!K || !V)) || ldq < (int64_t)heads_q * head_dim || ldq % 8 ||
       ldk < (int64_t)heads_kv * head_dim || ldk % 8 || ldv < (int64_t)heads_kv * head_dim || ldv % 8)
     return QWM_ERR_INVALID_ARG;

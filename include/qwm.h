@@ -400,12 +400,16 @@ QWM_API qwm_status qwm_paged_append(const qwm_pages* p, const int32_t* table, in
  * K_b, V_b the first kv_len[b] positions of branch b's pages.  causal != 0:
  * row i of the n_b rows of branch b sees its own keys up to position
  * kv_len[b] - n_b + i only (and the whole history).  Rows without any key give
- * O = 0 and lse = -inf.  Places of the pages that no row sees may hold anything.
+ * O = 0 and lse = -inf.  Places of the pages behind kv_len[b], and pages of no
+ * branch, may hold anything; keys and values before it are finite, also where a
+ * causal limit hides them from a row.
  * Q: [n_q] rows of heads_q heads, ldq apart; heads_q a multiple of the cache's
  * heads, query head j attends to key head j / (heads_q / heads).  O: [n_q][heads_q][head_dim].
  * lse: null or [n_q][heads_q] fp32.  pages, table and kv_len may be null
  * (history only).  max_q, max_kv: upper bounds of a branch's rows and own keys,
- * which size the launch: rows and keys beyond them are left out.
+ * which size the launch: rows and keys beyond them are left out (the rows' O and
+ * lse as they were).  At most 2^30 rows times query heads per key head, tokens
+ * cached and keys of a branch, 65535 branches.
  * workspace: device scratch of this call, 256-byte aligned, not shared with
  * calls that can run at the same time; at least the `least` bytes of
  * qwm_attention_shared_workspace; `full` bytes serve all heads in one pass.

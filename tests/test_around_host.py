@@ -173,7 +173,7 @@ def test_shared_bad_pages(bad):
 @pytest.mark.parametrize("bad,status", [
     (dict(c=None), 1), (dict(Q=None), 1), (dict(O=None), 1), (dict(cu=None), 1), (dict(hq=3), 1), (dict(hq=0), 1),
     (dict(ldq=248), 1), (dict(ldq=260), 1), (dict(n_q=-1), 1), (dict(n_seq=0), 1), (dict(n_seq=65536), 1),
-    (dict(max_q=-1), 1), (dict(max_kv=-1), 1), (dict(max_kv=2**31), 1), (dict(pages=None), 1), (dict(table=None), 1),
+    (dict(max_q=-1), 1), (dict(max_kv=-1), 1), (dict(max_kv=2**30 + 1), 1), (dict(n_q=2**30), 1), (dict(pages=None), 1), (dict(table=None), 1),
     (dict(kv_len=None), 1), (dict(width=0), 1), (dict(Q=ODD), 2), (dict(O=ODD), 2), (dict(lse=ctypes.c_void_p(0x200002)), 2),
     (dict(ws=ctypes.c_void_p(0x40000010)), 2), (dict(ws=None), 3), (dict(ws_bytes=1000), 3),
     (dict(cache=dict(has_centroids=0)), 4), (dict(cache=dict(magic=0)), 1), (dict(n_q=0), 0), (dict(max_q=0), 0)])
@@ -205,7 +205,7 @@ def _cross(**kw):
 @pytest.mark.parametrize("bad,status", [
     (dict(Q=None), 1), (dict(K=None), 1), (dict(V=None), 1), (dict(O=None), 1), (dict(cu=None), 1), (dict(start=None), 1),
     (dict(len=None), 1), (dict(hq=3), 1), (dict(hk=0), 1), (dict(d=96), 1), (dict(d=128), 1), (dict(ldk=120), 1),
-    (dict(ldv=130), 1), (dict(n_kv=-1), 1), (dict(n_seq=0), 1), (dict(max_q=-1), 1), (dict(n_q=-1), 1), (dict(Q=ODD), 2),
+    (dict(ldv=130), 1), (dict(n_kv=-1), 1), (dict(n_kv=2**30 + 1), 1), (dict(n_q=2**30), 1), (dict(n_seq=0), 1), (dict(max_q=-1), 1), (dict(n_q=-1), 1), (dict(Q=ODD), 2),
     (dict(K=ODD), 2), (dict(ws=ctypes.c_void_p(0x40000010)), 2), (dict(n_q=0), 0), (dict(max_q=0), 0)])
 def test_cross_arguments(bad, status):
     assert _cross(**bad) == status

@@ -289,6 +289,28 @@ def test_shared_history_alone_is_qwm_attention():
     assert (short[11:] == 7.0).all()
 
 
+@pytest.mark.parametrize("T,new", [(300, (130, 140)), (0, (3, 5)), (200, (2, 3))])
+def test_shared_bounds_below_the_lengths(T, new):
+    """max_kv below a branch's keys leaves the keys behind it out, max_q the rows; the causal limit still
+    counts from the branch's true length."""
+    own, most_q, most_kv = (150, 160), min(new), 100
+    c, Kp, Vp, rows, kv, table, Q, cu, lens = _shared_case(64, 2, 1, T, new, own, 16, True, 41)
+    O, lse = torch.full_like(Q, 7.0).contiguous(), torch.full(Q.shape[:2], 5.0, device="cuda")
+    c.attention_shared(Q, cu, most_q, kv, table, lens, most_kv, causal=True, O=O, lse=lse)
+    _fine()
+    at = torch.arange(T + most_kv, device="cuda")
+    for b in range(2):
+        s = slice(sum(new[:b]), sum(new[:b]) + most_q)
+        last = T + own[b] - new[b] + torch.arange(most_q, device="cuda")
+        for h in range(2):
+            k, v = (torch.cat([x[h], y[h][:most_kv]]) for x, y in zip((Kp, Vp), rows[b]))
+            want, bound, wl, lb = attend(Q[s, h], k, v, 1 / 8, (at <= last[:, None]) | (at < T))
+            check("O", O[s, h], want, bound)
+            check_lse("lse", lse[s, h], wl, lb)
+    left = slice(new[0] + most_q, None)
+    assert (O[left] == 7.0).all() and (lse[left] == 5.0).all()
+
+
 def test_shared_bad_device_arrays():
     """Page numbers, lengths and offsets outside their buffers are clamped and reported."""
     c, Kp, Vp, rows, kv, table, Q, cu, lens = _shared_case(64, 1, 1, 100, (4, 4), (20, 20), 16, False, 31)
