@@ -18,11 +18,10 @@ int read_and_clear_flash_timeout();
 struct RowsPlan {
   int grid, slots;
 };
-bool rows_supported(const Dims& D, int64_t rows);  // rows: query rows per key head
-// K' and V' of `heads` heads from h0 on, [head][T][d] bf16, for ranks up to 8.
-bool unpack_fast_supported(const Dims& D);
-cudaError_t launch_unpack_fast(const Dims& D, const CacheView& v, int64_t T, int h0, int heads,
-                               uint16_t* K, uint16_t* V, int sms, cudaStream_t s);
+bool rows_supported(const Dims& D, int64_t T, int64_t rows, int sms);  // rows: query rows per key head
+// K' and V' of `heads` heads from h0 on, [head][T][d] bf16.
+cudaError_t launch_unpack(const Dims& D, const CacheView& v, int64_t T, int h0, int heads,
+                          uint16_t* K, uint16_t* V, int sms, cudaStream_t s);
 RowsPlan rows_plan(const Dims& D, int64_t T, int sms, int most);  // at most `most` >= 3 slots
 cudaError_t launch_rows(const Dims& D, const CacheView& v, int64_t T, const uint16_t* Q, int64_t ldq,
                         int64_t nq, int Hq, float scale_log2, const RowsPlan& plan, float* ws_o,

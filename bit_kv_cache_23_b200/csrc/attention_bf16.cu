@@ -35,7 +35,6 @@
 #include <math.h>
 
 #include "around.cuh"
-#include "dequant.cuh"
 #include "tc.cuh"
 
 namespace qwm {
@@ -684,126 +683,6 @@ __global__ void __launch_bounds__(256) merge_kernel(const float* __restrict__ ws
   if (lse && lane == 0) lse[row] = den > 0.0f ? L + logf(den) : -INFINITY;
 }
 
-// ------------------------------------------------------------------ unpacking
-// K' and V' of the cache's first T tokens, heads h0 .. h0 + gridDim.y - 1, as
-// [head][T][D] bf16, each element summed in fp32 in the order of the cache's
-// reconstruction and rounded once.  A thread owns 16 channels (within one INT2
-// group) of two tokens at a time, so that each basis value that it reads from
-// shared memory serves two; the basis of the block's first token is staged
-// transposed, tokens of another version read theirs from global memory.
-constexpr int UT = 64;  // tokens per block
-
-__device__ __forceinline__ void add_residual(uint4 lo, uint4 hi, uint32_t code, uint32_t par,
-                                             float (&v)[16]) {
-  const float mn = h2f((uint16_t)(par & 0xffffu)), sc = h2f((uint16_t)(par >> 16));
-  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    const float c = __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
-    v[e] = c + fmaf((float)((code >> (2 * e)) & 3u), sc, mn);
-  }
-}
-
-__device__ __forceinline__ void store16(uint16_t* dst, const float (&v)[16]) {
-  uint4* d = reinterpret_cast<uint4*>(dst);
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
-    d[k] = make_uint4(pack_bf16(v[8 * k], v[8 * k + 1]), pack_bf16(v[8 * k + 2], v[8 * k + 3]),
-                      pack_bf16(v[8 * k + 4], v[8 * k + 5]), pack_bf16(v[8 * k + 6], v[8 * k + 7]));
-}
-
-template <int D>
-__global__ void __launch_bounds__(256) unpack_kernel(const Dims Dm, const CacheView cv, int64_t T,
-                                                     int h0, uint16_t* __restrict__ Kd,
-                                                     uint16_t* __restrict__ Vd) {
-  constexpr int SL = D / 16;      // 16-channel slices
-  constexpr int TP = 256 / SL;    // tokens per round
-  __shared__ __align__(16) float Us[16 * D];
-  const int h = h0 + blockIdx.y;
-  const int64_t t0 = (int64_t)blockIdx.x * UT;
-  const int r = Dm.r, sl = threadIdx.x % SL, tr = threadIdx.x / SL;
-  const PackedHead p = packed_head(cv, Dm, h);
-  const int ver0 = cv.tokver[t0];
-  if (r > 0) {
-    const float* U = basis_of(cv, Dm, ver0, h);
-    for (int e = threadIdx.x; e < r * D; e += 256) Us[e] = __ldg(U + (size_t)(e % D) * r + e / D);
-  }
-  __syncthreads();
-  const int gi = 16 * sl / Dm.G;
-  uint16_t* kh = Kd + (int64_t)blockIdx.y * T * D + 16 * sl;
-  uint16_t* vh = Vd + (int64_t)blockIdx.y * T * D + 16 * sl;
-  for (int k0 = tr; k0 < UT; k0 += 2 * TP) {
-    float kv[2][16];
-    bool ok[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int64_t t = t0 + k0 + u * TP;
-      ok[u] = k0 + u * TP < UT && t < T;
-      if (!ok[u]) continue;
-      const size_t cs = (size_t)p.centver[t] * p.cstride;
-      const uint4* ck = reinterpret_cast<const uint4*>(
-          p.cent_k + cs + (size_t)load_idx(p.k_idx, t, Dm.idx_bytes) * D + 16 * sl);
-      const uint4* cw = reinterpret_cast<const uint4*>(
-          p.cent_v + cs + (size_t)load_idx(p.v_idx, t, Dm.idx_bytes) * D + 16 * sl);
-      const uint32_t kc = *reinterpret_cast<const uint32_t*>(p.k_codes + t * (D / 4) + 4 * sl);
-      const uint32_t vc = *reinterpret_cast<const uint32_t*>(p.v_codes + t * (D / 4) + 4 * sl);
-      const uint32_t kp = reinterpret_cast<const uint32_t*>(p.k_params)[t * Dm.ng + gi];
-      const uint32_t vp = reinterpret_cast<const uint32_t*>(p.v_params)[t * Dm.ng + gi];
-      add_residual(__ldg(ck), __ldg(ck + 1), kc, kp, kv[u]);
-      float vv[16];
-      add_residual(__ldg(cw), __ldg(cw + 1), vc, vp, vv);
-      store16(vh + t * D, vv);
-    }
-    if (r > 0) {
-      float cr[2][16];
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) cr[u][e] = 0.0f;
-      const int64_t ta = t0 + k0, tb = ta + TP;
-      const bool same0 = ok[0] && cv.tokver[ta] == ver0, same1 = ok[1] && cv.tokver[tb] == ver0;
-      const float sa = ok[0] ? h2f(p.k_cscale[ta]) : 0.0f, sb = ok[1] ? h2f(p.k_cscale[tb]) : 0.0f;
-      for (int q = 0; q < r; ++q) {
-        const float ca = ok[0] ? (float)p.k_coef[ta * r + q] * sa : 0.0f;
-        const float cb = ok[1] ? (float)p.k_coef[tb * r + q] * sb : 0.0f;
-        const float4* u4 = reinterpret_cast<const float4*>(Us + q * D + 16 * sl);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float4 x = u4[k];
-          cr[0][4 * k] = fmaf(x.x, ca, cr[0][4 * k]);
-          cr[0][4 * k + 1] = fmaf(x.y, ca, cr[0][4 * k + 1]);
-          cr[0][4 * k + 2] = fmaf(x.z, ca, cr[0][4 * k + 2]);
-          cr[0][4 * k + 3] = fmaf(x.w, ca, cr[0][4 * k + 3]);
-          cr[1][4 * k] = fmaf(x.x, cb, cr[1][4 * k]);
-          cr[1][4 * k + 1] = fmaf(x.y, cb, cr[1][4 * k + 1]);
-          cr[1][4 * k + 2] = fmaf(x.z, cb, cr[1][4 * k + 2]);
-          cr[1][4 * k + 3] = fmaf(x.w, cb, cr[1][4 * k + 3]);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        if (!ok[u]) continue;
-        const int64_t t = u ? tb : ta;
-        if (!(u ? same1 : same0)) {  // another version than the staged one
-          const float* U = basis_of(cv, Dm, cv.tokver[t], h) + (size_t)16 * sl * r;
-          const float cs = u ? sb : sa;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float a = 0.0f;
-            for (int q = 0; q < r; ++q)
-              a = fmaf(__ldg(U + e * r + q), (float)p.k_coef[t * r + q] * cs, a);
-            cr[u][e] = a;
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) kv[u][e] += cr[u][e];
-      }
-    }
-    if (ok[0]) store16(kh + (t0 + k0) * D, kv[0]);
-    if (ok[1]) store16(kh + (t0 + k0 + TP) * D, kv[1]);
-  }
-}
-
 // ------------------------------------------------------------------ host side
 int device_sms() {
   static int cache[64] = {0};
@@ -905,15 +784,6 @@ cudaError_t launch_merge(int D, const FlashArgs& a, int np, const int32_t* cu, i
   return cudaGetLastError();
 }
 
-cudaError_t launch_unpack(const Dims& D, const CacheView& v, int64_t T, int h0, int heads,
-                          uint16_t* K, uint16_t* V, cudaStream_t s) {
-  if (unpack_fast_supported(D)) return launch_unpack_fast(D, v, T, h0, heads, K, V, device_sms(), s);
-  const dim3 grid((unsigned)((T + UT - 1) / UT), (unsigned)heads);
-  if (D.d == 128) unpack_kernel<128><<<grid, 256, 0, s>>>(D, v, T, h0, K, V);
-  else unpack_kernel<64><<<grid, 256, 0, s>>>(D, v, T, h0, K, V);
-  return cudaGetLastError();
-}
-
 constexpr int64_t kMaxGridX = (int64_t(1) << 31) - 1;
 
 // Partials that a call may use: as many as 64 MiB hold, 64 at most.
@@ -946,7 +816,7 @@ SharedPlan plan_shared(const Dims& D, int64_t T, int Hq, int64_t n_q, int64_t n_
   const int64_t apart = (n_q * g + QT - 1) / QT, joined = n_seq * ((mq * g + QT - 1) / QT);
   p.joined = T == 0 || max_kv == 0 ? T == 0 : joined * 8 <= apart * 9;
   p.np = partials_of(n_q, Hq, d);
-  p.rows = T > 0 && p.np >= 8 && rows_supported(D, n_q * g);
+  p.rows = T > 0 && p.np >= 8 && rows_supported(D, T, n_q * g, device_sms());
   if (p.rows) p.joined = false;
   if (!p.joined && p.np < 2) p.np = 2;
   return p;
@@ -1112,7 +982,7 @@ extern "C" qwm_status qwm_attention_shared(const qwm_cache* c, const void* Q, in
       with0.len0 = T;
       if (!map_3d(&with0.k0, K0, D.d, T, D.d, nh, T * D.d, KT, 1) ||
           !map_3d(&with0.v0, V0, D.d, T, D.d, nh, T * D.d, KT, 1) ||
-          launch_unpack(D, v, T, h0, nh, K0, V0, s) != cudaSuccess)
+          launch_unpack(D, v, T, h0, nh, K0, V0, device_sms(), s) != cudaSuccess)
         return QWM_ERR_CUDA;
     }
     with0.head0 = h0;

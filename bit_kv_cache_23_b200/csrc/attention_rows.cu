@@ -39,7 +39,6 @@ constexpr int NW_ROWS = 12;     // warps of the attention (168 registers per thr
 constexpr int NW_UNPACK = 16;  // and of the unpacking
 constexpr int KT = 16;        // keys per tile
 constexpr int NSTAGE = 2;     // tiles in a warp's ring
-constexpr int MAX_R = 8;      // PSAC rank served here
 constexpr float TAU = 8.0f;   // a row's reference moves when its maximum grew by more (log2)
 
 struct RowsArgs {
@@ -47,8 +46,8 @@ struct RowsArgs {
   CacheView v;
   int64_t T;
   const uint16_t* Q;
-  int64_t ldq, rows;   // rows per head: tokens x query heads of a key head
-  int Hq, g;
+  int64_t ldq;
+  int rows, Hq, g;     // rows per head: tokens x query heads of a key head, 16 at most
   float scale_log2;
   float *ws_o, *ws_l;  // [slot][token][Hq][D], [slot][token][Hq]
   int64_t nq;
@@ -62,20 +61,26 @@ struct Stage {  // its fixed fields: code words and K's parameters
 };
 // Shared memory.  A stage holds the packed fields of a tile; where each begins
 // depends on the rank, the group size and the centroid numbers' width.
-template <int D, int NW>
+// RK: the rank, rounded up to 8 or 16 (the depth of the compensation's products).
+template <int D, int NW, int RK>
 struct RLay {
   static constexpr uint32_t OFF_ML = 0;                        // [warp][16] m, l
   static constexpr uint32_t OFF_Q = OFF_ML + 2 * NW * 16 * 4;  // [16][D] bf16
-  static constexpr uint32_t OFF_U = OFF_Q + 16 * D * 2;        // [D / 8][32] {high, middle, low, -}
-  static constexpr uint32_t OFF_ST = OFF_U + D / 8 * 32 * 16;  // [warp][NSTAGE] stages
-  static constexpr uint32_t MERGE = NW * 16 * D * 4;           // the warps' O
+  static constexpr uint32_t OFF_U = OFF_Q + 16 * D * 2;        // [D / 8][32] parts of U
+  static constexpr uint32_t OFF_ST = OFF_U + D / 8 * 32 * (RK == 8 ? 16 : 24);  // [warp][NSTAGE] stages
 };
+// Place of the low parts of U behind the others (RK = 16).
+template <int D>
+__host__ __device__ constexpr uint32_t u_low() { return D / 8 * 32 * 16; }
+// The warps' O of rows_kernel, over the tables' place.
+template <int D>
+constexpr uint32_t merge_bytes() { return NW_ROWS * 16 * D * 4; }
 struct Fields {  // offsets in a stage
   uint32_t vp, co, cs, ki, vi, stage, tab;  // and of the tables (or the warps' O) in shared memory
 };
-template <int D, int NW>
+template <int D, int NW, int RK>
 __host__ __device__ __forceinline__ Fields fields_of(const Dims& Dm) {
-  using L = RLay<D, NW>;
+  using L = RLay<D, NW, RK>;
   Fields f;
   f.vp = Stage<D>::KP + KT * Dm.ng * 4;
   f.co = f.vp + KT * Dm.ng * 4;
@@ -147,7 +152,7 @@ __device__ __forceinline__ Source<D> source_of(const Dims& Dm, const Fields& F, 
   const int half = lane >> 4, i = lane & 15;
   S.params = (const uint8_t*)(half ? p.v_params : p.k_params) + 16 * i;
   S.dst_params = (half ? F.vp : L::KP) + 16 * i;
-  // the short ones side by side: at most 8 + 2 + 2 + 2 lanes
+  // the short ones side by side: at most 16 + 2 + 2 + 2 lanes
   const int a = r, b = a + 2, c = b + ib, d = c + ib;  // ends, in pieces
   S.rest = nullptr;
   S.dst_rest = S.step_rest = 0;
@@ -213,8 +218,10 @@ __device__ __forceinline__ int k_channel(int c, int e) {
 }
 
 // U of head h, version ver, as B operands: n-tile j's column n is position
-// 2j + n % 2 of the lanes with c = n / 2.
-template <int D>
+// 2j + n % 2 of the lanes with c = n / 2.  A lane's pairs of components, 2c and 2c + 1
+// (and 2c + 8, 2c + 9), as {high, middle, low, -}, or {high, high, middle, middle}
+// and {low, low}.
+template <int D, int RK>
 __device__ __forceinline__ void stage_basis(const Dims& Dm, const CacheView& v, uint8_t* dst, int h,
                                             int ver) {
   const int r = Dm.r;
@@ -222,15 +229,24 @@ __device__ __forceinline__ void stage_basis(const Dims& Dm, const CacheView& v, 
   for (int e = threadIdx.x; e < D / 8 * 32; e += blockDim.x) {
     const int j = e >> 5, g = (e & 31) >> 2, c = e & 3;
     const float* u = U + (size_t)k_channel<D>(g >> 1, 2 * j + (g & 1)) * r + 2 * c;
-    float x = 2 * c < r ? __ldg(u) : 0.0f, y = 2 * c + 1 < r ? __ldg(u + 1) : 0.0f;
-    uint32_t part[3];
+    uint32_t part[RK / 8][3];
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      part[k] = pack_bf16(x, y);
-      x -= __uint_as_float(part[k] << 16);  // exact: the rounding's remainder
-      y -= __uint_as_float(part[k] & 0xffff0000u);
+    for (int i = 0; i < RK / 8; ++i) {
+      const int at = 2 * c + 8 * i;
+      float x = at < r ? __ldg(u + 8 * i) : 0.0f, y = at + 1 < r ? __ldg(u + 8 * i + 1) : 0.0f;
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        part[i][k] = pack_bf16(x, y);
+        x -= __uint_as_float(part[i][k] << 16);  // exact: the rounding's remainder
+        y -= __uint_as_float(part[i][k] & 0xffff0000u);
+      }
     }
-    reinterpret_cast<uint4*>(dst)[e] = make_uint4(part[0], part[1], part[2], 0);
+    if constexpr (RK == 8) {
+      reinterpret_cast<uint4*>(dst)[e] = make_uint4(part[0][0], part[0][1], part[0][2], 0);
+    } else {
+      reinterpret_cast<uint4*>(dst)[e] = make_uint4(part[0][0], part[1][0], part[0][1], part[1][1]);
+      reinterpret_cast<uint2*>(dst + u_low<D>())[e] = make_uint2(part[0][2], part[1][2]);
+    }
   }
 }
 
@@ -238,10 +254,44 @@ __device__ __forceinline__ uint32_t i8_pair_bf16(uint32_t two) {
   return pack_bf16(i8_to_f32((int8_t)(two & 0xff)), i8_to_f32((int8_t)(two >> 8)));
 }
 
+// A lane's coefficients of key k: components 2c, 2c + 1 (and 2c + 8, 2c + 9), as an A operand.
+template <int RK>
+__device__ __forceinline__ void coefs_of(const uint8_t* co, int k, int c, int r, uint32_t (&a)[RK / 8]) {
+#pragma unroll
+  for (int i = 0; i < RK / 8; ++i) {
+    const int at = 2 * c + 8 * i;
+    uint32_t two = 0;
+    if (r == RK) {
+      two = *reinterpret_cast<const uint16_t*>(co + k * RK + at);
+    } else {
+      if (at < r) two = co[k * r + at];
+      if (at + 1 < r) two |= (uint32_t)co[k * r + at + 1] << 8;
+    }
+    a[i] = i8_pair_bf16(two);
+  }
+}
+
+// sum_i U_i c8_i of keys g and g + 8 (a[0], a[1]) over n-tile j, from the lane's place
+// in the staged basis.
+template <int D, int RK>
+__device__ __forceinline__ void compensation(float (&d)[4], const uint32_t (&a)[2][RK / 8],
+                                             const uint8_t* us, int j) {
+  const uint4 u = *reinterpret_cast<const uint4*>(us + 16 * (threadIdx.x & 31) + j * 512);
+  if constexpr (RK == 8) {  // (the high and middle parts as one product of depth 16)
+    mma16_new(d, a[0][0], a[1][0], a[0][0], a[1][0], u.x, u.y);
+    mma8(d, a[0][0], a[1][0], u.z);
+  } else {
+    const uint2 l = *reinterpret_cast<const uint2*>(us + u_low<D>() + 8 * (threadIdx.x & 31) + j * 256);
+    mma16_new(d, a[0][0], a[1][0], a[0][1], a[1][1], u.x, u.y);
+    mma16(d, a[0][0], a[1][0], a[0][1], a[1][1], u.z, u.w);
+    mma16(d, a[0][0], a[1][0], a[0][1], a[1][1], l.x, l.y);
+  }
+}
+
 // S_i and M_i of one parameter word (positions 0 .. 3 of a code byte).  Scalar
 // fp32 here: the two-wide forms need their operands in register pairs, and the
-// moves that gather them cost more than they save (1860 against COUNT
-// instructions per 16 keys).
+// moves that gather them cost more than they save (399 against 328 us with 8 warps
+// at the size above).
 struct Decode {
   float s[4], m[4];
 };
@@ -282,12 +332,12 @@ __device__ __forceinline__ uint32_t piece_at(int row, int piece) {
 
 // One warp: keys [lo, hi) of the staged 16, all of the staged basis and table
 // version (the fields of other keys are not used).
-template <int D, bool TAB>
+template <int D, bool TAB, int RK>
 __device__ __forceinline__ void keys16(const RowsArgs& A, const Fields& F, const uint8_t* pk,
                                        const uint8_t* smem,
                                        const uint16_t* gk, const uint16_t* gv, int lo, int hi,
                                        State<D>& st) {
-  using L = RLay<D, NW_ROWS>;
+  using L = RLay<D, NW_ROWS, RK>;
   using St = Stage<D>;
   constexpr int KCH = D / 4;       // a lane's K channels
   constexpr int KW = KCH / 16;     // their code words
@@ -314,27 +364,19 @@ __device__ __forceinline__ void keys16(const RowsArgs& A, const Fields& F, const
   {
     int row[2];
     float cs[2];
-    uint32_t a[2];
+    uint32_t a[2][RK / 8];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int k = g + 8 * x;
       const bool live = k >= lo && k < hi;
       row[x] = number(F.ki, k, live);
       cs[x] = 0.0f;
-      a[x] = 0;
       if (r > 0) {
         cs[x] = live ? h2f(reinterpret_cast<const uint16_t*>(pk + F.cs)[k]) : 0.0f;
-        uint32_t two = 0;
-        if (r == MAX_R) {
-          two = reinterpret_cast<const uint16_t*>(pk + F.co)[k * (MAX_R / 2) + c];
-        } else {
-          if (2 * c < r) two = pk[F.co + k * r + 2 * c];
-          if (2 * c + 1 < r) two |= (uint32_t)pk[F.co + k * r + 2 * c + 1] << 8;
-        }
-        a[x] = i8_pair_bf16(two);
+        coefs_of<RK>(pk + F.co, k, c, r, a[x]);
       }
     }
-    const uint4* us = reinterpret_cast<const uint4*>(smem + L::OFF_U) + lane;
+    const uint8_t* us = smem + L::OFF_U;
     const uint4* qs = reinterpret_cast<const uint4*>(smem + L::OFF_Q) + lane;
 #pragma unroll
     for (int w = 0; w < KW; ++w) {
@@ -368,11 +410,7 @@ __device__ __forceinline__ void keys16(const RowsArgs& A, const Fields& F, const
           for (int y = 0; y < 2; ++y) {
             const int j = 2 * ks + y;
             float corr[4];
-            if (r > 0) {
-              const uint4 u = us[j * 32];
-              mma16_new(corr, a[0], a[1], a[0], a[1], u.x, u.y);
-              mma8(corr, a[0], a[1], u.z);
-            }
+            if (r > 0) compensation<D, RK>(corr, a, us, j);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               const uint32_t at = bytes[x];
@@ -536,10 +574,10 @@ __device__ __forceinline__ void stage_tables(const Dims& Dm, uint8_t* d, const u
 // versions, whose basis and tables are staged; one(pk, lo, hi, t, gk, gv) for each
 // tile, warp by warp: keys [lo, hi) of tile t with its fields at pk; gk, gv: the
 // head's tables in memory.
-template <int D, int NW, bool TAB, class One>
+template <int D, int NW, bool TAB, int RK, class One>
 __device__ __forceinline__ void walk(const Dims& Dm, const CacheView& v, const Fields& F, uint8_t* smem,
                                      int h, int64_t at, int64_t tend, One one) {
-  using L = RLay<D, NW>;
+  using L = RLay<D, NW, RK>;
   const int warp = threadIdx.x >> 5;
   uint8_t* const ring = smem + L::OFF_ST + warp * NSTAGE * F.stage;
   const uint32_t ring_at = smem_u32(ring);
@@ -558,7 +596,7 @@ __device__ __forceinline__ void walk(const Dims& Dm, const CacheView& v, const F
     }
     if (cvn != tabver || uv != uver) {
       __syncthreads();
-      if (uv != uver && Dm.r > 0) stage_basis<D>(Dm, v, smem + L::OFF_U, h, uv);
+      if (uv != uver && Dm.r > 0) stage_basis<D, RK>(Dm, v, smem + L::OFF_U, h, uv);
       if (cvn != tabver) {
         const size_t off = (size_t)cvn * cent_slot_elems(Dm) + (size_t)h * Dm.C * D;
         gk = v.cent_k + off;
@@ -587,16 +625,15 @@ __device__ __forceinline__ void walk(const Dims& Dm, const CacheView& v, const F
   }
 }
 
-template <int D, bool TAB>
+template <int D, bool TAB, int RK>
 __global__ void __launch_bounds__(32 * NW_ROWS, 1) rows_kernel(const __grid_constant__ RowsArgs A) {
   constexpr int NW = NW_ROWS;
-  using L = RLay<D, NW>;
+  using L = RLay<D, NW, RK>;
   extern __shared__ __align__(128) uint8_t smem[];
   const Dims& Dm = A.Dm;
-  const Fields F = fields_of<D, NW>(Dm);
+  const Fields F = fields_of<D, NW, RK>(Dm);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int64_t x0 = blockIdx.x * A.total / gridDim.x, x1 = (blockIdx.x + 1) * A.total / gridDim.x;
-  const int64_t r0 = (int64_t)blockIdx.y * 16;  // first row of this row tile
   State<D> st;
   for (int64_t x = x0; x < x1;) {
     const int h = (int)(x / A.nt);
@@ -608,12 +645,11 @@ __global__ void __launch_bounds__(32 * NW_ROWS, 1) rows_kernel(const __grid_cons
       const int ks = e >> 5, gg = (e & 31) >> 2, cc = e & 3;
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        const int64_t r = r0 + gg + 8 * y;
+        const int r = gg + 8 * y;
         uint2 q = make_uint2(0, 0);
         if (r < A.rows) {
-          const int64_t tok = r / A.g;
-          q = __ldg(reinterpret_cast<const uint2*>(A.Q + tok * A.ldq +
-                                                   ((int64_t)h * A.g + (r - tok * A.g)) * D +
+          const int tok = r / A.g;
+          q = __ldg(reinterpret_cast<const uint2*>(A.Q + tok * A.ldq + (h * A.g + (r - tok * A.g)) * D +
                                                    k_channel<D>(cc, 4 * ks)));
         }
         reinterpret_cast<uint32_t*>(smem + L::OFF_Q)[e * 4 + y] = q.x;
@@ -628,9 +664,9 @@ __global__ void __launch_bounds__(32 * NW_ROWS, 1) rows_kernel(const __grid_cons
       for (int e = 0; e < 4; ++e) st.o[j][e] = 0.0f;
     const int64_t at = (x - head0) * KT;
     const int64_t tend = (end - head0) * KT < A.T ? (end - head0) * KT : A.T;
-    walk<D, NW, TAB>(Dm, A.v, F, smem, h, at, tend,
+    walk<D, NW, TAB, RK>(Dm, A.v, F, smem, h, at, tend,
                      [&](const uint8_t* pk, int lo, int hi, int64_t, const uint16_t* gk, const uint16_t* gv) {
-                       keys16<D, TAB>(A, F, pk, smem, gk, gv, lo, hi, st);
+                       keys16<D, TAB, RK>(A, F, pk, smem, gk, gv, lo, hi, st);
                      });
     x = end;
     // ---- the warps' results: maxima and sums, then O over the tables' place
@@ -658,8 +694,7 @@ __global__ void __launch_bounds__(32 * NW_ROWS, 1) rows_kernel(const __grid_cons
     const int slot = (int)(blockIdx.x - cta_of(A, head0));
     for (int e = threadIdx.x; e < 16 * D; e += 32 * NW) {
       const int row = e / D, ch = e % D;
-      const int64_t r = r0 + row;
-      if (r >= A.rows) break;  // rows ascend
+      if (row >= A.rows) break;  // rows ascend
       float top = -INFINITY;
 #pragma unroll
       for (int w = 0; w < NW; ++w) top = fmaxf(top, ml[w * 16 + row]);
@@ -671,8 +706,8 @@ __global__ void __launch_bounds__(32 * NW_ROWS, 1) rows_kernel(const __grid_cons
         l = fmaf(f, ml[NW * 16 + w * 16 + row], l);
         o = fmaf(f, ow[(w * 16 + row) * D + ch], o);
       }
-      const int64_t tok = r / A.g;
-      const int64_t out = tok * A.Hq + (int64_t)h * A.g + (r - tok * A.g);
+      const int tok = row / A.g;
+      const int64_t out = (int64_t)tok * A.Hq + h * A.g + (row - tok * A.g);
       A.ws_o[((size_t)slot * A.nq * A.Hq + out) * D + ch] = o / l;
       if (ch == 0) {
         A.ws_l[(size_t)slot * A.nq * A.Hq + out] = (top + log2f(l)) * 0.6931471805599453f;
@@ -702,7 +737,7 @@ __device__ __forceinline__ void store32(uint16_t* dst, const uint32_t (&w)[8]) {
                : "memory");
 }
 
-template <int D, bool TAB>
+template <int D, bool TAB, int RK>
 __device__ __forceinline__ void unpack16(const UnpackArgs& A, const Fields& F, const uint8_t* pk,
                                          const uint8_t* smem, const uint16_t* gk, const uint16_t* gv,
                                          int lo, int hi, uint16_t* K, uint16_t* V) {
@@ -716,7 +751,7 @@ __device__ __forceinline__ void unpack16(const UnpackArgs& A, const Fields& F, c
   const uint8_t* tvv = tk + Dm.C * D * 2;
   uint32_t one;
   asm volatile("mov.b32 %0, 0x3F800000;" : "=r"(one));
-  uint32_t a[2] = {0, 0};
+  uint32_t a[2][RK / 8];
   float cs[2] = {0.0f, 0.0f};
   bool live[2];
 #pragma unroll
@@ -725,17 +760,10 @@ __device__ __forceinline__ void unpack16(const UnpackArgs& A, const Fields& F, c
     live[x] = k >= lo && k < hi;
     if (r > 0) {
       cs[x] = h2f(reinterpret_cast<const uint16_t*>(pk + F.cs)[k]);
-      uint32_t two = 0;
-      if (r == MAX_R) {
-        two = reinterpret_cast<const uint16_t*>(pk + F.co)[k * (MAX_R / 2) + c];
-      } else {
-        if (2 * c < r) two = pk[F.co + k * r + 2 * c];
-        if (2 * c + 1 < r) two |= (uint32_t)pk[F.co + k * r + 2 * c + 1] << 8;
-      }
-      a[x] = i8_pair_bf16(two);
+      coefs_of<RK>(pk + F.co, k, c, r, a[x]);
     }
   }
-  const uint4* us = reinterpret_cast<const uint4*>(smem + RLay<D, NW_UNPACK>::OFF_U) + lane;
+  const uint8_t* us = smem + RLay<D, NW_UNPACK, RK>::OFF_U;
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv) {
     const bool comp = kv == 0 && r > 0;
@@ -773,11 +801,7 @@ __device__ __forceinline__ void unpack16(const UnpackArgs& A, const Fields& F, c
         for (int y = 0; y < 4; ++y) {  // pair of channels 2y, 2y + 1 of the piece
           const int j = 8 * w + 4 * hf + y;
           float corr[4];
-          if (comp) {
-            const uint4 u = us[j * 32];
-            mma16_new(corr, a[0], a[1], a[0], a[1], u.x, u.y);
-            mma8(corr, a[0], a[1], u.z);
-          }
+          if (comp) compensation<D, RK>(corr, a, us, j);
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const uint32_t at = hf == 0 ? (y < 2 ? code_byte<0>(code[x]) : code_byte<1>(code[x]))
@@ -803,10 +827,10 @@ __device__ __forceinline__ void unpack16(const UnpackArgs& A, const Fields& F, c
   }
 }
 
-template <int D, bool TAB>
+template <int D, bool TAB, int RK>
 __global__ void __launch_bounds__(32 * NW_UNPACK, 1) unpack_kernel(const __grid_constant__ UnpackArgs A) {
   extern __shared__ __align__(128) uint8_t smem[];
-  const Fields F = fields_of<D, NW_UNPACK>(A.Dm);
+  const Fields F = fields_of<D, NW_UNPACK, RK>(A.Dm);
   const int64_t x0 = blockIdx.x * A.total / gridDim.x, x1 = (blockIdx.x + 1) * A.total / gridDim.x;
   for (int64_t x = x0; x < x1;) {
     const int hr = (int)(x / A.nt);  // head of this call
@@ -815,11 +839,11 @@ __global__ void __launch_bounds__(32 * NW_UNPACK, 1) unpack_kernel(const __grid_
     const int64_t tend = (end - head0) * KT < A.T ? (end - head0) * KT : A.T;
     uint16_t* const K = A.K + (size_t)hr * A.T * D;
     uint16_t* const V = A.V + (size_t)hr * A.T * D;
-    walk<D, NW_UNPACK, TAB>(
+    walk<D, NW_UNPACK, TAB, RK>(
         A.Dm, A.v, F, smem, A.h0 + hr, (x - head0) * KT, tend,
         [&](const uint8_t* pk, int lo, int hi, int64_t t, const uint16_t* gk, const uint16_t* gv) {
           const size_t o = (size_t)t * KT * D;
-          unpack16<D, TAB>(A, F, pk, smem, gk, gv, lo, hi, K + o, V + o);
+          unpack16<D, TAB, RK>(A, F, pk, smem, gk, gv, lo, hi, K + o, V + o);
         });
     __syncthreads();  // the tables are done with
     x = end;
@@ -828,39 +852,64 @@ __global__ void __launch_bounds__(32 * NW_UNPACK, 1) unpack_kernel(const __grid_
 
 constexpr uint32_t kMostSmem = 227 * 1024;
 
-template <int D, bool TAB>
-cudaError_t launch_rows(const RowsArgs& a, int grid, int tiles, cudaStream_t s) {
+template <int D, bool TAB, int RK>
+cudaError_t launch_rows(const RowsArgs& a, int grid, cudaStream_t s) {
   uint32_t tab = TAB ? 2u * a.Dm.C * D * 2 : 0u;
-  if (tab < RLay<D, NW_ROWS>::MERGE) tab = RLay<D, NW_ROWS>::MERGE;
-  const uint32_t bytes = fields_of<D, NW_ROWS>(a.Dm).tab + tab;
+  if (tab < merge_bytes<D>()) tab = merge_bytes<D>();
+  const uint32_t bytes = fields_of<D, NW_ROWS, RK>(a.Dm).tab + tab;
   if (bytes > kMostSmem) return cudaErrorInvalidConfiguration;
   static std::atomic<uint64_t> allowed{0};
-  const cudaError_t e = allow_smem(rows_kernel<D, TAB>, allowed, (int)kMostSmem);
+  const cudaError_t e = allow_smem(rows_kernel<D, TAB, RK>, allowed, (int)kMostSmem);
   if (e != cudaSuccess) return e;
-  rows_kernel<D, TAB><<<dim3((unsigned)grid, (unsigned)tiles), 32 * NW_ROWS, bytes, s>>>(a);
+  rows_kernel<D, TAB, RK><<<(unsigned)grid, 32 * NW_ROWS, bytes, s>>>(a);
   return cudaGetLastError();
 }
 
-template <int D, bool TAB>
+template <int D, bool TAB, int RK>
 cudaError_t launch_unpack(const UnpackArgs& a, int grid, cudaStream_t s) {
   const uint32_t tab = TAB ? 2u * a.Dm.C * D * 2 : 0u;
-  const uint32_t bytes = fields_of<D, NW_UNPACK>(a.Dm).tab + tab;
+  const uint32_t bytes = fields_of<D, NW_UNPACK, RK>(a.Dm).tab + tab;
   if (bytes > kMostSmem) return cudaErrorInvalidConfiguration;
   static std::atomic<uint64_t> allowed{0};
-  const cudaError_t e = allow_smem(unpack_kernel<D, TAB>, allowed, (int)kMostSmem);
+  const cudaError_t e = allow_smem(unpack_kernel<D, TAB, RK>, allowed, (int)kMostSmem);
   if (e != cudaSuccess) return e;
-  unpack_kernel<D, TAB><<<(unsigned)grid, 32 * NW_UNPACK, bytes, s>>>(a);
+  unpack_kernel<D, TAB, RK><<<(unsigned)grid, 32 * NW_UNPACK, bytes, s>>>(a);
   return cudaGetLastError();
 }
 
 // Both centroid tables of a head fit in shared memory beside the rest.
 bool tables_fit(const Dims& D) { return (int64_t)D.C * D.d <= 32768; }
 
+// f.operator()<D, TAB, RK>() of the variant that serves a cache.
+template <class F>
+cudaError_t variant(const Dims& D, F f) {
+  const bool tab = tables_fit(D), deep = D.r > 8;
+  if (D.d == 128) {
+    if (tab) return deep ? f.template run<128, true, 16>() : f.template run<128, true, 8>();
+    return deep ? f.template run<128, false, 16>() : f.template run<128, false, 8>();
+  }
+  if (tab) return deep ? f.template run<64, true, 16>() : f.template run<64, true, 8>();
+  return deep ? f.template run<64, false, 16>() : f.template run<64, false, 8>();
+}
+
+struct RunRows {
+  const RowsArgs& a;
+  int grid;
+  cudaStream_t s;
+  template <int D, bool TAB, int RK>
+  cudaError_t run() { return launch_rows<D, TAB, RK>(a, grid, s); }
+};
+struct RunUnpack {
+  const UnpackArgs& a;
+  int grid;
+  cudaStream_t s;
+  template <int D, bool TAB, int RK>
+  cudaError_t run() { return launch_unpack<D, TAB, RK>(a, grid, s); }
+};
+
 }  // namespace
 
-bool unpack_fast_supported(const Dims& D) { return D.r <= MAX_R; }
-
-cudaError_t launch_unpack_fast(const Dims& D, const CacheView& v, int64_t T, int h0, int heads, uint16_t* K,
+cudaError_t launch_unpack(const Dims& D, const CacheView& v, int64_t T, int h0, int heads, uint16_t* K,
                                uint16_t* V, int sms, cudaStream_t s) {
   UnpackArgs a = {};
   a.Dm = D;
@@ -873,14 +922,18 @@ cudaError_t launch_unpack_fast(const Dims& D, const CacheView& v, int64_t T, int
   a.V = V;
   const int64_t most = (a.total + NW_UNPACK - 1) / NW_UNPACK;  // CTAs with a tile for every warp
   const int grid = (int)(most < sms ? most : sms);
-  if (D.d == 128)
-    return tables_fit(D) ? launch_unpack<128, true>(a, grid, s) : launch_unpack<128, false>(a, grid, s);
-  return tables_fit(D) ? launch_unpack<64, true>(a, grid, s) : launch_unpack<64, false>(a, grid, s);
+  return variant(D, RunUnpack{a, grid, s});
 }
 
-// At most this many rows per head run here: up to two 16-row tiles, which decode
-// the history once each.
-bool rows_supported(const Dims& D, int64_t rows) { return D.r <= MAX_R && rows <= 32; }
+// Rows of one product, and a history that gives every warp two tiles.  Otherwise the
+// history is unpacked and attended to as bf16: at 40 heads x 37440 tokens 16 rows
+// take 249 us here and 354 us there, and a second row tile, decoding all again,
+// 463 against 356 us; over 12 x 7919 tokens (3.3 tiles a warp) 8 rows take 50 and
+// 53 us, over 4 x 1560 (a tile for every fourth warp) 34.5 and 33.5 us, one row over
+// 1 x 7919 40 and 32 us.
+bool rows_supported(const Dims& D, int64_t T, int64_t rows, int sms) {
+  return rows <= 16 && (T + KT - 1) / KT * D.H >= 2 * (int64_t)NW_ROWS * sms;
+}
 
 RowsPlan rows_plan(const Dims& D, int64_t T, int sms, int most) {
   RowsPlan p;
@@ -904,7 +957,7 @@ cudaError_t launch_rows(const Dims& D, const CacheView& v, int64_t T, const uint
   a.Q = Q;
   a.ldq = ldq;
   a.g = Hq / D.H;
-  a.rows = nq * a.g;
+  a.rows = (int)(nq * a.g);
   a.Hq = Hq;
   a.scale_log2 = scale_log2;
   a.ws_o = ws_o;
@@ -913,11 +966,7 @@ cudaError_t launch_rows(const Dims& D, const CacheView& v, int64_t T, const uint
   a.nslot = plan.slots;
   a.nt = (T + KT - 1) / KT;
   a.total = a.nt * D.H;
-  const bool tab = tables_fit(D);
-  const int tiles = (int)((a.rows + 15) / 16);
-  if (D.d == 128)
-    return tab ? launch_rows<128, true>(a, plan.grid, tiles, s) : launch_rows<128, false>(a, plan.grid, tiles, s);
-  return tab ? launch_rows<64, true>(a, plan.grid, tiles, s) : launch_rows<64, false>(a, plan.grid, tiles, s);
+  return variant(D, RunRows{a, plan.grid, s});
 }
 
 }  // namespace qwm

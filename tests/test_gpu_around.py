@@ -236,7 +236,7 @@ def test_shared_history_is_the_reconstruction(C, G, r, d):
     bit.  The compensation's r products are summed in another order, so before the one rounding a key
     element may be off by (r + 4) 2^-24 of sum |U c| <= 2 |K'| or so; the rounding then falls the other
     way, by one step, where the sum lies that near a border between two bf16 values, 2^-7 |K'| apart: for
-    at most 2 (8 + 4) 2^-24 2 / 2^-7 = 4e-4 of the elements."""
+    at most 2 (r + 4) 2^-24 2 / 2^-7 = (r + 4) 2^-15 of the elements (6e-4 at r = 16)."""
     c, Kp, Vp, rows, kv, table, Q, cu, lens = _shared_case(d, 2, 1, 701, (70,), (20,), 16, False, 5, C=C, G=G, r=r)
     full = q.qwm_attention_shared_workspace(c.c, Q.shape[0], 2, 1, 70, 20)[1]
     ws = torch.zeros(full, dtype=torch.uint8, device="cuda")
@@ -246,27 +246,41 @@ def test_shared_history_is_the_reconstruction(C, G, r, d):
     tail = ws[full - 4 * n:].view(torch.int16)
     assert torch.equal(tail[n:].view(2, 701, d), Vp.view(torch.int16))
     off = (tail[:n].view(2, 701, d).int() - Kp.view(torch.int16).int()).abs()
-    assert off.max() <= (1 if 0 < r <= 8 else 0) and (off > 0).double().mean() <= 4e-4, (off.max(), (off > 0).sum())
+    assert off.max() <= (1 if r else 0) and (off > 0).double().mean() <= (r + 4) / 2**15, (off.max(), (off > 0).sum())
 
 
-@pytest.mark.parametrize("C,G,r,d,T,rows", [
-    (256, 32, 8, 128, 4000, 8),     # both tables in shared memory; keys of two basis versions in one tile
-    (300, 32, 8, 128, 1000, 16),    # tables read through the cache, 16-bit centroid numbers
-    (512, 16, 3, 64, 1500, 32),     # two row tiles
-    (40, 16, 8, 128, 129, 1),       # a chunk of one key
-    (16, 32, 1, 64, 1, 5),          # a single key
-    (64, 32, 0, 128, 777, 17),      # no compensation
-    (64, 32, 9, 128, 777, 17),      # a rank that the few-row kernel does not serve
+@pytest.mark.parametrize("H,C,G,r,d,T,rows", [
+    (3, 256, 32, 8, 128, 4000, 8),     # both tables in shared memory; keys of two basis versions in one tile
+    (3, 300, 32, 8, 128, 1000, 16),    # tables read through the cache, 16-bit centroid numbers
+    (3, 512, 16, 3, 64, 1500, 32),
+    (3, 40, 16, 8, 128, 129, 1),       # a chunk of one key
+    (3, 16, 32, 1, 64, 1, 5),          # a single key
+    (3, 64, 32, 0, 128, 777, 17),      # no compensation
+    (3, 64, 32, 9, 128, 777, 17),      # an odd rank above 8
+    (3, 256, 16, 16, 128, 700, 3),     # the largest rank and tables that shared memory takes
+    (3, 512, 16, 16, 64, 700, 16),
+    (3, 512, 32, 12, 128, 700, 16),
+    # as many tiles as the few-row kernel wants (two for every warp of the GPU, below 3600)
+    (2, 256, 16, 16, 128, 28801, 3),
+    (2, 256, 32, 8, 128, 28809, 16),
+    (2, 256, 32, 8, 128, 28809, 17),   # a row more than it takes
+    (2, 300, 32, 8, 128, 28800, 16),
+    (1, 512, 16, 3, 64, 57631, 7),
+    (2, 512, 16, 12, 64, 28823, 1),
+    (5, 64, 32, 0, 128, 11537, 5),
+    (100, 40, 16, 5, 128, 577, 2),     # a block's run of tiles crosses heads
+    (1200, 16, 32, 8, 64, 48, 16),     # many heads in a block's run, a table and basis for each
+    (3700, 16, 16, 4, 64, 1, 1),       # a key per head
 ])
-def test_few_rows_over_the_history(C, G, r, d, T, rows):
-    H, g = 3, _gen(C + T)
+def test_few_rows_over_the_history(H, C, G, r, d, T, rows):
+    g = _gen(C + T)
     c = _cache(g, H, d, T, C, G, r)
     Kp, Vp = c.reconstruct()
     Q = randn(g, rows, H, d).to(BF16)
     lse = torch.empty(rows, H, device="cuda")
     O = c.attention_shared(Q, ints([0, rows]), rows, lse=lse)
     _fine()
-    for h in range(H):
+    for h in range(H) if H <= 5 else range(0, H, H // 50):
         want, bound, wl, lb = attend(Q[:, h], Kp[h], Vp[h], 1 / math.sqrt(d))
         check("O", O[:, h], want, bound)
         check_lse("lse", lse[:, h], wl, lb)
