@@ -336,10 +336,10 @@ def _mat_ptr(t, name, index, dtype, n=None, m=None):
     return t.data_ptr()
 
 
-def _new(shape, x, stream):
-    """A contiguous bf16 tensor beside x, allocated on the current stream and, where
-    another one is given, used there."""
-    o = x.new_empty(shape)
+def _new(x, stream):
+    """A contiguous tensor like x, allocated on the current stream and, where another
+    one is given, used there."""
+    o = torch.empty_like(x, memory_format=torch.contiguous_format)
     return o if stream is None else _held(stream, o)
 
 
@@ -429,7 +429,7 @@ def qwm_norm_rope(rope: qwm_rope | None, Q: torch.Tensor | None, K: torch.Tensor
             raise ValueError("Q and K differ in rows or head_dim")
         n, h, d = shape
         if o is None:
-            o = _new(shape, x, stream)
+            o = _new(x, stream)
             po, ldo = o.data_ptr(), max(h * d, 8)
         else:
             po, ldo = _rows_ptr(o, name + "_out", index)
@@ -470,7 +470,7 @@ def _lse_ptr(lse, n, heads, index):
 
 def _out(O, Q, index, stream):
     if O is None:
-        return _new(Q.shape, Q, stream)
+        return _new(Q, stream)
     if (not isinstance(O, torch.Tensor) or O.dtype is not _BF16 or O.get_device() != index
             or O.shape != Q.shape or not O.is_contiguous()):
         _refuse(O, "O", index, _BF16, f"{tuple(Q.shape)} as Q has")
@@ -481,7 +481,11 @@ def _scratch(workspace, sizes, Q, index, stream):
     """(tensor, pointer, bytes): the caller's workspace, or one for this call of the
     full size that sizes() gives."""
     if workspace is None:
-        nbytes = sizes()[1]
+        if torch.cuda.current_device() == index:
+            nbytes = sizes()[1]
+        else:
+            with torch.cuda.device(index):
+                nbytes = sizes()[1]
         if nbytes == 0:
             return None, None, 0
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=Q.device)

@@ -685,36 +685,40 @@ __global__ void __launch_bounds__(256) merge_kernel(const float* __restrict__ ws
 
 // ------------------------------------------------------------------ host side
 int device_sms() {
-  static int cache[64] = {0};
-  int dev = 0;
+  static std::atomic<int> known[64];
+  int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-  if (!cache[dev]) {
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
-      n = 148;
-    cache[dev] = n;
+  n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) n = 148;
+    known[dev].store(n, std::memory_order_relaxed);
   }
-  return cache[dev];
+  return n;
 }
 
 // How a launch divides its work: row blocks per sequence, key ranges per row block.
 struct Blocks {
   int qblocks, nsplit;
+  double cost;  // in key tiles of a CTA
 };
 
 // rows: of a sequence; units: sequences times key heads; ntile: key tiles; most:
-// key ranges at most.  The key ranges are the count that minimizes (rounds of CTAs
-// on the GPU) x (tiles per range + a fixed cost of 8 tiles).
-Blocks blocks_of(int64_t rows, int64_t units, int64_t ntile, int most) {
+// key ranges at most; merged: the result is a partial in any case.  The key ranges
+// are the count that minimizes (rounds of CTAs on the GPU) x (tiles per range + a
+// fixed cost of 8 tiles) + 8 tiles for a merge's launch that one range does not need:
+// a tile of few rows takes 0.76 us (eight single rows x 12 heads over 512 keys: 12.3
+// us whole, 15.2 us in two ranges; over 1000 keys 18.4 us whole, 17.8 us in three).
+Blocks blocks_of(int64_t rows, int64_t units, int64_t ntile, int most, bool merged) {
   Blocks b;
   b.qblocks = (int)((rows + QT - 1) / QT);
   const int64_t ctas = units * b.qblocks, slots = 2 * (int64_t)device_sms();
   b.nsplit = 1;
-  double bestc = 1e300;
+  b.cost = 1e300;
   for (int s = 1; s <= most && s * 4 <= (ntile > 4 ? ntile : 4); ++s) {
-    const double c = (double)((ctas * s + slots - 1) / slots) * ((double)ntile / s + 8.0);
-    if (c < bestc * 0.98) {
-      bestc = c;
+    const double c = (double)((ctas * s + slots - 1) / slots) * ((double)ntile / s + 8.0) +
+                     (merged || s > 1 ? 8.0 : 0.0);
+    if (c < b.cost * 0.98) {
+      b.cost = c;
       b.nsplit = s;
     }
   }
@@ -803,22 +807,37 @@ size_t partial_bytes(int np, int64_t n_q, int Hq, int d) {
 // pack into common row blocks for the history, which few rows per branch would
 // leave mostly empty, the own keys follow per branch, and the two are merged.
 // With few rows in all the history is not unpacked at all (attention_rows.cu).
+// Between the first two the costs of blocks_of decide.
 struct SharedPlan {
-  bool joined, rows;
-  int np;  // partials that the workspace holds
+  bool rows, joined;
+  int np;          // partials that the workspace holds
+  Blocks all;      // joined
+  Blocks own;      // not joined; no key range: no own keys
+  Blocks history;  // not joined, not rows
 };
 
 SharedPlan plan_shared(const Dims& D, int64_t T, int Hq, int64_t n_q, int64_t n_seq, int64_t max_q,
                        int64_t max_kv) {
-  SharedPlan p;
-  const int g = Hq / D.H, d = D.d;
+  SharedPlan p = {};
+  const int g = Hq / D.H;
   const int64_t mq = max_q < n_q ? max_q : n_q;
-  const int64_t apart = (n_q * g + QT - 1) / QT, joined = n_seq * ((mq * g + QT - 1) / QT);
-  p.joined = T == 0 || max_kv == 0 ? T == 0 : joined * 8 <= apart * 9;
-  p.np = partials_of(n_q, Hq, d);
-  p.rows = T > 0 && p.np >= 8 && rows_supported(D, T, n_q * g, device_sms());
-  if (p.rows) p.joined = false;
-  if (!p.joined && p.np < 2) p.np = 2;
+  const int64_t tiles0 = (T + KT - 1) / KT, tiles1 = (max_kv + KT - 1) / KT;
+  p.np = partials_of(n_q, Hq, D.d);
+  p.rows = p.np >= 8 && rows_supported(D, T, n_q * g, device_sms());
+  p.all = blocks_of(mq * g, D.H * n_seq, tiles0 + tiles1, p.np < 2 ? 1 : p.np, false);
+  if (p.rows || T > 0) {
+    const int np = p.np < 2 ? 2 : p.np;
+    double cost = 0.0;
+    if (max_kv > 0) {
+      p.own = blocks_of(mq * g, D.H * n_seq, tiles1, np / 2, true);
+      cost = p.own.cost;
+    }
+    p.history = blocks_of(n_q * g, D.H, tiles0, np - p.own.nsplit, true);
+    p.joined = !p.rows && p.all.cost <= cost + p.history.cost;
+    if (!p.joined) p.np = np;
+  } else {
+    p.joined = true;
+  }
   return p;
 }
 
@@ -896,10 +915,9 @@ extern "C" qwm_status qwm_attention_shared(const qwm_cache* c, const void* Q, in
 
   const int g = heads_q / D.H;
   const int64_t T = c->len;
-  const SharedPlan plan = plan_shared(D, T, heads_q, n_q, n_seq, max_q, max_kv);
+  SharedPlan plan = plan_shared(D, T, heads_q, n_q, n_seq, max_q, max_kv);
   const CacheView v = view_of(c);
   const cudaStream_t s = (cudaStream_t)stream;
-  const int64_t mq = max_q < n_q ? max_q : n_q;
   FlashArgs a = {};
   a.Q = (const uint16_t*)Q;
   a.ldq = ldq;
@@ -945,33 +963,35 @@ extern "C" qwm_status qwm_attention_shared(const qwm_cache* c, const void* Q, in
   // passes of even size
   const int passes = (D.H + hp - 1) / hp;
   hp = (D.H + passes - 1) / passes;
+  const int64_t mq = max_q < n_q ? max_q : n_q;
   const int64_t tiles0 = (T + KT - 1) / KT, tiles1 = (max_kv + KT - 1) / KT;
+  if (passes > 1) {
+    plan.all = blocks_of(mq * g, hp * n_seq, tiles0 + tiles1, plan.np < 2 ? 1 : plan.np, false);
+    plan.history = blocks_of(n_q * g, hp, tiles0, plan.np - plan.own.nsplit, true);
+  }
   int np = 0;
-  Blocks bo = {};
   const auto set = [](FlashArgs& f, const Blocks& b) {
     f.qblocks = b.qblocks;
     f.nsplit = b.nsplit;
   };
   if (plan.joined) {
-    bo = blocks_of(mq * g, hp * n_seq, tiles0 + tiles1, plan.np < 2 ? 1 : plan.np);
-    set(own, bo);
-    own.part0 = bo.nsplit > 1 ? 0 : -1;
-    np = bo.nsplit > 1 ? bo.nsplit : 0;
+    set(own, plan.all);
+    np = own.nsplit > 1 ? own.nsplit : 0;
+    own.part0 = np > 0 ? 0 : -1;
   } else {
-    if (pages && max_kv > 0) bo = blocks_of(mq * g, D.H * n_seq, tiles1, plan.np / 2);
-    set(own, bo);
+    set(own, plan.own);
     if (plan.rows) {
-      const RowsPlan rp = rows_plan(D, T, device_sms(), plan.np - bo.nsplit);
+      const RowsPlan rp = rows_plan(D, T, device_sms(), plan.np - own.nsplit);
       a.nsplit = rp.slots;
       if (launch_rows(D, v, T, a.Q, ldq, n_q, heads_q, a.scale_log2, rp, a.ws_o, a.ws_l, s) != cudaSuccess)
         return QWM_ERR_CUDA;
     } else {
       a.max_q = n_q;
-      set(a, blocks_of(n_q * g, hp, tiles0, plan.np - bo.nsplit));
+      set(a, plan.history);
     }
     a.part0 = 0;
     own.part0 = a.nsplit;
-    np = a.nsplit + bo.nsplit;
+    np = a.nsplit + own.nsplit;
   }
   FlashArgs& with0 = plan.joined ? own : a;
   for (int h0 = 0; h0 < D.H && !plan.rows; h0 += hp) {
@@ -1004,7 +1024,7 @@ extern "C" qwm_status qwm_cross_attention_workspace(int32_t heads_q, int32_t hea
     return QWM_ERR_INVALID_ARG;
   const int64_t mq = max_q < n_q ? max_q : n_q;
   const int np = blocks_of(mq * (heads_q / heads_kv), heads_kv * n_seq, (max_kv + KT - 1) / KT,
-                           partials_of(n_q, heads_q, head_dim))
+                           partials_of(n_q, heads_q, head_dim), false)
                      .nsplit;
   *least = 0;
   *full = np > 1 ? partial_bytes(np, n_q, heads_q, head_dim) : 0;
@@ -1057,7 +1077,7 @@ extern "C" qwm_status qwm_cross_attention(const void* Q, int64_t ldq, int64_t n_
   a.lse = lse;
   const bool parts = full > 0 && workspace && workspace_bytes >= full;
   const Blocks b = blocks_of(mq * g, heads_kv * n_seq, (max_kv + KT - 1) / KT,
-                             parts ? partials_of(n_q, heads_q, head_dim) : 1);
+                             parts ? partials_of(n_q, heads_q, head_dim) : 1, false);
   a.qblocks = b.qblocks;
   a.nsplit = b.nsplit;
   a.part0 = -1;
