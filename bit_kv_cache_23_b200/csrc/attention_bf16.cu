@@ -441,15 +441,17 @@ __device__ __forceinline__ void issue_tile(const FlashArgs& A, const Work& w, in
   }
 }
 
-// One warp: K and V of the tiles in turn.
+// One warp: K and V of the tiles, in the order in which the products free their
+// places (S 0, S 1, P V 0, S 2, P V 1, S 3, ...).  (In the order of the keys K of the
+// tile after the next waited behind V of the next, and came late: 259 us against 248
+// at 1560 rows x 40 heads over 8192 keys.)
 template <int D>
 __device__ __forceinline__ void load_role(const FlashArgs& A, uint8_t* smem, uint64_t* bars,
                                           const Work& w) {
   using L = Lay<D>;
   const int lane = threadIdx.x & 31;
   const uint32_t base = smem_u32(smem);
-  bool ok = true;
-  int rag = 0, e = 0;  // e = 2 t: K of tile t; e = 2 t + 1: its V
+  int rag = 0, done[2] = {0, 0};  // ragged tiles so far; tiles of K and V on their way
   if (A.qtma) {
     // boxes of 64 channels, the key head's g query heads and 128 / g tokens; rows of
     // no row of this CTA are computed with and not stored
@@ -462,12 +464,10 @@ __device__ __forceinline__ void load_role(const FlashArgs& A, uint8_t* smem, uin
     }
     __syncwarp();
   }
-  for (; e < 2 * w.n; ++e) {
-    const int t = e >> 1, v = e & 1, at = t & 1;
-    if (t >= 2 && !warp_wait(&bars[(v ? L::B_PV : L::B_S) + at], ((t >> 1) - 1) & 1)) {
-      ok = false;
-      break;
-    }
+  // K (v = 0) or V (v = 1) of tile t < w.n; whether its place came free
+  auto load = [&](int t, int v) -> bool {
+    const int at = t & 1;
+    if (t >= 2 && !warp_wait(&bars[(v ? L::B_PV : L::B_S) + at], ((t >> 1) - 1) & 1)) return false;
     const int j = w.j0 + t;
     const int left = j < w.nt0 ? KT : w.len1 - (j - w.nt0) * KT;
     const uint32_t off = (v ? L::OFF_V : L::OFF_K) + at * L::ENT, dst = base + off;
@@ -481,7 +481,7 @@ __device__ __forceinline__ void load_role(const FlashArgs& A, uint8_t* smem, uin
     }
     __syncwarp();
     if (wipe) {
-      if (!warp_wait(bar, rag++ & 1)) { ok = false; ++e; break; }
+      if (!warp_wait(bar, rag++ & 1)) return false;
       constexpr int C = D / 8;
       for (int x = left * C + lane; x < KT * C; x += 32)
         *reinterpret_cast<uint4*>(smem + off + sw128_off(x / C, x % C, KT)) =
@@ -489,72 +489,115 @@ __device__ __forceinline__ void load_role(const FlashArgs& A, uint8_t* smem, uin
       fence_proxy_async_smem();
       warp_arrive(full);
     }
-  }
+    ++done[v];
+    return true;
+  };
+  const int n = w.n;
+  bool ok = true;
+  for (int t = 0; ok && t < 2 && t < n; ++t) ok = load(t, 0);
+  for (int t = 0; ok && t < 2 && t < n; ++t) ok = load(t, 1);
+  if (ok && n > 2) ok = load(2, 0);
+  for (int t = 2; ok && t < n; ++t) ok = (t + 1 >= n || load(t + 1, 0)) && load(t, 1);
   // every box issued has landed before the CTA may exit
   if (A.qtma && !warp_wait(&bars[L::B_Q], 0)) ok = false;
-  for (int k = e > 4 ? e - 4 : 0; k < e; ++k)
-    if (!warp_wait(&bars[(k & 1 ? L::B_V : L::B_K) + ((k >> 1) & 1)], (k >> 2) & 1)) ok = false;
+#pragma unroll
+  for (int v = 0; v < 2; ++v)
+    for (int t = done[v] > 2 ? done[v] - 2 : 0; t < done[v]; ++t)
+      if (!warp_wait(&bars[(v ? L::B_V : L::B_K) + (t & 1)], (t >> 1) & 1)) ok = false;
   if (!ok && lane == 0) timeout_flag();
 }
 
 // ------------------------------------------------------------------ MMA role
-// One thread: two tiles' S = Q K^T ahead, then for each tile O += P V and S of the
+// One warp: two tiles' S = Q K^T ahead, then for each tile O += P V and S of the
 // tile after the next, into the buffer that P occupied (the tensor core works in
 // issue order).  A commit tells when all before it is complete.
+//
+// The whole warp runs the role, on values that the compiler knows to be uniform and
+// with the places of two tiles as constants, and one lane issues: a lane by itself
+// spent 1250 cycles on the twelve products and two commits of a tile, moving
+// descriptors, and bounded everything (1350 cycles per tile; the products take 643:
+// 64 each for P V, and 48 each for S, whose 64 columns read 6 KB of shared memory).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+
+template <int D>
+struct MmaWarp {
+  using L = Lay<D>;
+  uint64_t* bars;
+  uint32_t tmem;
+  uint64_t qd, kd, vd;
+  bool leader;
+
+  template <int AT>
+  __device__ __forceinline__ void scores() const {  // S of the tile whose K lies in place AT
+    constexpr uint32_t IDQ = idesc_bf16(QT, KT, false, false);
+    tc_fence_after();
+    if (leader) {
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t in = (k & 3) * 32;
+        mma_bf16_ss(tmem + 64 * AT, qd + (((k >> 2) * (QT * 128) + in) >> 4),
+                    kd + ((AT * L::ENT + (k >> 2) * (KT * 128) + in) >> 4), IDQ, k > 0);
+      }
+      mma_commit(&bars[L::B_S + AT]);
+    }
+    __syncwarp();
+  }
+
+  // O += P V of tile t in place AT, and S of tile t + 2
+  template <int AT>
+  __device__ __forceinline__ bool step(int t, int n) const {
+    constexpr uint32_t IDP = idesc_bf16(QT, D, false, true);
+    const uint32_t phase = (t >> 1) & 1;
+    if (!warp_wait(&bars[L::B_V + AT], phase) || !warp_wait(&bars[L::B_P + AT], phase)) return false;
+    tc_fence_after();
+    if (leader) {
+#pragma unroll
+      for (int k = 0; k < KT / 16; ++k)
+        mma_bf16_ts(tmem + 128, tmem + 64 * AT + 8 * k, vd + ((AT * L::ENT + k * 16 * 128) >> 4), IDP,
+                    (k > 0 || t > 0) ? 1u : 0u);
+      mma_commit(&bars[L::B_PV + AT]);
+    }
+    __syncwarp();
+    if (t + 2 < n) {
+      if (!warp_wait(&bars[L::B_K + AT], phase ^ 1)) return false;
+      scores<AT>();
+    }
+    return true;
+  }
+};
+
 template <int D>
 __device__ __forceinline__ void mma_role(uint8_t* smem, uint64_t* bars, uint32_t tmem,
                                          const Work& w) {
   using L = Lay<D>;
-  constexpr uint32_t IDQ = idesc_bf16(QT, KT, false, false);
-  constexpr uint32_t IDP = idesc_bf16(QT, D, false, true);
   const uint32_t base = smem_u32(smem);
-  const uint64_t qd = desc_sw128(base, 16, 1024);
-  const uint64_t kd = desc_sw128(base + L::OFF_K, 16, 1024);
+  MmaWarp<D> m;
+  m.bars = bars;
+  m.tmem = __shfl_sync(0xffffffffu, tmem, 0);
+  m.qd = desc_sw128(base, 16, 1024);
+  m.kd = desc_sw128(base + L::OFF_K, 16, 1024);
   // V: channels are the contiguous dimension; its 64-channel blocks lie KT * 128 bytes apart
-  const uint64_t vd = desc_sw128(base + L::OFF_V, KT * 128, 1024);
-  auto scores = [&](int t) {  // S of tile t, whose K is there
-    const uint64_t k0 = kd + (((t & 1) * L::ENT) >> 4);
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      const uint32_t in = (k & 3) * 32;
-      mma_bf16_ss(tmem + 64 * (t & 1), qd + (((k >> 2) * (QT * 128) + in) >> 4),
-                  k0 + (((k >> 2) * (KT * 128) + in) >> 4), IDQ, k > 0);
-    }
-    mma_commit(&bars[L::B_S + (t & 1)]);
-  };
-  bool ok = mbar_wait(&bars[L::B_Q], 0);
-  for (int t = 0; ok && t < 2 && t < w.n; ++t) {
-    ok = mbar_wait(&bars[L::B_K + t], 0);
-    if (!ok) break;
-    tc_fence_after();
-    scores(t);
+  m.vd = desc_sw128(base + L::OFF_V, KT * 128, 1024);
+  m.leader = elect_one();
+  const int n = __shfl_sync(0xffffffffu, w.n, 0);
+  bool ok = warp_wait(&bars[L::B_Q], 0) && warp_wait(&bars[L::B_K], 0);
+  if (ok) m.template scores<0>();
+  if (ok && n > 1) {
+    ok = warp_wait(&bars[L::B_K + 1], 0);
+    if (ok) m.template scores<1>();
   }
-  for (int t = 0; ok && t < w.n; ++t) {
-    const int at = t & 1;
-    const uint32_t phase = (t >> 1) & 1;
-    // (a test only: P V must not wait for a later key tile)
-    const bool there = t + 2 < w.n && mbar_test(&bars[L::B_K + at], phase ^ 1);
-    ok = mbar_wait(&bars[L::B_V + at], phase) && mbar_wait(&bars[L::B_P + at], phase);
-    if (!ok) break;
-    tc_fence_after();
-    const uint64_t v0 = vd + ((at * L::ENT) >> 4);
-#pragma unroll
-    for (int k = 0; k < KT / 16; ++k)
-      mma_bf16_ts(tmem + 128, tmem + 64 * at + 8 * k, v0 + ((k * 16 * 128) >> 4), IDP,
-                  (t > 0 || k > 0) ? 1u : 0u);
-    mma_commit(&bars[L::B_PV + at]);
-    if (t + 2 < w.n) {
-      if (!there) {
-        ok = mbar_wait(&bars[L::B_K + at], phase ^ 1);
-        if (!ok) break;
-        tc_fence_after();
-      }
-      scores(t + 2);
-    }
+  for (int t = 0; ok && t < n; t += 2) {
+    ok = m.template step<0>(t, n);
+    if (ok && t + 1 < n) ok = m.template step<1>(t + 1, n);
   }
-  mma_commit(&bars[L::B_DONE]);
-  if (!mbar_wait(&bars[L::B_DONE], 0)) ok = false;
-  if (!ok) timeout_flag();
+  if (m.leader) mma_commit(&bars[L::B_DONE]);
+  __syncwarp();
+  if (!warp_wait(&bars[L::B_DONE], 0)) ok = false;
+  if (!ok && m.leader) timeout_flag();
 }
 
 template <int D>
@@ -583,7 +626,7 @@ __global__ void __launch_bounds__(NTHREADS, 2) flash_kernel(const __grid_constan
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
   uint32_t* holder = reinterpret_cast<uint32_t*>(smem + L::OFF_BAR + L::NBAR * 8);
-  const int warp = threadIdx.x / 32;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0);
   if (threadIdx.x == 0) {
     mbar_init(&bars[L::B_Q], A.qtma ? 1 : W_LOAD);
     for (int b = 0; b < 2; ++b) {
@@ -610,8 +653,7 @@ __global__ void __launch_bounds__(NTHREADS, 2) flash_kernel(const __grid_constan
   } else if (warp < W_MMA) {
     load_role<D>(A, smem, bars, w);
   } else {
-    if ((threadIdx.x & 31) == 0) mma_role<D>(smem, bars, tmem, w);
-    __syncwarp();
+    mma_role<D>(smem, bars, tmem, w);
   }
   tc_fence_before();
   __syncthreads();
