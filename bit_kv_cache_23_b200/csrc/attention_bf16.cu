@@ -96,7 +96,6 @@ struct FlashArgs {
   float* lse;          // or null
   int head0;           // first key head of the pass
   int qblocks, nsplit;
-  int o32;             // O is 32-byte aligned
   int part0;           // first partial of this launch; -1: no partials
   float *ws_o, *ws_l;  // [partial][nq][Hq][D], [partial][nq][Hq]
   int qtma;            // Q rows come through the map (g divides 128)
@@ -133,29 +132,22 @@ __device__ __forceinline__ bool work_of(const FlashArgs& A, Work& w) {
   w.h = A.head0 + blockIdx.y;
   w.b = blockIdx.z;
   w.part = A.part0 + split;
-  bool fault = false;
-  w.tok0 = 0;
-  w.nb = (int)A.nq;
-  if (A.cu) {
-    const int64_t c0 = A.cu[w.b], c1 = A.cu[w.b + 1];
-    fault = c0 < 0 || c1 < c0 || c1 > A.nq;
-    if (!fault) {
-      w.tok0 = c0;
-      w.nb = (int)(c1 - c0);
-    } else {
-      w.nb = 0;
-    }
-  }
+  // all loads at once (each takes about 400 cycles)
+  const bool seqs = A.cu != nullptr, keys = A.own != OWN_NONE, rows_own = A.own == OWN_ROWS;
+  const int64_t c0 = seqs ? __ldg(A.cu + w.b) : 0, c1 = seqs ? __ldg(A.cu + w.b + 1) : A.nq;
+  int64_t len = keys ? __ldg(A.kv_len + w.b) : 0;
+  const int64_t start = rows_own ? __ldg(A.kv_start + w.b) : 0;
+  bool fault = c0 < 0 || c1 < c0 || c1 > A.nq;
+  w.tok0 = fault ? 0 : c0;
+  w.nb = fault ? 0 : (int)(c1 - c0);
   // (the host refuses more than 2^31 - 1 rows, keys or pages' places)
   const int rows = (w.nb < A.max_q ? w.nb : (int)A.max_q) * A.g;
   w.r0 = qb * QT;
   w.len = w.len1 = 0;
   w.start1 = 0;
-  if (A.own != OWN_NONE) {
-    int64_t len = A.kv_len[w.b];
+  if (keys) {
     int64_t room = A.own == OWN_PAGES ? (int64_t)A.width << A.shift : A.n_kv;
-    if (A.own == OWN_ROWS) {
-      const int64_t start = A.kv_start[w.b];
+    if (rows_own) {
       fault |= start < 0 || start > A.n_kv;
       w.start1 = (int)(start < 0 ? 0 : start > A.n_kv ? A.n_kv : start);
       room -= w.start1;
@@ -252,52 +244,68 @@ __device__ __forceinline__ int64_t out_row(const FlashArgs& A, const Work& w, in
 }
 
 // 32 bytes, one sector, to a 32-byte aligned address.
-__device__ __forceinline__ void store32(void* dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d,
-                                        uint32_t e, uint32_t f, uint32_t g, uint32_t h) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a), "r"(b),
-               "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h)
+__device__ __forceinline__ void store32(float* dst, const float* v, float f) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(v[0] * f), "f"(v[1] * f),
+               "f"(v[2] * f), "f"(v[3] * f), "f"(v[4] * f), "f"(v[5] * f), "f"(v[6] * f), "f"(v[7] * f)
                : "memory");
 }
 
-// One row of O from TMEM, times `inv`, to O or to this CTA's partial.
+// A warp's rows of O from TMEM, times each lane's `inv`, to this CTA's partial; row:
+// the lane's row among O's.
 template <int D>
-__device__ __forceinline__ void store_row(const FlashArgs& A, const Work& w, bool valid, int64_t row,
-                                          uint32_t to, float inv, float lse) {
-  const size_t at = A.part0 >= 0 ? (size_t)w.part * A.nq * A.Hq + row : (size_t)row;
-  if (valid) {
-    if (A.part0 >= 0) A.ws_l[at] = lse;
-    else if (A.lse) A.lse[at] = lse;
+__device__ __forceinline__ void store_part(const FlashArgs& A, const Work& w, bool valid, int64_t row, uint32_t to,
+                                           float inv, float lse) {
+  const size_t at = (size_t)w.part * A.nq * A.Hq + row;
+  if (valid) A.ws_l[at] = lse;
+#pragma unroll 1
+  for (int c = 0; c < D / 32; ++c) {
+    float o[32];
+    tmem_ld32(to + c * 32, o);
+    if (!valid) continue;
+#pragma unroll
+    for (int k = 0; k < 32; k += 8) store32(A.ws_o + at * D + 32 * c + k, o + k, inv);
   }
+}
+
+// The same to O, through shared memory, where nothing is needed any more, so that a
+// store covers whole rows (16-byte pieces exchanged by the row number keep the banks
+// apart): four 720p frames of cross attention 210 us, 217 with each lane's pieces of
+// its own row, 32 rows to a store.  (Of the fp32 partials those are whole sectors, and
+// the way through shared memory took 1 % longer.)
+template <int D>
+__device__ __forceinline__ void store_rows(const FlashArgs& A, const Work& w, uint8_t* smem, bool valid,
+                                           int64_t row, uint32_t to, float inv, float lse) {
+  constexpr int RB = D * 2, UPR = RB / 16, RPI = 32 / UPR;  // bytes and pieces of a row; rows per store
+  const int lane = threadIdx.x & 31;
+  if (valid && A.lse) A.lse[row] = lse;
+  uint8_t* const mine = smem + (threadIdx.x >> 5) * 32 * RB;
 #pragma unroll 1
   for (int c = 0; c < D / 32; ++c) {
     float o[32];
     tmem_ld32(to + c * 32, o);
 #pragma unroll
-    for (int e = 0; e < 32; ++e) o[e] *= inv;
-    if (!valid) continue;
-    if (A.part0 >= 0) {
-      float* dst = A.ws_o + at * D + 32 * c;
+    for (int k = 0; k < 4; ++k)
+      *reinterpret_cast<uint4*>(mine + lane * RB + (((4 * c + k) ^ (lane & 7)) << 4)) =
+          make_uint4(pack_bf16(o[8 * k] * inv, o[8 * k + 1] * inv), pack_bf16(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                     pack_bf16(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
+                     pack_bf16(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+  }
+  __syncwarp();
+  const uint8_t* const src = mine + (lane / UPR) * RB;
+  const int u = lane % UPR, left = w.nr - (int)(threadIdx.x & ~31u);  // rows of this warp and those behind
+#pragma unroll 1
+  for (int r0 = 0; r0 < 32 && r0 < left; r0 += 8 * RPI) {
+    uint4 v[8];
 #pragma unroll
-      for (int k = 0; k < 32; k += 8)
-        store32(dst + k, __float_as_uint(o[k]), __float_as_uint(o[k + 1]), __float_as_uint(o[k + 2]),
-                __float_as_uint(o[k + 3]), __float_as_uint(o[k + 4]), __float_as_uint(o[k + 5]),
-                __float_as_uint(o[k + 6]), __float_as_uint(o[k + 7]));
-    } else {
-      uint16_t* dst = A.O + at * D + 32 * c;
-      if (A.o32) {  // O is 32-byte aligned
+    for (int i = 0; i < 8; ++i) {
+      const int rr = r0 + i * RPI;
+      v[i] = *reinterpret_cast<const uint4*>(src + rr * RB + ((u ^ ((rr + lane / UPR) & 7)) << 4));
+    }
 #pragma unroll
-        for (int k = 0; k < 32; k += 16)
-          store32(dst + k, pack_bf16(o[k], o[k + 1]), pack_bf16(o[k + 2], o[k + 3]),
-                  pack_bf16(o[k + 4], o[k + 5]), pack_bf16(o[k + 6], o[k + 7]),
-                  pack_bf16(o[k + 8], o[k + 9]), pack_bf16(o[k + 10], o[k + 11]),
-                  pack_bf16(o[k + 12], o[k + 13]), pack_bf16(o[k + 14], o[k + 15]));
-      } else {
-#pragma unroll
-        for (int k = 0; k < 32; k += 8)
-          *reinterpret_cast<uint4*>(dst + k) =
-              make_uint4(pack_bf16(o[k], o[k + 1]), pack_bf16(o[k + 2], o[k + 3]),
-                         pack_bf16(o[k + 4], o[k + 5]), pack_bf16(o[k + 6], o[k + 7]));
-      }
+    for (int i = 0; i < 8; ++i) {
+      const int rr = r0 + i * RPI + lane / UPR;
+      const int64_t to_row = __shfl_sync(0xffffffffu, row, rr);
+      if (rr < left) *reinterpret_cast<uint4*>(A.O + to_row * D + 8 * u) = v[i];
     }
   }
 }
@@ -389,20 +397,29 @@ __device__ __forceinline__ void softmax_role(const FlashArgs& A, uint8_t* smem, 
     tc_fence_before();
     warp_arrive(&bars[L::B_P + (i & 1)]);
   }
+  float la, lb;
+  f2unpack(fadd2(l2[0], l2[1]), la, lb);
+  const float l = la + lb;
+  // (a row without keys; a NaN among the scores stays one)
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const float lse = l == 0.0f ? -INFINITY : (m_used + log2f(l)) * 0.6931471805599453f;
+  const int64_t row = out_row(A, w, r);
   if (ok) ok = warp_wait(&bars[L::B_PV + ((w.n - 1) & 1)], ((w.n - 1) >> 1) & 1);
   if (!ok) {
     if ((threadIdx.x & 31) == 0) timeout_flag();
     return;
   }
   tc_fence_after();
-  float la, lb;
-  f2unpack(fadd2(l2[0], l2[1]), la, lb);
-  const float l = la + lb;
-  store_row<D>(A, w, valid, out_row(A, w, r), to, l > 0.0f ? 1.0f / l : 0.0f,
-               l > 0.0f ? (m_used + log2f(l)) * 0.6931471805599453f : -INFINITY);
+  if (A.part0 >= 0) store_part<D>(A, w, valid, row, to, inv, lse);
+  else store_rows<D>(A, w, smem, valid, row, to, inv, lse);
 }
 
 // ------------------------------------------------------------------ loader role
+// All warps, from wherever they are: the barriers are set up, TMEM is there.
+__device__ __forceinline__ void start_barrier() {
+  asm volatile("barrier.sync 1, %0;" ::"n"(NTHREADS) : "memory");
+}
+
 // The boxes of K (v = 0) or V (v = 1) rows of key tile j to `dst`, ENT bytes
 // in all; one thread.
 template <int D>
@@ -445,6 +462,8 @@ __device__ __forceinline__ void issue_tile(const FlashArgs& A, const Work& w, in
 // places (S 0, S 1, P V 0, S 2, P V 1, S 3, ...).  (In the order of the keys K of the
 // tile after the next waited behind V of the next, and came late: 259 us against 248
 // at 1560 rows x 40 heads over 8192 keys.)
+//
+// What it asks for first is on its way while the others still wait for TMEM.
 template <int D>
 __device__ __forceinline__ void load_role(const FlashArgs& A, uint8_t* smem, uint64_t* bars,
                                           const Work& w) {
@@ -494,7 +513,8 @@ __device__ __forceinline__ void load_role(const FlashArgs& A, uint8_t* smem, uin
   };
   const int n = w.n;
   bool ok = true;
-  for (int t = 0; ok && t < 2 && t < n; ++t) ok = load(t, 0);
+  for (int t = 0; t < 2 && t < n; ++t) load(t, 0);
+  start_barrier();
   for (int t = 0; ok && t < 2 && t < n; ++t) ok = load(t, 1);
   if (ok && n > 2) ok = load(2, 0);
   for (int t = 2; ok && t < n; ++t) ok = (t + 1 >= n || load(t + 1, 0)) && load(t, 1);
@@ -627,39 +647,29 @@ __global__ void __launch_bounds__(NTHREADS, 2) flash_kernel(const __grid_constan
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
   uint32_t* holder = reinterpret_cast<uint32_t*>(smem + L::OFF_BAR + L::NBAR * 8);
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0);
-  if (threadIdx.x == 0) {
-    mbar_init(&bars[L::B_Q], A.qtma ? 1 : W_LOAD);
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&bars[L::B_K + b], 1);
-      mbar_init(&bars[L::B_V + b], 1);
-      mbar_init(&bars[L::B_S + b], 1);
-      mbar_init(&bars[L::B_P + b], (w.nr + 31) / 32);
-      mbar_init(&bars[L::B_PV + b], 1);
-    }
-    mbar_init(&bars[L::B_DONE], 1);
-    mbar_init(&bars[L::B_RAG], 1);
+  if (warp == W_LOAD) {
+    const int b = threadIdx.x & 31;  // one each
+    if (b < L::NBAR)
+      mbar_init(&bars[b], b == L::B_P || b == L::B_P + 1 ? (w.nr + 31) / 32 : b == L::B_Q && !A.qtma ? W_LOAD : 1);
     fence_mbar_init();
-  }
-  if (warp == W_MMA) {
-    tmem_alloc(holder, COLS);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *holder;
-  if (warp < W_LOAD) {
-    softmax_role<D>(A, smem, bars, tmem, w);
-  } else if (warp < W_MMA) {
-    load_role<D>(A, smem, bars, w);
+    __syncwarp();
+    load_role<D>(A, smem, bars, w);  // (passes the barrier below on its way)
   } else {
-    mma_role<D>(smem, bars, tmem, w);
+    if (warp == W_MMA) {
+      tmem_alloc(holder, COLS);
+      tmem_relinquish();
+    }
+    tc_fence_before();
+    start_barrier();
+    tc_fence_after();
+    if (warp < W_LOAD) softmax_role<D>(A, smem, bars, *holder, w);
+    else mma_role<D>(smem, bars, *holder, w);
   }
   tc_fence_before();
   __syncthreads();
   if (warp == W_MMA) {
     tc_fence_after();
-    tmem_dealloc(tmem, COLS);
+    tmem_dealloc(*holder, COLS);
   }
 }
 
@@ -697,11 +707,12 @@ __global__ void __launch_bounds__(256) merge_kernel(const float* __restrict__ ws
   float L = fmaxf(l0, l1);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) L = fmaxf(L, __shfl_xor_sync(0xffffffffu, L, o));
+  if (__any_sync(0xffffffffu, l0 != l0 || l1 != l1)) L = NAN;  // (the maximum leaves a NaN out)
   constexpr int V = D / 32;
   float acc[V], den = 0.0f;
 #pragma unroll
   for (int e = 0; e < V; ++e) acc[e] = 0.0f;
-  if (L > -INFINITY) {
+  if (L != -INFINITY) {
     const float w0 = expf(l0 - L), w1 = expf(l1 - L);
 #pragma unroll 4
     for (int c = 0; c < np; ++c) {
@@ -717,12 +728,12 @@ __global__ void __launch_bounds__(256) merge_kernel(const float* __restrict__ ws
       }
     }
   }
-  const float inv = den > 0.0f ? 1.0f / den : 0.0f;
+  const float inv = den == 0.0f ? 0.0f : 1.0f / den;
 #pragma unroll
   for (int e = 0; e < V; e += 2)
     *reinterpret_cast<uint32_t*>(O + row * D + V * lane + e) =
         pack_bf16(acc[e] * inv, acc[e + 1] * inv);
-  if (lse && lane == 0) lse[row] = den > 0.0f ? L + logf(den) : -INFINITY;
+  if (lse && lane == 0) lse[row] = den == 0.0f ? -INFINITY : L + logf(den);
 }
 
 // ------------------------------------------------------------------ host side
@@ -969,7 +980,6 @@ extern "C" qwm_status qwm_attention_shared(const qwm_cache* c, const void* Q, in
   a.max_q = max_q;
   a.scale_log2 = (scale > 0.0f ? scale : 1.0f / sqrtf((float)D.d)) * 1.4426950408889634f;
   a.O = (uint16_t*)O;
-  a.o32 = aligned_to(O, 32);
   a.lse = lse;
   a.ws_o = (float*)workspace;
   a.ws_l = a.ws_o + (size_t)plan.np * n_q * heads_q * D.d;
@@ -1115,7 +1125,6 @@ extern "C" qwm_status qwm_cross_attention(const void* Q, int64_t ldq, int64_t n_
   a.max_kv = max_kv;
   a.scale_log2 = (scale > 0.0f ? scale : 1.0f / sqrtf((float)head_dim)) * 1.4426950408889634f;
   a.O = (uint16_t*)O;
-  a.o32 = aligned_to(O, 32);
   a.lse = lse;
   const bool parts = full > 0 && workspace && workspace_bytes >= full;
   const Blocks b = blocks_of(mq * g, heads_kv * n_seq, (max_kv + KT - 1) / KT,

@@ -386,6 +386,25 @@ def test_cross_attention_bad_device_arrays():
         assert q.qwm_device_status() == 2
 
 
+@pytest.mark.parametrize("new,states,split", [((130,), (200,), False), ((3,), (5000,), True)])
+def test_a_nan_query_stays_in_its_row(new, states, split):
+    """A NaN in one query row gives NaN (O and lse) there, and leaves the other rows' bits alone; in one
+    key range and in several."""
+    g = _gen(41)
+    Q, kv = randn(g, new[0], 2, 128).to(BF16), randn(g, states[0], 2, 128).to(BF16)
+    sizes = q.qwm_cross_attention_workspace(2, 2, 128, new[0], 1, new[0], states[0])
+    assert (sizes[1] > 0) == split
+    args = ints([0, new[0]]), ints([0]), ints(list(states)), new[0], states[0]
+    lse, bad = (torch.empty(new[0], 2, device="cuda") for _ in range(2))
+    O = q.qwm_cross_attention(Q, kv, kv, *args, lse=lse)
+    Q[1, 1, 5] = NAN
+    P = q.qwm_cross_attention(Q, kv, kv, *args, lse=bad)
+    _fine()
+    assert P[1, 1].isnan().all() and bad[1, 1].isnan()
+    P[1, 1], bad[1, 1] = O[1, 1], lse[1, 1]
+    assert torch.equal(P, O) and torch.equal(bad, lse)
+
+
 def test_large_scores_and_scale():
     """Scores up to +-2000: the running maximum moves, no weight overflows; an explicit scale."""
     g = _gen(77)
