@@ -120,20 +120,27 @@ __device__ __forceinline__ float2 turn(int pos, double freq, float gain) {
 
 // Place of row t's position in the pools, as an element offset of head 0, or -1:
 // a row of no sequence, or a page outside the pool or the table.  One warp; the
-// sequence is the last that begins at or before t, found by 32 probes at a time.
+// sequence is the last that begins at or before t, found by 32 probes at a time; where
+// its positions start comes with the probes, a load's latency earlier.
 __device__ __forceinline__ int64_t place_of(const RopeArgs& A, int64_t t, int D) {
   const int lane = threadIdx.x & 31;
   int64_t lo = -1, hi = A.n_seq + 1;  // cu[lo] <= t < cu[hi]
+  int begin = 0, start = 0;           // of lo
   while (hi - lo > 1) {
     const int64_t step = (hi - lo + 31) / 32, x = lo + (lane + 1) * step;
-    const unsigned below = __ballot_sync(0xffffffffu, x < hi && __ldg(A.cu + x) <= t);
+    const int c = x < hi ? __ldg(A.cu + x) : 0, s = x < A.n_seq ? __ldg(A.start + x) : 0;
+    const unsigned below = __ballot_sync(0xffffffffu, x < hi && c <= t);
     const int n = below == 0xffffffffu ? 32 : __ffs(~below) - 1;  // the leading probes
+    if (n > 0) {
+      begin = __shfl_sync(0xffffffffu, c, n - 1);
+      start = __shfl_sync(0xffffffffu, s, n - 1);
+    }
     const int64_t up = lo + (n + 1) * step;
     lo += n * step;
     hi = up < hi ? up : hi;
   }
   if (lo < 0 || lo >= A.n_seq) return -1;
-  const int64_t p = (int64_t)__ldg(A.start + lo) + (t - __ldg(A.cu + lo));
+  const int64_t p = (int64_t)start + (t - begin);
   const int64_t col = p >> A.shift;
   int64_t page = -1;
   if (p >= 0 && col < A.width) page = __ldg(A.table + lo * A.width + col);
