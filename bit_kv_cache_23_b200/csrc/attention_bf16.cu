@@ -19,9 +19,15 @@
 // while the softmax works on this one.  Two CTAs share an SM: one's products run
 // while the other has the exponential unit, and one's beginning and end hide
 // behind the other's tiles.  (One CTA of 256 rows, with each K and V tile read
-// once for two such groups, took 8 to 18 % longer up to 2048 keys, the same at
-// 4096, and 5 % less at 8192: the groups fall into step, both waiting for
-// products and then both for the exponential unit.)
+// once for two such groups, took 8 to 18 % longer up to 2048 keys: the groups fall
+// into step, both waiting for products and then both for the exponential unit.)
+//
+// Bound by the tensor core's reading of shared memory, and by the power limit: a
+// 128 x 64 tile's products take 643 cycles, of which S takes 386 (a product of 64
+// columns reads 6 KB in 48 cycles for 32 cycles of arithmetic; 128 columns would
+// take 64, but two such buffers beside O do not fit in half of TMEM), and an SM with
+// two CTAs needs 720 cycles per tile.  1560 rows x 40 heads over 8192 keys: 243 to 247
+// us, 1060 to 1080 TFLOP/s, at 1.6 GHz; 592 even row blocks 1170 TFLOP/s.
 //
 // K and V tiles go through one ring of TMA boxes in the 128-byte-swizzled layout
 // that the MMA descriptors read (one box per 64 channels and, for pages, per
@@ -89,7 +95,7 @@ struct FlashArgs {
   int64_t n_kv;                 // rows
   const int32_t *kv_start, *kv_len, *table;
   int64_t max_kv, n_pages;
-  int width, shift, pool_heads; // pages
+  int width, shift;             // pages
   int causal;
   float scale_log2;
   uint16_t* O;
@@ -1003,7 +1009,6 @@ extern "C" qwm_status qwm_attention_shared(const qwm_cache* c, const void* Q, in
     own.n_pages = pages->n_pages;
     own.width = table_width;
     own.shift = page_shift(pages);
-    own.pool_heads = pages->heads;
   }
   // heads per pass: what the workspace holds unpacked
   const uint64_t head = plan.rows ? 0 : (uint64_t)T * D.d * 4;

@@ -4,7 +4,9 @@
 //
 // Bound by the decoding, not by memory: at 40 heads x 37440 tokens x 128 channels
 // the packed fields are 162 MB (25 us), while every element takes about four
-// instructions to rebuild.  So the layout serves the decoder.  A warp takes 16
+// instructions to rebuild; one row takes 225 us, eight 234 us and sixteen 245 us (at
+// rank 16 292, 301 and 311), with 56 % of the issue slots and 44 % of the integer
+// pipe in use.  So the layout serves the decoder.  A warp takes 16
 // keys at a time; in the products' operand layout (lane = 4 g + c) the channels
 // are permuted such that a lane owns a quarter head of keys g and g + 8 of K'
 // (whole code words) and D / 8 channels of keys 2c, 2c+1, 2c+8, 2c+9 of V', and
@@ -33,10 +35,9 @@ namespace qwm {
 namespace {
 using namespace tc;
 
-constexpr int NW_ROWS = 12;     // warps of the attention (168 registers per thread; with 16 it
-                               // spills, 310 us, with 8 too few latencies overlap, 260 us
-                               // against 254 us at the size above)
-constexpr int NW_UNPACK = 16;  // and of the unpacking
+constexpr int NW_ROWS = 12;    // warps of the attention: 168 registers per thread (16 warps spill:
+                               // 320 us, against 240 us when this was chosen)
+constexpr int NW_UNPACK = 16;  // and of the unpacking, which keeps no O
 constexpr int KT = 16;        // keys per tile
 constexpr int NSTAGE = 2;     // tiles in a warp's ring
 constexpr float TAU = 8.0f;   // a row's reference moves when its maximum grew by more (log2)
@@ -144,7 +145,7 @@ struct Source {
 template <int D>
 __device__ __forceinline__ Source<D> source_of(const Dims& Dm, const Fields& F, const PackedHead& p) {
   using L = Stage<D>;
-  const int lane = threadIdx.x & 31, ng = Dm.ng, r = Dm.r, ib = Dm.idx_bytes;
+  const int lane = threadIdx.x & 31, r = Dm.r, ib = Dm.idx_bytes;
   Source<D> S;
   S.codes = p.k_codes + 16 * lane;
   S.vcodes = p.v_codes - p.k_codes;
@@ -165,7 +166,6 @@ __device__ __forceinline__ Source<D> source_of(const Dims& Dm, const Fields& F, 
   else if (lane < b) piece(p.k_cscale, F.cs, a, 2);
   else if (lane < c) piece(p.k_idx, F.ki, b, ib);
   else if (lane < d) piece(p.v_idx, F.vi, c, ib);
-  (void)ng;
   return S;
 }
 
@@ -723,6 +723,10 @@ __global__ void __launch_bounds__(32 * NW_ROWS, 1) rows_kernel(const __grid_cons
 // K' and V' of heads h0 .. as [head][T][D] bf16, the cache that the
 // reconstruction returns, with the decoding of K' above for both: a lane rebuilds
 // 16 adjacent channels of a key at a time and stores them as one 32-byte sector.
+// Bound by the decoding as well: 211 us at 40 heads x 37440 tokens x 128 (the 767 MB
+// that it writes are 117 us; a thread per 16 channels, with the basis read from
+// shared memory for every element, took 700 us); 28 us over 12 x 7919 tokens, where a
+// warp has two or three tiles and a block's tables and basis are not yet hidden.
 struct UnpackArgs {
   Dims Dm;
   CacheView v;

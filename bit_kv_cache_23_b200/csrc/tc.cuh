@@ -141,36 +141,6 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
       : "memory");
 }
 
-// 32 lanes x 64 consecutive fp32 columns into v[O .. O+63], waited in the same
-// statement.
-template <int O, int N>
-__device__ __forceinline__ void tmem_ld64_at(uint32_t taddr, float (&v)[N]) {
-  static_assert(O + 64 <= N, "columns");
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
-      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
-      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
-      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63"
-      "}, [%64];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=f"(v[O + 0]), "=f"(v[O + 1]), "=f"(v[O + 2]), "=f"(v[O + 3]), "=f"(v[O + 4]),
-        "=f"(v[O + 5]), "=f"(v[O + 6]), "=f"(v[O + 7]), "=f"(v[O + 8]), "=f"(v[O + 9]),
-        "=f"(v[O + 10]), "=f"(v[O + 11]), "=f"(v[O + 12]), "=f"(v[O + 13]), "=f"(v[O + 14]),
-        "=f"(v[O + 15]), "=f"(v[O + 16]), "=f"(v[O + 17]), "=f"(v[O + 18]), "=f"(v[O + 19]),
-        "=f"(v[O + 20]), "=f"(v[O + 21]), "=f"(v[O + 22]), "=f"(v[O + 23]), "=f"(v[O + 24]),
-        "=f"(v[O + 25]), "=f"(v[O + 26]), "=f"(v[O + 27]), "=f"(v[O + 28]), "=f"(v[O + 29]),
-        "=f"(v[O + 30]), "=f"(v[O + 31]), "=f"(v[O + 32]), "=f"(v[O + 33]), "=f"(v[O + 34]),
-        "=f"(v[O + 35]), "=f"(v[O + 36]), "=f"(v[O + 37]), "=f"(v[O + 38]), "=f"(v[O + 39]),
-        "=f"(v[O + 40]), "=f"(v[O + 41]), "=f"(v[O + 42]), "=f"(v[O + 43]), "=f"(v[O + 44]),
-        "=f"(v[O + 45]), "=f"(v[O + 46]), "=f"(v[O + 47]), "=f"(v[O + 48]), "=f"(v[O + 49]),
-        "=f"(v[O + 50]), "=f"(v[O + 51]), "=f"(v[O + 52]), "=f"(v[O + 53]), "=f"(v[O + 54]),
-        "=f"(v[O + 55]), "=f"(v[O + 56]), "=f"(v[O + 57]), "=f"(v[O + 58]), "=f"(v[O + 59]),
-        "=f"(v[O + 60]), "=f"(v[O + 61]), "=f"(v[O + 62]), "=f"(v[O + 63])
-      : "r"(taddr)
-      : "memory");
-}
-
 // 32 lanes x 8 consecutive fp32 columns, waited in the same statement.
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
   asm volatile(
