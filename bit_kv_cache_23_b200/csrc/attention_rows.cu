@@ -4,7 +4,7 @@
 //
 // Bound by the decoding, not by memory: at 40 heads x 37440 tokens x 128 channels
 // the packed fields are 162 MB (25 us), while every element takes about four
-// instructions to rebuild; one row takes 225 us, eight 234 us and sixteen 245 us (at
+// instructions to rebuild, not counting what each group of them needs; one row takes 225 us, eight 234 us and sixteen 245 us (at
 // rank 16 292, 301 and 311), with 56 % of the issue slots and 44 % of the integer
 // pipe in use.  So the layout serves the decoder.  A warp takes 16
 // keys at a time; in the products' operand layout (lane = 4 g + c) the channels
@@ -725,8 +725,8 @@ __global__ void __launch_bounds__(32 * NW_ROWS, 1) rows_kernel(const __grid_cons
 // 16 adjacent channels of a key at a time and stores them as one 32-byte sector.
 // Bound by the decoding as well: 211 us at 40 heads x 37440 tokens x 128 (the 767 MB
 // that it writes are 117 us; a thread per 16 channels, with the basis read from
-// shared memory for every element, took 700 us); 28 us over 12 x 7919 tokens, where a
-// warp has two or three tiles and a block's tables and basis are not yet hidden.
+// shared memory for every element, took 700 us); 23 us over 12 x 7919 tokens, where a
+// warp has two or three tiles and a block's beginning is not hidden.
 struct UnpackArgs {
   Dims Dm;
   CacheView v;
@@ -884,10 +884,10 @@ cudaError_t launch_unpack(const UnpackArgs& a, int grid, cudaStream_t s) {
 // Both centroid tables of a head fit in shared memory beside the rest.
 bool tables_fit(const Dims& D) { return (int64_t)D.C * D.d <= 32768; }
 
-// f.operator()<D, TAB, RK>() of the variant that serves a cache.
+// f.run<D, TAB, RK>() of the variant that serves a cache; tab: with staged tables.
 template <class F>
-cudaError_t variant(const Dims& D, F f) {
-  const bool tab = tables_fit(D), deep = D.r > 8;
+cudaError_t variant(const Dims& D, bool tab, F f) {
+  const bool deep = D.r > 8;
   if (D.d == 128) {
     if (tab) return deep ? f.template run<128, true, 16>() : f.template run<128, true, 8>();
     return deep ? f.template run<128, false, 16>() : f.template run<128, false, 8>();
@@ -926,7 +926,12 @@ cudaError_t launch_unpack(const Dims& D, const CacheView& v, int64_t T, int h0, 
   a.V = V;
   const int64_t most = (a.total + NW_UNPACK - 1) / NW_UNPACK;  // CTAs with a tile for every warp
   const int grid = (int)(most < sms ? most : sms);
-  return variant(D, RunUnpack{a, grid, s});
+  // Staging both tables of a head pays from about 32 keys per centroid in a block's run
+  // on: at 256 centroids 40 x 9360 tokens (2530 keys per block) take 7 us less without,
+  // 40 x 37440 (10118 keys) 9 us more; at 16 centroids 40 x 9360 3 us more.  (The
+  // attention of few rows takes as long or longer without at every length.)
+  const bool tab = tables_fit(D) && a.total * KT >= (int64_t)grid * 32 * D.C;
+  return variant(D, tab, RunUnpack{a, grid, s});
 }
 
 // Rows of one product, and a history that gives every warp two tiles.  Otherwise the
@@ -970,7 +975,7 @@ cudaError_t launch_rows(const Dims& D, const CacheView& v, int64_t T, const uint
   a.nslot = plan.slots;
   a.nt = (T + KT - 1) / KT;
   a.total = a.nt * D.H;
-  return variant(D, RunRows{a, plan.grid, s});
+  return variant(D, tables_fit(D), RunRows{a, plan.grid, s});
 }
 
 }  // namespace qwm

@@ -6,7 +6,8 @@ import pytest
 import torch
 
 import bit_kv_cache_23_b200 as q
-from around_util import (BF16, attend, check, check_lse, frequencies, ints, norm_rope, offsets, randn)
+from around_util import (BF16, F32, HALF, attend, check, check_lse, frequencies, ints, norm_rope, offsets,
+                         randn)
 
 pytestmark = pytest.mark.gpu
 
@@ -229,24 +230,38 @@ def test_attention_shared(d, H, gh, T, new, own, page, causal):
         assert (O[live:] == 7.0).all() and (lse[live:] == 5.0).all(), "rows of no sequence were written"
 
 
-@pytest.mark.parametrize("C,G,r,d", [(16, 16, 0, 128), (300, 32, 16, 128), (300, 32, 8, 64), (16, 32, 5, 64)])
-def test_shared_history_is_the_reconstruction(C, G, r, d):
+@pytest.mark.parametrize("C,G,r,d,T", [
+    (16, 16, 0, 128, 701), (300, 32, 16, 128, 701), (300, 32, 8, 64, 701), (16, 32, 5, 64, 701),
+    (4, 16, 8, 128, 9601), (4, 32, 16, 64, 9600), (8, 16, 0, 128, 19001),   # long runs: staged tables
+])
+def test_shared_history_is_the_reconstruction(C, G, r, d, T):
     """The unpacked history, read back from the workspace, which ends with it (keys, then values), is the
     bf16 cache that the reconstruction returns.  Values, and keys without compensation, are equal bit for
-    bit.  The compensation's r products are summed in another order, so before the one rounding a key
-    element may be off by (r + 4) 2^-24 of sum |U c| <= 2 |K'| or so; the rounding then falls the other
-    way, by one step, where the sum lies that near a border between two bf16 values, 2^-7 |K'| apart: for
-    at most 2 (r + 4) 2^-24 2 / 2^-7 = (r + 4) 2^-15 of the elements (6e-4 at r = 16)."""
-    c, Kp, Vp, rows, kv, table, Q, cu, lens = _shared_case(d, 2, 1, 701, (70,), (20,), 16, False, 5, C=C, G=G, r=r)
+    bit.  The compensation's r products are summed in another order: with S = |c + mn + code sc| + sum |U c8
+    cs| each of the two sums is off by at most E = (r + 4) 2^-24 S before its one rounding, so the results
+    differ by 2 E and a bf16 step (at most 2^-7 of the larger), and they differ at all only where a border
+    between two bf16 values (2^-8 |K'| apart at least) lies within 2 E: for a share 2 E / (2^-8 |K'|) of
+    such elements, which is small unless the compensation cancels the rest."""
+    c, Kp, Vp, rows, kv, table, Q, cu, lens = _shared_case(d, 2, 1, T, (70,), (20,), 16, False, 5, C=C, G=G, r=r)
     full = q.qwm_attention_shared_workspace(c.c, Q.shape[0], 2, 1, 70, 20)[1]
     ws = torch.zeros(full, dtype=torch.uint8, device="cuda")
     c.attention_shared(Q, cu, 70, kv, table, lens, 20, workspace=ws)
     _fine()
-    n = 2 * 701 * d
+    n = 2 * T * d
     tail = ws[full - 4 * n:].view(torch.int16)
-    assert torch.equal(tail[n:].view(2, 701, d), Vp.view(torch.int16))
-    off = (tail[:n].view(2, 701, d).int() - Kp.view(torch.int16).int()).abs()
-    assert off.max() <= (1 if r else 0) and (off > 0).double().mean() <= (r + 4) / 2**15, (off.max(), (off > 0).sum())
+    assert torch.equal(tail[n:].view(2, T, d), Vp.view(torch.int16))
+    got, want = tail[:n].view(BF16).view(2, T, d).double(), Kp.double()
+    if r == 0:
+        assert torch.equal(tail[:n].view(2, T, d), Kp.view(torch.int16))
+        return
+    U, ver = c.view("basis").double().abs(), c.view("tokver")[:T].long()
+    c8, cs = c.view("k_coef")[:, :T].double().abs(), c.view("k_cscale").view(torch.float16)[:, :T].double().abs()
+    comp = torch.stack([torch.einsum("tdr,tr->td", U[ver, h], c8[h]) * cs[h][:, None] for h in range(2)])
+    both = 2 * (r + 4) * F32 * (want.abs() + 2 * comp)
+    off = (got - want).abs()
+    assert (off <= both + 2 * HALF * torch.maximum(got.abs(), want.abs())).all(), off.max()
+    share = (both / (HALF * want.abs().clamp_min(1e-30))).clamp_max(1.0)
+    assert (off > 0).sum() <= share.sum(), ((off > 0).sum(), share.sum())
 
 
 @pytest.mark.parametrize("H,C,G,r,d,T,rows", [
