@@ -351,13 +351,14 @@ def _raw_stream(stream, index) -> int:
 
 def _launch(name: str, index: int, *args) -> None:
     """The library launches on the current device: make it cuda:index for the call."""
-    before = torch.cuda.current_device()
+    fn = getattr(_lib or lib(), name)
+    before = torch._C._cuda_getDevice()
     if before == index:
-        st = getattr(lib(), name)(*args)
+        st = fn(*args)
     else:
         torch.cuda.set_device(index)
         try:
-            st = getattr(lib(), name)(*args)
+            st = fn(*args)
         finally:
             torch.cuda.set_device(before)
     if st != 0:
@@ -415,32 +416,32 @@ def qwm_norm_rope(rope: qwm_rope | None, Q: torch.Tensor | None, K: torch.Tensor
     if x0 is None:
         raise ValueError("neither Q nor K given")
     index = _device_of(x0, "Q" if Q is not None else "K")
-    args, outs, n, d = [], [], None, None
-    for x, w, o, name in ((Q, q_weight, Q_out, "Q"), (K, k_weight, K_out, "K")):
-        if x is None:
-            if w is not None or o is not None:
-                raise ValueError(f"{name} is missing")
-            args += (None, 0, 0, None, None, 0)
-            outs.append(None)
-            continue
-        p, ld = _rows_ptr(x, name, index)
-        shape = x.shape
-        if n is not None and (shape[0] != n or shape[2] != d):
-            raise ValueError("Q and K differ in rows or head_dim")
-        n, h, d = shape
-        if o is None:
-            o = _new(x, stream)
-            po, ldo = o.data_ptr(), max(h * d, 8)
-        else:
-            po, ldo = _rows_ptr(o, name + "_out", index)
-            if o.shape != shape:
-                raise ValueError(f"{name}_out must have the shape of {name}")
-        outs.append(o)
-        wp = None if w is None else _vec_ptr(w, name + " weight", index, _BF16, d)
-        args += (p, ld, h, wp, po, ldo)
+    if Q is not None and K is not None and (Q.shape[0] != K.shape[0] or Q.shape[-1] != K.shape[-1]):
+        raise ValueError("Q and K differ in rows or head_dim")
+    q, Q_out = _rope_side(Q, q_weight, Q_out, "Q", index, stream)
+    k, K_out = _rope_side(K, k_weight, K_out, "K", index, stream)
+    n, _, d = x0.shape
     rp, pp = _pos_ptr(rope, pos, n, index)
-    _launch("qwm_norm_rope", index, rp, d, n, *args, pp, n, eps, _raw_stream(stream, index))
-    return outs[0], outs[1]
+    _launch("qwm_norm_rope", index, rp, d, n, *q, *k, pp, n, eps, _raw_stream(stream, index))
+    return Q_out, K_out
+
+
+def _rope_side(x, w, o, name, index, stream):
+    """One side's arguments of qwm_norm_rope, and its output."""
+    if x is None:
+        if w is not None or o is not None:
+            raise ValueError(f"{name} is missing")
+        return (None, 0, 0, None, None, 0), None
+    p, ld = _rows_ptr(x, name, index)
+    _, h, d = x.shape
+    if o is None:
+        o = _new(x, stream)
+        po, ldo = o.data_ptr(), max(h * d, 8)
+    else:
+        po, ldo = _rows_ptr(o, name + "_out", index)
+        if o.shape != x.shape:
+            raise ValueError(f"{name}_out must have the shape of {name}")
+    return (p, ld, h, None if w is None else _vec_ptr(w, name + " weight", index, _BF16, d), po, ldo), o
 
 
 def qwm_paged_append(pages: qwm_pages, table: torch.Tensor, cu: torch.Tensor, start: torch.Tensor,

@@ -210,6 +210,8 @@ def _shared_want(Kp, Vp, rows, Q, new, own, causal, g_heads):
     (64, 1, 2, 0, (5,), (3,), 256, True),                             # causal rows before the first key
     (128, 1, 1, 2500, (260, 129), (1, 300), 16, True),                # more than one row block, split ranges
     (128, 4, 1, 40, (2,) * 70, (3,) * 70, 16, False),                 # many short branches
+    (128, 4, 1, 2000, (1,) * 100, (5, 0, 33, 1) * 25, 16, False),     # the history apart from the branches' keys
+    (64, 3, 2, 1500, (2, 0, 1, 3) * 30, (70, 9, 1, 3) * 30, 32, True),
 ])
 def test_attention_shared(d, H, gh, T, new, own, page, causal):
     c, Kp, Vp, rows, kv, table, Q, cu, lens = _shared_case(d, H, gh, T, new, own, page, causal, 11 + T)
@@ -494,3 +496,108 @@ def test_layer_step_in_a_graph():
             for h in range(H):
                 x = attend(replayed[1][cb[b]:cb[b + 1], h], enc[s:s + m, 0, h], enc[s:s + m, 1, h], 1 / math.sqrt(d))
                 check("cross", replayed[2][cb[b]:cb[b + 1], h], x[0], x[1])
+
+
+def test_replay_with_other_lengths():
+    """One captured call serves other lengths and rows per branch up to its bounds: the device arrays are
+    read at each replay."""
+    c, Kp, Vp, rows, kv, table, Q, cu, lens = _shared_case(128, 2, 1, 300, (9, 6), (80, 50), 16, True, 3, poison=False)
+    n = Q.shape[0]
+    O = torch.zeros(n, 2, 128, dtype=BF16, device="cuda")
+    lse = torch.zeros(n, 2, device="cuda")
+    ws = torch.empty(q.qwm_attention_shared_workspace(c.c, n, 2, 2, 12, 90)[1], dtype=torch.uint8, device="cuda")
+
+    def call():
+        c.attention_shared(Q, cu, 12, kv, table, lens, 80, causal=True, O=O, lse=lse, workspace=ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for new, own in (((9, 6), (80, 50)), ((3, 12), (17, 12)), ((0, 1), (0, 1)), ((1, 1), (64, 33))):
+        cu.copy_(ints(offsets(new)))
+        lens.copy_(ints(list(own)))
+        graph.replay()
+        _fine()
+        part = [(k[:, :m], v[:, :m]) for (k, v), m in zip(rows, own)]
+        want, bound, wl, lb = _shared_want(Kp, Vp, part, Q, new, own, True, 1)
+        live = sum(new)
+        check("O", O[:live], want[:live], bound[:live])
+        check_lse("lse", lse[:live], wl[:live], lb[:live])
+
+
+def test_two_calls_at_once():
+    """Calls on two streams at once, each with a workspace of its own, give what they give alone."""
+    cases = [_shared_case(128, 2, 1, 900, (40, 40), (70, 20), 16, True, seed) for seed in (1, 2)]
+    g = _gen(5)
+    x, enc = randn(g, 300, 2, 128).to(BF16), randn(g, 2500, 2, 128).to(BF16)
+    args = ints([0, 300]), ints([0]), ints([2500]), 300, 2500
+
+    def shared(i, stream=None):
+        c, _, _, _, kv, table, Q, cu, lens = cases[i]
+        return c.attention_shared(Q[:80], cu, 40, kv, table, lens, 70, causal=True, stream=stream)
+
+    alone = shared(0), shared(1), q.qwm_cross_attention(x, enc, enc, *args)
+    _fine()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(5):
+        for s in streams:
+            s.wait_stream(torch.cuda.current_stream())
+        got = (shared(0, streams[0]), shared(1, streams[1]),
+               q.qwm_cross_attention(x, enc, enc, *args, stream=streams[2]))
+        for s in streams:
+            s.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(alone, got))
+    _fine()
+
+
+def test_branches_that_share_pages():
+    """Two branches whose tables begin with the same pages (a common prefix), and one page named twice in
+    a table: pages are only read."""
+    g = _gen(8)
+    c = _cache(g, 2, 64, 100)
+    Kp, Vp = c.reconstruct()
+    kv = q.PagedKV(randn(g, 5, 2, 32, 64).to(BF16), randn(g, 5, 2, 32, 64).to(BF16))
+    table = ints([[3, 1, 1], [3, 1, 4]])
+    own, new = (80, 96), (2, 3)
+    rows = [(kv.K[t.long()].transpose(0, 1).reshape(2, -1, 64)[:, :m],
+             kv.V[t.long()].transpose(0, 1).reshape(2, -1, 64)[:, :m]) for t, m in zip(table, own)]
+    Q = randn(g, 5, 2, 64).to(BF16)
+    O = c.attention_shared(Q, ints([0, 2, 5]), 3, kv, table, ints(list(own)), 96)
+    _fine()
+    want, bound, _, _ = _shared_want(Kp, Vp, rows, Q, new, own, False, 1)
+    check("O", O, want, bound)
+
+
+def test_many_sequences():
+    """65535 sequences, most of them empty, in append and in both attentions."""
+    g = _gen(21)
+    n_seq, live = 65535, (0, 77, 40000, 65534)
+    cu = torch.zeros(n_seq + 1, dtype=torch.int32, device="cuda")
+    for b in live:
+        cu[b + 1:] += 1
+    K, V, Q = (randn(g, 4, 1, 64).to(BF16) for _ in range(3))
+    kv = q.PagedKV(torch.zeros(4, 1, 16, 64, dtype=BF16, device="cuda"), torch.zeros(4, 1, 16, 64, dtype=BF16, device="cuda"))
+    table = torch.full((n_seq, 1), -1, dtype=torch.int32, device="cuda")
+    start, lens = torch.zeros(n_seq, dtype=torch.int32, device="cuda"), torch.zeros(n_seq, dtype=torch.int32, device="cuda")
+    for i, b in enumerate(live):
+        table[b], start[b], lens[b] = i, 2 * i, 2 * i + 1
+    kv.append(table, cu, start, K, V)
+    for i in range(4):
+        assert torch.equal(kv.K[i, :, 2 * i], K[i]) and torch.equal(kv.V[i, :, 2 * i], V[i])
+    c = _cache(g, 1, 64, 50)
+    Kp, Vp = c.reconstruct()
+    O = c.attention_shared(Q, cu, 1, kv, table, lens, 16)
+    X = q.qwm_cross_attention(Q, kv.K.view(64, 1, 64), kv.V.view(64, 1, 64), cu, start, lens, 1, 16)
+    _fine()
+    for i in range(4):
+        k, v = kv.K[i, 0, :2 * i + 1], kv.V[i, 0, :2 * i + 1]
+        want, bound, _, _ = attend(Q[i], torch.cat([Kp[0], k]), torch.cat([Vp[0], v]), 0.125)
+        check("shared", O[i], want, bound)
+        k, v = (x.view(64, 64)[2 * i:4 * i + 1] for x in (kv.K, kv.V))
+        want, bound, _, _ = attend(Q[i], k, v, 0.125)
+        check("cross", X[i], want, bound)
