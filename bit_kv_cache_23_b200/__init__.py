@@ -12,6 +12,7 @@ Tensors Q, K, V, O are token-major ``[n][heads][head_dim]`` ``torch.bfloat16``
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -108,7 +109,7 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         I32, I64, F32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
         U64, F64 = ctypes.c_uint64, ctypes.c_double
-        pc, pu = ctypes.POINTER(qwm_cache), ctypes.POINTER(U64)
+        pc = ctypes.POINTER(qwm_cache)
         sig = {
             "qwm_abi_version": (I32, []),
             "qwm_status_string": (ctypes.c_char_p, [I32]),
@@ -129,10 +130,10 @@ def lib():
                                     I64, _P, I64, F32, _P]),
             "qwm_paged_append": (I32, [ctypes.POINTER(qwm_pages), _P, I64, I32, _P, _P, _P, I64, _P,
                                        I64, I64, _P, _P, I64, _P, F32, _P]),
-            "qwm_attention_shared_workspace": (I32, [pc, I64, I32, I64, I64, I64, pu, pu]),
+            "qwm_attention_shared_workspace": (I32, [pc, I64, I32, I64, I64, I64, _P, _P]),
             "qwm_attention_shared": (I32, [pc, _P, I64, I64, I32, _P, I64, I64, _P, _P, I32, _P, I64,
                                            I32, F32, _P, _P, _P, U64, _P]),
-            "qwm_cross_attention_workspace": (I32, [I32, I32, I32, I64, I64, I64, I64, pu, pu]),
+            "qwm_cross_attention_workspace": (I32, [I32, I32, I32, I64, I64, I64, I64, _P, _P]),
             "qwm_cross_attention": (I32, [_P, I64, I64, I32, _P, I64, _P, I64, I64, I32, I32, _P, _P,
                                           _P, I64, I64, I64, F32, _P, _P, _P, U64, _P]),
         }
@@ -478,15 +479,11 @@ def _out(O, Q, index, stream):
     return O
 
 
-def _scratch(workspace, sizes, Q, index, stream):
+def _scratch(workspace, sizes, args, Q, index, stream):
     """(tensor, pointer, bytes): the caller's workspace, or one for this call of the
-    full size that sizes() gives."""
+    full size that sizes(index, *args) gives."""
     if workspace is None:
-        if torch.cuda.current_device() == index:
-            nbytes = sizes()[1]
-        else:
-            with torch.cuda.device(index):
-                nbytes = sizes()[1]
+        nbytes = sizes(index, *args)
         if nbytes == 0:
             return None, None, 0
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=Q.device)
@@ -499,10 +496,31 @@ def _scratch(workspace, sizes, Q, index, stream):
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
+def _full(name, index, args) -> int:
+    """The full workspace bytes of a call on cuda:index."""
+    if torch._C._cuda_getDevice() == index:
+        return _sizes(name, *args)[1]
+    with torch.cuda.device(index):
+        return _sizes(name, *args)[1]
+
+
+def _shared_full(index, *args) -> int:
+    return _full("qwm_attention_shared_workspace", index, args)
+
+
+@functools.lru_cache(maxsize=1024)
+def _cross_full(index, *args) -> int:   # of the sizes alone, which a program repeats
+    return _full("qwm_cross_attention_workspace", index, args)
+
+
+_TWO = ctypes.c_uint64 * 2
+
+
 def _sizes(name, *args) -> tuple[int, int]:
-    least, full = ctypes.c_uint64(0), ctypes.c_uint64(0)
-    _check(name, getattr(lib(), name)(*args, ctypes.byref(least), ctypes.byref(full)))
-    return least.value, full.value
+    both = _TWO()
+    at = ctypes.addressof(both)
+    _check(name, getattr(_lib or lib(), name)(*args, at, at + 8))
+    return both[0], both[1]
 
 
 def qwm_attention_shared_workspace(cache: qwm_cache, n_q: int, heads_q: int, n_seq: int, max_q: int,
@@ -535,8 +553,8 @@ def qwm_attention_shared(cache: qwm_cache, Q: torch.Tensor, cu: torch.Tensor, ma
         pg, width = ctypes.addressof(pages), table.shape[1]
     O = _out(O, Q, index, stream)
     lp = _lse_ptr(lse, n, h, index)
-    ws, wp, wn = _scratch(workspace, lambda: qwm_attention_shared_workspace(cache, n, h, n_seq, max_q, max_kv),
-                          Q, index, stream)
+    ws, wp, wn = _scratch(workspace, _shared_full, (cache, n, h, n_seq, max_q, max_kv), Q,
+                          index, stream)
     _launch("qwm_attention_shared", index, cache, qp, ldq, n, h, cup, n_seq, max_q, pg, tp, width, kp,
             max_kv, int(causal), scale, O.data_ptr(), lp, wp, wn, _raw_stream(stream, index))
     return O
@@ -569,8 +587,8 @@ def qwm_cross_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu: t
     lnp = _vec_ptr(kv_len, "kv_len", index, _I32, n_seq)
     O = _out(O, Q, index, stream)
     lp = _lse_ptr(lse, n, h, index)
-    ws, wp, wn = _scratch(workspace, lambda: qwm_cross_attention_workspace(h, hk, d, n, n_seq, max_q, max_kv),
-                          Q, index, stream)
+    ws, wp, wn = _scratch(workspace, _cross_full, (h, hk, d, n, n_seq, max_q, max_kv), Q,
+                          index, stream)
     _launch("qwm_cross_attention", index, qp, ldq, n, h, kp, ldk, vp, ldv, n_kv, hk, d, cup, sp, lnp, n_seq,
             max_q, max_kv, scale, O.data_ptr(), lp, wp, wn, _raw_stream(stream, index))
     return O
