@@ -212,6 +212,8 @@ def _shared_want(Kp, Vp, rows, Q, new, own, causal, g_heads):
     (128, 4, 1, 40, (2,) * 70, (3,) * 70, 16, False),                 # many short branches
     (128, 4, 1, 2000, (1,) * 100, (5, 0, 33, 1) * 25, 16, False),     # the history apart from the branches' keys
     (64, 3, 2, 1500, (2, 0, 1, 3) * 30, (70, 9, 1, 3) * 30, 32, True),
+    (128, 2, 2, 28810, (2, 3), (40, 7), 16, True),                    # few rows of shared key heads, long history
+    (64, 2, 3, 28805, (1, 0, 1), (0, 5, 130), 32, False),
 ])
 def test_attention_shared(d, H, gh, T, new, own, page, causal):
     c, Kp, Vp, rows, kv, table, Q, cu, lens = _shared_case(d, H, gh, T, new, own, page, causal, 11 + T)
