@@ -934,14 +934,13 @@ cudaError_t launch_unpack(const Dims& D, const CacheView& v, int64_t T, int h0, 
   return variant(D, tab, RunUnpack{a, grid, s});
 }
 
-// Rows of one product, and a history that gives every warp two tiles.  Otherwise the
-// history is unpacked and attended to as bf16: at 40 heads x 37440 tokens 16 rows
-// take 249 us here and 354 us there, and a second row tile, decoding all again,
-// 463 against 356 us; over 12 x 7919 tokens (3.3 tiles a warp) 8 rows take 50 and
-// 53 us, over 4 x 1560 (a tile for every fourth warp) 34.5 and 33.5 us, one row over
-// 1 x 7919 40 and 32 us.
+// Rows of one product, and a history that gives every warp four tiles.  Otherwise the
+// history is unpacked and attended to as bf16: at 40 heads x 37440 tokens 16 rows take
+// 248 us here and 357 us there, and a second row tile, decoding all again, would take
+// 463 us; 8 rows over 4 x 37440 tokens (5.3 tiles a warp) 54 and 69 us, over 40 x 3120
+// (4.4) 55 and 56, over 12 x 7919 (3.3) 48 and 46, one row there 46 and 40.
 bool rows_supported(const Dims& D, int64_t T, int64_t rows, int sms) {
-  return rows <= 16 && (T + KT - 1) / KT * D.H >= 2 * (int64_t)NW_ROWS * sms;
+  return rows <= 16 && (T + KT - 1) / KT * D.H >= 4 * (int64_t)NW_ROWS * sms;
 }
 
 RowsPlan rows_plan(const Dims& D, int64_t T, int sms, int most) {

@@ -186,9 +186,9 @@ def test_shared_workspace_sizes():
     least, full = q.qwm_attention_shared_workspace(c, 80, 4, 2, 40, 40)
     assert full - least == 1000 * 64 * 4      # one of the two heads, keys and values
     assert _shared(n_q=80, max_q=40, ws_bytes=least - 1) == 3
-    long = _cache(len=28800)   # few rows over a long history: nothing is unpacked
+    long = _cache(len=57600)   # few rows over a long history: nothing is unpacked
     few = q.qwm_attention_shared_workspace(long, 8, 4, 2, 4, 40)
-    assert few[0] == few[1] and _shared(cache=dict(len=28800), ws_bytes=few[0] - 1) == 3
+    assert few[0] == few[1] and _shared(cache=dict(len=57600), ws_bytes=few[0] - 1) == 3
     empty = _cache(len=0)
     least, full = q.qwm_attention_shared_workspace(empty, 8, 4, 2, 4, 40)
     assert least == full
