@@ -337,11 +337,26 @@ def _mat_ptr(t, name, index, dtype, n=None, m=None):
     return t.data_ptr()
 
 
-def _new(x, stream):
-    """A contiguous tensor like x, allocated on the current stream and, where another
-    one is given, used there."""
-    o = torch.empty_like(x, memory_format=torch.contiguous_format)
-    return o if stream is None else _held(stream, o)
+def _made(stream, index, make):
+    """make(), which allocates, with `stream` (None: the current stream) as the current one.
+    Memory of another stream's pool may be free with its last use still queued there, and
+    work on `stream` does not wait for that."""
+    if stream is None:
+        return make()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=index)
+    with torch.cuda.stream(stream):
+        return make()
+
+
+def _new(x, stream, index):
+    """A contiguous tensor like x for a call on `stream`, whose caller reads it on the
+    current stream."""
+    if stream is None:
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
+    o = _made(stream, index, lambda: torch.empty_like(x, memory_format=torch.contiguous_format))
+    o.record_stream(torch.cuda.current_stream(index))
+    return o
 
 
 def _raw_stream(stream, index) -> int:
@@ -364,15 +379,6 @@ def _launch(name: str, index: int, *args) -> None:
             torch.cuda.set_device(before)
     if st != 0:
         raise QwmError(name, st)
-
-
-def _held(stream, t):
-    """A tensor allocated here (on the current stream) and used on `stream`."""
-    if stream is not None:
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=t.device)
-        t.record_stream(stream)
-    return t
 
 
 def qwm_rope_init(head_dim: int, rot_dim: int, layout: str = "half", theta: float = 10000.0,
@@ -436,7 +442,7 @@ def _rope_side(x, w, o, name, index, stream):
     p, ld = _rows_ptr(x, name, index)
     _, h, d = x.shape
     if o is None:
-        o = _new(x, stream)
+        o = _new(x, stream, index)
         po, ldo = o.data_ptr(), max(h * d, 8)
     else:
         po, ldo = _rows_ptr(o, name + "_out", index)
@@ -472,7 +478,7 @@ def _lse_ptr(lse, n, heads, index):
 
 def _out(O, Q, index, stream):
     if O is None:
-        return _new(Q, stream)
+        return _new(Q, stream, index)
     if (not isinstance(O, torch.Tensor) or O.dtype is not _BF16 or O.get_device() != index
             or O.shape != Q.shape or not O.is_contiguous()):
         _refuse(O, "O", index, _BF16, f"{tuple(Q.shape)} as Q has")
@@ -486,9 +492,7 @@ def _scratch(workspace, sizes, args, Q, index, stream):
         nbytes = sizes(index, *args)
         if nbytes == 0:
             return None, None, 0
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=Q.device)
-        if stream is not None:
-            _held(stream, workspace)
+        workspace = _made(stream, index, lambda: torch.empty(nbytes, dtype=torch.uint8, device=Q.device))
         return workspace, workspace.data_ptr(), nbytes
     if (not isinstance(workspace, torch.Tensor) or workspace.get_device() != index
             or not workspace.is_contiguous()):

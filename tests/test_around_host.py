@@ -224,3 +224,62 @@ def test_binding_refuses_wrong_tensors():
         q.PagedKV(x[None], x[None])
     with pytest.raises(ValueError):
         q.qwm_norm_rope(rope, None, None)
+
+
+# ------------------------------------------------------------------ the binding, without a GPU
+class _Device:
+    """Stands in for the GPU beneath the binding: CPU tensors pass its checks, launches are kept
+    instead of made, and every allocation is kept with the stream that was current."""
+
+    def __init__(self, monkeypatch):
+        self.streams, self.made, self.launches = ["current"], [], []
+        empty, empty_like = torch.empty, torch.empty_like
+
+        def on(stream):
+            device = self
+
+            class Context:
+                def __enter__(self):
+                    device.streams.append(stream)
+
+                def __exit__(self, *error):
+                    device.streams.pop()
+
+            return Context()
+
+        def allocated(make):
+            def call(*a, **kw):
+                kw.pop("device", None)
+                self.made.append(self.streams[-1])
+                return make(*a, **kw)
+            return call
+
+        for at, name, value in (
+                (torch, "empty", allocated(empty)), (torch, "empty_like", allocated(empty_like)),
+                (torch.cuda, "stream", on), (torch.cuda, "current_stream", lambda *a: self.streams[-1]),
+                (torch.cuda, "ExternalStream", lambda handle, device=None: ("raw", handle)),
+                (torch.Tensor, "record_stream", lambda *a: None),
+                (q, "_device_of", lambda t, name: t.get_device()), (q, "_raw_stream", lambda *a: 0),
+                (q, "_launch", lambda name, index, *a: self.launches.append((name, a))),
+                (q, "_shared_full", lambda *a: 4096), (q, "_cross_full", lambda *a: 4096)):
+            monkeypatch.setattr(at, name, value)
+
+
+class _Stream:
+    cuda_stream = 64
+
+
+@pytest.mark.parametrize("stream,where", [(_Stream, _Stream), (128, ("raw", 128)), (None, "current")])
+def test_what_a_call_allocates_belongs_to_its_stream(monkeypatch, stream, where):
+    """Outputs and workspaces come from the pool of the stream that the call runs on: in the current
+    stream's pool lie blocks whose last use is still queued there."""
+    x, i = torch.zeros(4, 2, 64, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)
+    cache = _cache()
+    device = _Device(monkeypatch)
+    q.qwm_norm_rope(None, x, x, stream=stream)
+    assert device.made == [where] * 2
+    q.qwm_attention_shared(cache, x, i, 4, stream=stream)
+    assert device.made[2:] == [where] * 2
+    q.qwm_cross_attention(x, x, x, i, i[:2], i[:2], 4, 4, stream=stream)
+    assert device.made[4:] == [where] * 2
+    assert [name for name, _ in device.launches] == ["qwm_norm_rope", "qwm_attention_shared", "qwm_cross_attention"]

@@ -611,3 +611,58 @@ def test_many_sequences():
         k, v = (x.view(64, 64)[2 * i:4 * i + 1] for x in (kv.K, kv.V))
         want, bound, _, _ = attend(Q[i], k, v, 0.125)
         check("cross", X[i], want, bound)
+
+
+def _small_calls():
+    """Calls of each operator that allocates, by stream."""
+    c, _, _, _, kv, table, Q, cu, lens = _shared_case(128, 2, 1, 900, (40, 40), (70, 20), 16, True, 7)
+    g = _gen(5)
+    x, enc = randn(g, 300, 2, 128).to(BF16), randn(g, 2500, 2, 128).to(BF16)
+    args = ints([0, 300]), ints([0]), ints([2500]), 300, 2500
+    w = (1 + randn(g, 128)).to(BF16)
+    sizes = {"rope": 0, "shared": q.qwm_attention_shared_workspace(c.c, 80, 2, 2, 40, 70)[1],
+             "cross": q.qwm_cross_attention_workspace(2, 2, 128, 300, 1, 300, 2500)[1]}
+    calls = {"rope": lambda s: q.qwm_norm_rope(None, x, q_weight=w, stream=s)[0],
+             "shared": lambda s: c.attention_shared(Q[:80], cu, 40, kv, table, lens, 70, causal=True, stream=s),
+             "cross": lambda s: q.qwm_cross_attention(x, enc, enc, *args, stream=s)}
+    return calls, sizes
+
+
+@pytest.mark.parametrize("name", ["rope", "shared", "cross"])
+def test_a_call_on_another_stream_leaves_freed_memory_alone(name):
+    """Blocks that were freed while the current stream's work still reads them are not what a call on
+    another stream, which does not wait for that work, writes to."""
+    calls, sizes = _small_calls()
+    alone = calls[name](None)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    calls[name](side)   # (the other stream's pool has blocks of these sizes from here on)
+    g = _gen(6)
+    for raw in (False, True):
+        read = [torch.randint(0, 256, (n,), generator=g, device="cuda", dtype=torch.uint8)
+                for n in (alone.numel() * 2, sizes[name]) if n]
+        want = [t.clone() for t in read]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(100_000_000)   # about 0.06 s
+        kept = [t.clone() for t in read]
+        del read
+        got = calls[name](side.cuda_stream if raw else side)
+        side.synchronize()
+        assert torch.equal(got, alone)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(kept, want))
+
+
+def test_a_call_here_beside_one_on_another_stream():
+    """A call on the current stream, whose workspace is free again while it still runs, and one on a
+    stream that does not wait for it."""
+    calls, _ = _small_calls()
+    alone = {name: call(None) for name, call in calls.items()}
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        for here, there in (("shared", "shared"), ("cross", "shared"), ("shared", "cross"), ("rope", "cross")):
+            side.wait_stream(torch.cuda.current_stream())
+            a, b = calls[here](None), calls[there](side)
+            side.synchronize()
+            assert torch.equal(a, alone[here]) and torch.equal(b, alone[there])
+    _fine()
