@@ -156,6 +156,38 @@ def _stream(stream, device) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _made(stream, index, make):
+    """make(), which allocates, with `stream` (None: the current stream) as the current one.
+    Memory of another stream's pool may be free with its last use still queued there, and
+    work on `stream` does not wait for that."""
+    if stream is None:
+        return make()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=index)
+    with torch.cuda.stream(stream):
+        return make()
+
+
+def _read_here(o, stream, index):
+    """o, which a call on `stream` writes and its caller reads on the current stream."""
+    if stream is not None:
+        o.record_stream(torch.cuda.current_stream(index))
+    return o
+
+
+def _new(x, stream, index):
+    """A contiguous tensor like x, an output of a call on `stream`."""
+    if stream is None:
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
+    return _read_here(_made(stream, index, lambda: torch.empty_like(x, memory_format=torch.contiguous_format)),
+                      stream, index)
+
+
+def _fresh(shape, dtype, device, stream):
+    """A tensor of `shape`, an output of a call on `stream`."""
+    return _read_here(_made(stream, device, lambda: torch.empty(shape, dtype=dtype, device=device)), stream, device)
+
+
 def _dev_ptr(t: torch.Tensor, name: str, dtype=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -220,10 +252,11 @@ def qwm_append_kv(cache: qwm_cache, K: torch.Tensor, V: torch.Tensor, stream=Non
 
 def qwm_attention(cache: qwm_cache, Q: torch.Tensor, O: torch.Tensor | None = None,
                   scale: float = 0.0, stream=None) -> torch.Tensor:
+    qp = _dev_ptr(Q, "Q", torch.bfloat16)
     if O is None:
-        O = torch.empty_like(Q)
+        O = _new(Q, stream, Q.get_device())
     _check("qwm_attention", lib().qwm_attention(
-        ctypes.byref(cache), _dev_ptr(Q, "Q", torch.bfloat16), Q.shape[0], float(scale),
+        ctypes.byref(cache), qp, Q.shape[0], float(scale),
         _dev_ptr(O, "O", torch.bfloat16), _stream(stream, Q.device)))
     return O
 
@@ -235,8 +268,9 @@ def qwm_attention_ext(cache: qwm_cache, Q: torch.Tensor, K_seg: torch.Tensor | N
     """Attention over the packed cache followed by the bf16 segment (K_seg, V_seg),
     [n_seg][H][d]; lse, if given, is a [n_q][H] float32 tensor that receives the
     natural-log softmax denominators."""
+    qp = _dev_ptr(Q, "Q", torch.bfloat16)
     if O is None:
-        O = torch.empty_like(Q)
+        O = _new(Q, stream, Q.get_device())
     n_seg = 0 if K_seg is None else K_seg.shape[0]
     if (K_seg is None) != (V_seg is None) or (V_seg is not None and V_seg.shape != K_seg.shape):
         raise ValueError("K_seg and V_seg must be given together, with equal shapes")
@@ -244,15 +278,14 @@ def qwm_attention_ext(cache: qwm_cache, Q: torch.Tensor, K_seg: torch.Tensor | N
     vp = _dev_ptr(V_seg, "V_seg", torch.bfloat16) if n_seg else None
     lp = _dev_ptr(lse, "lse", torch.float32) if lse is not None else None
     _check("qwm_attention_ext", lib().qwm_attention_ext(
-        ctypes.byref(cache), _dev_ptr(Q, "Q", torch.bfloat16), Q.shape[0], kp, vp, n_seg,
+        ctypes.byref(cache), qp, Q.shape[0], kp, vp, n_seg,
         float(scale), _dev_ptr(O, "O", torch.bfloat16), lp, _stream(stream, Q.device)))
     return O
 
 
 def qwm_reconstruct(cache: qwm_cache, t0: int, n: int, device, stream=None):
     H, d = cache.cfg.heads, cache.cfg.head_dim
-    Kp = torch.empty((H, n, d), dtype=torch.bfloat16, device=device)
-    Vp = torch.empty((H, n, d), dtype=torch.bfloat16, device=device)
+    Kp, Vp = (_fresh((H, n, d), torch.bfloat16, device, stream) for _ in range(2))
     _check("qwm_reconstruct", lib().qwm_reconstruct(
         ctypes.byref(cache), int(t0), int(n), _dev_ptr(Kp, "Kp"), _dev_ptr(Vp, "Vp"),
         _stream(stream, device)))
@@ -261,11 +294,10 @@ def qwm_reconstruct(cache: qwm_cache, t0: int, n: int, device, stream=None):
 
 def qwm_top1_shift(cache: qwm_cache, Q: torch.Tensor, K_exact: torch.Tensor, stream=None):
     H = cache.cfg.heads
-    ie = torch.empty((Q.shape[0], H), dtype=torch.int32, device=Q.device)
-    iq = torch.empty_like(ie)
+    qp, kp = _dev_ptr(Q, "Q", torch.bfloat16), _dev_ptr(K_exact, "K_exact", torch.bfloat16)
+    ie, iq = (_fresh((Q.shape[0], H), torch.int32, Q.device, stream) for _ in range(2))
     _check("qwm_top1_shift", lib().qwm_top1_shift(
-        ctypes.byref(cache), _dev_ptr(Q, "Q", torch.bfloat16), Q.shape[0],
-        _dev_ptr(K_exact, "K_exact", torch.bfloat16), _dev_ptr(ie, "idx_exact"),
+        ctypes.byref(cache), qp, Q.shape[0], kp, _dev_ptr(ie, "idx_exact"),
         _dev_ptr(iq, "idx_quant"), _stream(stream, Q.device)))
     return ie, iq
 
@@ -335,28 +367,6 @@ def _mat_ptr(t, name, index, dtype, n=None, m=None):
             or not t.is_contiguous()):
         _refuse(t, name, index, dtype, f"[{'n' if n is None else n}][{'m' if m is None else m}]")
     return t.data_ptr()
-
-
-def _made(stream, index, make):
-    """make(), which allocates, with `stream` (None: the current stream) as the current one.
-    Memory of another stream's pool may be free with its last use still queued there, and
-    work on `stream` does not wait for that."""
-    if stream is None:
-        return make()
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=index)
-    with torch.cuda.stream(stream):
-        return make()
-
-
-def _new(x, stream, index):
-    """A contiguous tensor like x for a call on `stream`, whose caller reads it on the
-    current stream."""
-    if stream is None:
-        return torch.empty_like(x, memory_format=torch.contiguous_format)
-    o = _made(stream, index, lambda: torch.empty_like(x, memory_format=torch.contiguous_format))
-    o.record_stream(torch.cuda.current_stream(index))
-    return o
 
 
 def _raw_stream(stream, index) -> int:
@@ -642,7 +652,7 @@ class QuantKVCache:
         bufs = qwm_buffers()
         for i, name in enumerate(BUFFER_NAMES):
             nb = int(self.sizes.bytes[i])
-            t = torch.empty(max(nb, 256), dtype=torch.uint8, device=self.device)
+            t = _fresh((max(nb, 256),), torch.uint8, self.device, stream)
             self.buffers[name] = t
             bufs.ptr[i] = t.data_ptr()
         self.bufs = bufs

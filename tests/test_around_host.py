@@ -283,3 +283,29 @@ def test_what_a_call_allocates_belongs_to_its_stream(monkeypatch, stream, where)
     q.qwm_cross_attention(x, x, x, i, i[:2], i[:2], 4, 4, stream=stream)
     assert device.made[4:] == [where] * 2
     assert [name for name, _ in device.launches] == ["qwm_norm_rope", "qwm_attention_shared", "qwm_cross_attention"]
+
+
+@pytest.mark.parametrize("stream,where", [(_Stream, _Stream), (128, ("raw", 128)), (None, "current")])
+def test_what_the_cache_calls_allocate_belongs_to_their_stream(monkeypatch, stream, where):
+    """The same of the calls on the packed cache, and of the cache's buffers, which its first call writes."""
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: 0
+
+    x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    cache = _cache()
+    sizes = q.qwm_cache_sizes(cache.cfg)
+    device = _Device(monkeypatch)
+    monkeypatch.setattr(q, "lib", Library)
+    monkeypatch.setattr(q, "qwm_cache_sizes", lambda cfg: sizes)
+    monkeypatch.setattr(q, "_dev_ptr", lambda t, *a: t.data_ptr())
+    monkeypatch.setattr(q, "_stream", lambda *a: 0)
+    for count, call in ((1, lambda: q.qwm_attention(cache, x, stream=stream)),
+                        (1, lambda: q.qwm_attention_ext(cache, x, stream=stream)),
+                        (2, lambda: q.qwm_reconstruct(cache, 0, 5, "cuda", stream=stream)),
+                        (2, lambda: q.qwm_top1_shift(cache, x, x, stream=stream)),
+                        (q.NBUF, lambda: q.QuantKVCache(2, 64, 16, 16, 4, 4, 1000, stream=stream))):
+        device.made.clear()
+        call()
+        assert device.made == [where] * count

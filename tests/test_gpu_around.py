@@ -666,3 +666,31 @@ def test_a_call_here_beside_one_on_another_stream():
             side.synchronize()
             assert torch.equal(a, alone[here]) and torch.equal(b, alone[there])
     _fine()
+
+
+def test_cache_calls_on_another_stream_leave_freed_memory_alone():
+    """The same of the calls on the packed cache that return tensors, and of a new cache."""
+    g = _gen(9)
+    c = _cache(g, 2, 128, 300)
+    Q = randn(g, 40, 2, 128).to(BF16)
+    K = randn(g, 300, 2, 128).to(BF16)
+    calls = (lambda s: [c.attention(Q, stream=s)], lambda s: [c.attention_ext(Q, stream=s)],
+             lambda s: c.reconstruct(stream=s), lambda s: c.top1_shift(Q, K, stream=s),
+             lambda s: list(q.QuantKVCache(2, 128, 16, 16, 4, 4, 300, stream=s).buffers.values()))
+    side = torch.cuda.Stream()
+    for call in calls:
+        alone = call(None)
+        torch.cuda.synchronize()
+        read = [torch.randint(0, 256, (t.numel() * t.element_size(),), generator=g, device="cuda",
+                              dtype=torch.uint8) for t in alone]
+        want = [t.clone() for t in read]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(100_000_000)
+        kept = [t.clone() for t in read]
+        del read
+        got = call(side)
+        side.synchronize()
+        if call is not calls[-1]:
+            assert all(torch.equal(a, b) for a, b in zip(got, alone))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(kept, want))
