@@ -694,3 +694,37 @@ def test_cache_calls_on_another_stream_leave_freed_memory_alone():
             assert all(torch.equal(a, b) for a, b in zip(got, alone))
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(kept, want))
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("d,rot", [(128, 64), (128, 16), (64, 16), (64, 48)])
+def test_channels_that_are_not_rotated_stay_alone(d, rot, layout):
+    """Behind rot_dim a channel without a norm leaves as it came, NaN, infinities and the sign of zero
+    included, whatever its neighbours hold; with a norm an infinity, which makes its own channel NaN
+    (inf / inf), leaves the others 0.  Rotated channels and an append's keys alike."""
+    g = _gen(d + rot)
+    n, rest = 9, d - rot
+    x = randn(g, n, 2, d).to(BF16)
+    special = torch.tensor([NAN, math.inf, -math.inf, -0.0, 0.0, -1.0, 3e38, -3e38], device="cuda").to(BF16)
+    for i in range(1, n):   # row 0 has no special values
+        for h in range(2):
+            at = torch.randperm(rest, generator=g, device="cuda")[:5] + rot
+            x[i, h, at] = special[torch.randint(0, 8, (5,), generator=g, device="cuda")]
+    clean = x.clone()
+    clean[..., rot:] = 1.0
+    rope, pos = q.qwm_rope_init(d, rot, layout), ints(list(range(100, 100 + n)))
+    out, _ = q.qwm_norm_rope(rope, x, pos=pos)
+    assert torch.equal(out[..., rot:].isnan(), x[..., rot:].isnan())
+    live = ~x[..., rot:].isnan()
+    assert torch.equal(out[..., rot:].view(torch.int16)[live], x[..., rot:].view(torch.int16)[live])
+    want, _ = q.qwm_norm_rope(rope, clean, pos=pos)
+    assert torch.equal(out[..., :rot], want[..., :rot])
+    kv = q.PagedKV(*(torch.zeros(1, 2, 16, d, dtype=BF16, device="cuda") for _ in range(2)))
+    kv.append(ints([[0]]), ints([0, n]), ints([0]), x, x, rope, pos)
+    assert torch.equal(kv.K[0, :, :n].transpose(0, 1).contiguous().view(torch.int16), out.view(torch.int16))
+    x = clean
+    x[:, :, rot + 5] = math.inf
+    out, _ = q.qwm_norm_rope(rope, x, pos=pos, q_weight=torch.ones(d, dtype=BF16, device="cuda"))
+    assert out[:, :, rot + 5].isnan().all()
+    out[:, :, rot + 5] = 0
+    assert (out == 0).all()
