@@ -545,13 +545,14 @@ def qwm_attention_shared_workspace(cache: qwm_cache, n_q: int, heads_q: int, n_s
 
 def qwm_attention_shared(cache: qwm_cache, Q: torch.Tensor, cu: torch.Tensor, max_q: int,
                          pages: qwm_pages | None = None, table: torch.Tensor | None = None,
-                         kv_len: torch.Tensor | None = None, max_kv: int = 0, causal: bool = False,
+                         kv_len: torch.Tensor | None = None, max_kv: int | None = None, causal: bool = False,
                          O: torch.Tensor | None = None, lse: torch.Tensor | None = None,
                          scale: float = 0.0, workspace: torch.Tensor | None = None,
                          stream=None) -> torch.Tensor:
     """Attention of the branches (rows cu[b] .. cu[b+1]-1 of Q) over the packed
     history that they share, followed by the first kv_len[b] positions of each
-    branch's pages.  max_q, max_kv: upper bounds of a branch's rows and keys."""
+    branch's pages.  max_q, max_kv: upper bounds of a branch's rows and keys, behind
+    which they are left out (max_kv None: as many keys as the table has places)."""
     index = _device_of(Q, "Q")
     qp, ldq = _rows_ptr(Q, "Q", index, None, cache.cfg.head_dim)
     n, h, _ = Q.shape
@@ -565,6 +566,12 @@ def qwm_attention_shared(cache: qwm_cache, Q: torch.Tensor, cu: torch.Tensor, ma
         tp = _mat_ptr(table, "table", index, _I32, n_seq)
         kp = _vec_ptr(kv_len, "kv_len", index, _I32, n_seq)
         pg, width = ctypes.addressof(pages), table.shape[1]
+        if max_kv is None:
+            max_kv = width * pages.page_size
+    elif table is not None or kv_len is not None:
+        raise ValueError("a table or kv_len without pages")
+    elif max_kv is None:
+        max_kv = 0
     O = _out(O, Q, index, stream)
     lp = _lse_ptr(lse, n, h, index)
     ws, wp, wn = _scratch(workspace, _shared_full, (cache, n, h, n_seq, max_q, max_kv), Q,
@@ -693,7 +700,7 @@ class QuantKVCache:
         return qwm_attention_ext(self.c, Q, K_seg, V_seg, O, lse, scale, stream)
 
     def attention_shared(self, Q, cu, max_q, pages: PagedKV | None = None, table=None, kv_len=None,
-                         max_kv=0, causal=False, O=None, lse=None, scale=0.0, workspace=None,
+                         max_kv=None, causal=False, O=None, lse=None, scale=0.0, workspace=None,
                          stream=None):
         if Q.device != self.buffers["k_codes"].device:
             raise ValueError(f"Q is on {Q.device}, the cache on {self.device}")

@@ -309,3 +309,25 @@ def test_what_the_cache_calls_allocate_belongs_to_their_stream(monkeypatch, stre
         device.made.clear()
         call()
         assert device.made == [where] * count
+
+
+def test_pages_without_a_bound_are_attended_to_whole(monkeypatch):
+    """max_kv left out bounds nothing: it is what the tables can hold; a table or lengths without pages,
+    which would be left out without a word, are refused."""
+    x, cu = torch.zeros(4, 2, 64, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)
+    table, lens = torch.zeros(2, 5, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    cache, pages = _cache(), _pages()
+    device = _Device(monkeypatch)
+
+    def bound(*a, **kw):
+        device.launches.clear()
+        q.qwm_attention_shared(cache, x, cu, 4, *a, **kw)
+        return device.launches[0][1][12]
+
+    assert bound(pages, table, lens) == 5 * 16
+    assert bound(pages, table, lens, 7) == 7
+    assert bound(pages, table, lens, max_kv=0) == 0
+    assert bound() == 0
+    for kw in (dict(table=table), dict(kv_len=lens), dict(pages=pages), dict(pages=pages, table=table)):
+        with pytest.raises(ValueError):
+            bound(**kw)

@@ -728,3 +728,14 @@ def test_channels_that_are_not_rotated_stay_alone(d, rot, layout):
     assert out[:, :, rot + 5].isnan().all()
     out[:, :, rot + 5] = 0
     assert (out == 0).all()
+
+
+def test_shared_without_a_bound_of_keys():
+    """max_kv left out: all of a branch's keys, as with the bound that the tables give."""
+    c, Kp, Vp, rows, kv, table, Q, cu, lens = _shared_case(64, 2, 1, 300, (3, 2), (40, 17), 16, True, 51)
+    lse = torch.empty(7, 2, device="cuda")
+    O = c.attention_shared(Q, cu, 3, kv, table, lens, causal=True, lse=lse)
+    _fine()
+    want, bound, wl, lb = _shared_want(Kp, Vp, rows, Q, (3, 2), (40, 17), True, 1)
+    check("O", O[:5], want[:5], bound[:5])
+    check_lse("lse", lse[:5], wl[:5], lb[:5])
