@@ -292,10 +292,12 @@ __global__ void __launch_bounds__(NT, 5) norm_rope_kernel(const __grid_constant_
 
 // A warp per token and side keeps the angles' share small; with few tokens the
 // heads are sliced, down to a step of rows, until 16 warps per SM have work.
+constexpr int MOST_HEADS = 64;  // per slice
+
 template <int D>
 void set_units(RopeArgs& a) {
   const int step = 32 / (D / 8) * UNROLL;
-  for (int per = 64;; per /= 2) {
+  for (int per = MOST_HEADS;; per /= 2) {
     a.per_slice = per;
     a.slices0 = (a.s[0].heads + per - 1) / per;
     a.slices = a.slices0 + (a.s[1].heads + per - 1) / per;
@@ -307,9 +309,7 @@ void set_units(RopeArgs& a) {
 template <int D, bool PAGED>
 cudaError_t launch(RopeArgs& a, int rot, cudaStream_t s) {
   set_units<D>(a);
-  const int64_t blocks = (a.units + NT / 32 - 1) / (NT / 32);
-  if (a.units > (int64_t(1) << 31) - 1) return cudaErrorInvalidConfiguration;
-  const unsigned grid = (unsigned)blocks;
+  const unsigned grid = (unsigned)((a.units + NT / 32 - 1) / (NT / 32));
   const bool full = 2 * a.pairs == D;
   if (rot == ROT_NONE) norm_rope_kernel<D, ROT_NONE, false, PAGED><<<grid, NT, 0, s>>>(a);
   else if (rot == ROT_HALF && full) norm_rope_kernel<D, ROT_HALF, true, PAGED><<<grid, NT, 0, s>>>(a);
@@ -317,6 +317,12 @@ cudaError_t launch(RopeArgs& a, int rot, cudaStream_t s) {
   else if (full) norm_rope_kernel<D, ROT_INTER, true, PAGED><<<grid, NT, 0, s>>>(a);
   else norm_rope_kernel<D, ROT_INTER, false, PAGED><<<grid, NT, 0, s>>>(a);
   return cudaGetLastError();
+}
+
+// The kernel counts units in 31 bits (with that many rows a slice is as long as it gets).
+bool units_ok(int64_t n, int32_t heads0, int32_t heads1) {
+  const int64_t slices = (heads0 + MOST_HEADS - 1) / MOST_HEADS + (heads1 + MOST_HEADS - 1) / MOST_HEADS;
+  return n <= (int64_t(1) << 31) - 1 && n * slices <= (int64_t(1) << 31) - 1;
 }
 
 bool rope_ok(const qwm_rope* r, int32_t head_dim) {
@@ -413,8 +419,8 @@ extern "C" qwm_status qwm_norm_rope(const qwm_rope* rope, int32_t head_dim, int6
                                     void* Q_out, int64_t ldqo, const void* K, int64_t ldk,
                                     int32_t heads_k, const void* w_k, void* K_out, int64_t ldko,
                                     const int32_t* pos, int64_t ldpos, float eps, void* stream) {
-  if ((head_dim != 64 && head_dim != 128) || n < 0 || n > (int64_t(1) << 31) - 1 || !(eps >= 0.0f) ||
-      heads_q < 0 || heads_k < 0 || heads_q > 65536 || heads_k > 65536)
+  if ((head_dim != 64 && head_dim != 128) || n < 0 || !(eps >= 0.0f) || heads_q < 0 || heads_k < 0 ||
+      heads_q > 65536 || heads_k > 65536 || !units_ok(n, heads_q, heads_k))
     return QWM_ERR_INVALID_ARG;
   if (rope && (!rope_ok(rope, head_dim) || (n > 0 && !pos) || ldpos < n)) return QWM_ERR_INVALID_ARG;
   RopeArgs a = {};
@@ -452,7 +458,7 @@ extern "C" qwm_status qwm_paged_append(const qwm_pages* p, const int32_t* table,
                                        const void* V, int64_t ldv, int64_t n, const qwm_rope* rope,
                                        const int32_t* pos, int64_t ldpos, const void* w_k,
                                        float eps, void* stream) {
-  if (!pages_ok(p) || n < 0 || n > (int64_t(1) << 31) - 1 || n_seq < 1 || n_seq > (1 << 24) ||
+  if (!pages_ok(p) || n < 0 || !units_ok(n, p->heads, p->heads) || n_seq < 1 || n_seq > (1 << 24) ||
       table_width < 1 || !table || !cu || !start || !(eps >= 0.0f) || (n > 0 && (!K || !V)))
     return QWM_ERR_INVALID_ARG;
   if (rope && (!rope_ok(rope, p->head_dim) || (n > 0 && !pos) || ldpos < n))

@@ -359,7 +359,8 @@ QWM_API qwm_status qwm_rope_init(qwm_rope* r, int32_t head_dim, int32_t rot_dim,
  * then ignored).  w_q, w_k: [head_dim] bf16 or null (no norm).  pos: [n_axes]
  * rows of n int32 positions, ldpos apart; any int32 value.  An output may be
  * its own input (same pointer and ld); other overlaps are not supported.
- * Without rope and w the call copies.  eps >= 0.
+ * Without rope and w the call copies.  eps >= 0.  At most 65536 heads a side, and
+ * 2^31 - 1 rows times blocks of 64 heads (each side's rounded up).
  * Errors: INVALID_ARG, ALIGNMENT, CUDA. */
 QWM_API qwm_status qwm_norm_rope(const qwm_rope* rope, int32_t head_dim, int64_t n, const void* Q,
                                  int64_t ldq, int32_t heads_q, const void* w_q, void* Q_out,
@@ -385,7 +386,8 @@ typedef struct qwm_pages {
  * of K and V) goes to position start[b] + i, the key after the norm (w_k not
  * null) and the rotation (rope not null) of qwm_norm_rope, the value as it is.
  * n: rows of K and V.  Every place is written by one row at most (the caller's
- * tables share no page that is being written).  n_seq >= 1.
+ * tables share no page that is being written).  1 <= n_seq <= 2^24; rows limited as in
+ * qwm_norm_rope.
  * Errors: INVALID_ARG, ALIGNMENT, CUDA. */
 QWM_API qwm_status qwm_paged_append(const qwm_pages* p, const int32_t* table, int64_t n_seq,
                                     int32_t table_width, const int32_t* cu, const int32_t* start,

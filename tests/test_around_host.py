@@ -331,3 +331,13 @@ def test_pages_without_a_bound_are_attended_to_whole(monkeypatch):
     for kw in (dict(table=table), dict(kv_len=lens), dict(pages=pages), dict(pages=pages, table=table)):
         with pytest.raises(ValueError):
             bound(**kw)
+
+
+def test_more_rows_than_a_launch_takes_are_an_invalid_argument():
+    """Rows times blocks of 64 heads (of queries and keys, or keys and values) end at 2^31 - 1; the call
+    says so itself, not the launch."""
+    many = dict(n=2**30, ldpos=2**30)
+    assert _norm_rope(**many) == 1
+    assert _norm_rope(n=2**31 - 1, ldpos=2**31, hq=1, hk=1) == 1
+    assert _append(n=2**30) == 1
+    assert _append(n=2**24, pages=dict(heads=4096, n_pages=1), ldk=4096 * 64, ldv=4096 * 64) == 1
