@@ -884,16 +884,18 @@ cudaError_t launch_unpack(const UnpackArgs& a, int grid, cudaStream_t s) {
 // Both centroid tables of a head fit in shared memory beside the rest.
 bool tables_fit(const Dims& D) { return (int64_t)D.C * D.d <= 32768; }
 
-// f.run<D, TAB, RK>() of the variant that serves a cache; tab: with staged tables.
-template <class F>
+// f.run<D, TAB, RK>() of the variant that serves a cache; tab: with staged tables (FIT64:
+// always so at head 64, where up to 512 centroids fit).
+template <bool FIT64, class F>
 cudaError_t variant(const Dims& D, bool tab, F f) {
   const bool deep = D.r > 8;
   if (D.d == 128) {
     if (tab) return deep ? f.template run<128, true, 16>() : f.template run<128, true, 8>();
     return deep ? f.template run<128, false, 16>() : f.template run<128, false, 8>();
   }
-  if (tab) return deep ? f.template run<64, true, 16>() : f.template run<64, true, 8>();
-  return deep ? f.template run<64, false, 16>() : f.template run<64, false, 8>();
+  if constexpr (!FIT64)
+    if (!tab) return deep ? f.template run<64, false, 16>() : f.template run<64, false, 8>();
+  return deep ? f.template run<64, true, 16>() : f.template run<64, true, 8>();
 }
 
 struct RunRows {
@@ -931,7 +933,7 @@ cudaError_t launch_unpack(const Dims& D, const CacheView& v, int64_t T, int h0, 
   // 40 x 37440 (10118 keys) 9 us more; at 16 centroids 40 x 9360 3 us more.  (The
   // attention of few rows takes as long or longer without at every length.)
   const bool tab = tables_fit(D) && a.total * KT >= (int64_t)grid * 32 * D.C;
-  return variant(D, tab, RunUnpack{a, grid, s});
+  return variant<false>(D, tab, RunUnpack{a, grid, s});
 }
 
 // Rows of one product, and a history that gives every warp four tiles.  Otherwise the
@@ -974,7 +976,7 @@ cudaError_t launch_rows(const Dims& D, const CacheView& v, int64_t T, const uint
   a.nslot = plan.slots;
   a.nt = (T + KT - 1) / KT;
   a.total = a.nt * D.H;
-  return variant(D, tables_fit(D), RunRows{a, plan.grid, s});
+  return variant<true>(D, tables_fit(D), RunRows{a, plan.grid, s});
 }
 
 }  // namespace qwm
