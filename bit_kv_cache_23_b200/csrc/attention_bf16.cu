@@ -19,11 +19,13 @@
 // while the softmax works on this one.  Two CTAs share an SM: one's products run
 // while the other has the exponential unit, and one's beginning and end hide
 // behind the other's tiles.  (One CTA of 256 rows, with each K and V tile read
-// once for two such groups, took 8 to 18 % longer up to 2048 keys: the groups fall
-// into step, both waiting for products and then both for the exponential unit.)
+// once for two such groups, took 8 to 18 % longer up to 2048 keys, as long at 4096 and
+// 5 % less at 8192: the groups fall into step, both waiting for products and then both
+// for the exponential unit.  That was with one lane issuing the products, which bounded
+// every form then; it was not measured again with the warp that issues them now.)
 //
-// Bound by the tensor core's reading of shared memory, and by the power limit: a
-// 128 x 64 tile's products take 643 cycles, of which S takes 386 (a product of 64
+// Bound, with tiles of 64 keys, by the tensor core's reading of shared memory, and by the
+// power limit: a 128 x 64 tile's products take 643 cycles, of which S takes 386 (a product of 64
 // columns reads 6 KB in 48 cycles for 32 cycles of arithmetic; 128 columns would
 // take 64, but two such buffers beside O do not fit in half of TMEM), and an SM with
 // two CTAs needs 720 cycles per tile.  1560 rows x 40 heads over 8192 keys: 243 to 247
@@ -864,7 +866,8 @@ size_t partial_bytes(int np, int64_t n_q, int Hq, int d) {
 // How a shared-history call runs.  joined: one CTA takes its rows through the
 // history and then through its branch's own keys.  Otherwise all branches' rows
 // pack into common row blocks for the history, which few rows per branch would
-// leave mostly empty, the own keys follow per branch, and the two are merged.
+// leave mostly empty, the own keys follow per branch, and the two are merged (two
+// partials, however large).
 // With few rows in all the history is not unpacked at all (attention_rows.cu).
 // Between the first two the costs of blocks_of decide.
 struct SharedPlan {

@@ -2,11 +2,12 @@
 // few branches) over the packed cache, decoded straight into the operands of
 // register-level matrix products: nothing but the packed fields crosses HBM.
 //
-// Bound by the decoding, not by memory: at 40 heads x 37440 tokens x 128 channels
-// the packed fields are 162 MB (25 us), while every element takes about four
-// instructions to rebuild, not counting what each group of them needs; one row takes 225 us, eight 234 us and sixteen 245 us (at
-// rank 16 292, 301 and 311), with 56 % of the issue slots and 44 % of the integer
-// pipe in use.  So the layout serves the decoder.  A warp takes 16
+// Bound by the decoding's latency, not by memory and by no single pipe: at 40 heads x
+// 37440 tokens x 128 channels the packed fields are 162 MB (25 us), while every element
+// takes about four instructions to rebuild, not counting what each group of them needs;
+// one row takes 225 us, eight 234 us and sixteen 245 us (at rank 16 292, 301 and 311),
+// with 56 % of the issue slots and 44 % of the integer pipe in use by the 12 warps that
+// the registers leave an SM.  So the layout serves the decoder.  A warp takes 16
 // keys at a time; in the products' operand layout (lane = 4 g + c) the channels
 // are permuted such that a lane owns a quarter head of keys g and g + 8 of K'
 // (whole code words) and D / 8 channels of keys 2c, 2c+1, 2c+8, 2c+9 of V', and
@@ -35,8 +36,9 @@ namespace qwm {
 namespace {
 using namespace tc;
 
-constexpr int NW_ROWS = 12;    // warps of the attention: 168 registers per thread (16 warps spill:
-                               // 320 us, against 240 us when this was chosen)
+constexpr int NW_ROWS = 12;    // warps of the attention: 168 registers per thread, and 32 to 48 bytes
+                               // of spills at head 128 (16 warps spill much more: 320 us, against
+                               // 240 us when this was chosen)
 constexpr int NW_UNPACK = 16;  // and of the unpacking, which keeps no O
 constexpr int KT = 16;        // keys per tile
 constexpr int NSTAGE = 2;     // tiles in a warp's ring
@@ -940,7 +942,9 @@ cudaError_t launch_unpack(const Dims& D, const CacheView& v, int64_t T, int h0, 
 // history is unpacked and attended to as bf16: at 40 heads x 37440 tokens 16 rows take
 // 248 us here and 357 us there, and a second row tile, decoding all again, would take
 // 463 us; 8 rows over 4 x 37440 tokens (5.3 tiles a warp) 54 and 69 us, over 40 x 3120
-// (4.4) 55 and 56, over 12 x 7919 (3.3) 48 and 46, one row there 46 and 40.
+// (4.4) 55 and 56, over 12 x 7919 (3.3) 48 and 46, one row there 46 and 40.  (64 partials
+// leave one key head 62 CTAs: 8 rows over 115200 tokens 66 us here, 63 unpacked; two heads
+// of 57600 tokens, on 124 CTAs, 50 and 57.)
 bool rows_supported(const Dims& D, int64_t T, int64_t rows, int sms) {
   return rows <= 16 && (T + KT - 1) / KT * D.H >= 4 * (int64_t)NW_ROWS * sms;
 }

@@ -18,11 +18,11 @@
 // them) by itself: no barrier ties its latencies (the angles, a page's place) to
 // other warps', and its next rows are on the way while it works on these.
 // Measured: the 480p frame (1560 x 80 heads x 128, normed and rotated) 10.9 us,
-// 5.9 TB/s; 9361 x 48 heads in the half layout 42.6 us, 5.4 TB/s; a paged append
-// of 5072 x 12 heads 16.6 us, 3.8 TB/s.  A block per token took 18.3, 102 and 44 us.
+// 5.9 TB/s; 9361 x 48 heads in the half layout, half of each head, 44.0 us, 5.2 TB/s; a
+// paged append of 5072 x 12 heads 17.1 us, 3.6 TB/s.  A block per token took 18.3, 102 and 44 us.
 //
-// Angles are formed in fp64 and reduced to (-pi, pi] before the fp32 sincosf:
-// in fp32 a position near 10^6 would be off by 0.06 rad.  A lane computes one or
+// Angles are formed in fp64 and reduced to half turns in (-1, 1] before the fp32
+// sincospif: in fp32 a position near 10^6 would be off by 0.06 rad.  A lane computes one or
 // two pairs for all of the warp's rows, through shared memory, which keeps the
 // fp64 work at 1 / heads of the elements.
 #include <math.h>

@@ -351,7 +351,9 @@ QWM_API qwm_status qwm_rope_init(qwm_rope* r, int32_t head_dim, int32_t rot_dim,
                                  double beta_fast, double beta_slow);
 
 /* Norm and rotation of n rows of queries and keys in one pass:
- *   y = x rsqrt(mean_j x_j^2 + eps) w      per head, where w is not null;
+ *   y = x rsqrt(mean_j x_j^2 + eps) w      per head, where w is not null (the
+ *   mean is over the head_dim channels of one head and its weight serves every
+ *   head; a norm over all heads of a row together is not offered);
  *   (a, b) -> gain (a cos t - b sin t, a sin t + b cos t) for each pair, t =
  *   pos freq (fp64) of the pair's axis,    where rope is not null;
  * in fp32, rounded once.  Q: [n] rows of heads_q heads, ldq apart, written to
@@ -398,7 +400,9 @@ QWM_API qwm_status qwm_paged_append(const qwm_pages* p, const int32_t* table, in
 /* Attention of n_seq branches over one packed history, which all share,
  * followed by each branch's own paged keys:
  *   O = softmax(scale Q [K' ; K_b]^T) [V' ; V_b]
- * with K', V' as in qwm_attention (all `len` cached tokens; len may be 0) and
+ * with K', V' as in qwm_attention (all `len` cached tokens; len may be 0; with
+ * rank > 0 the compensation's products are summed in another order, so an element
+ * of K' that lies next to a border between two bf16 values can be the other) and
  * K_b, V_b the first kv_len[b] positions of branch b's pages.  causal != 0:
  * row i of the n_b rows of branch b sees its own keys up to position
  * kv_len[b] - n_b + i only (and the whole history).  Rows without any key give
@@ -412,6 +416,7 @@ QWM_API qwm_status qwm_paged_append(const qwm_pages* p, const int32_t* table, in
  * which size the launch: rows and keys beyond them are left out (the rows' O and
  * lse as they were).  At most 2^30 rows times query heads per key head, tokens
  * cached and keys of a branch, 65535 branches.
+ * A query of NaN gives NaN in its own row.
  * workspace: device scratch of this call, 256-byte aligned, not shared with
  * calls that can run at the same time; at least the `least` bytes of
  * qwm_attention_shared_workspace; `full` bytes serve all heads in one pass.

@@ -128,3 +128,34 @@ def test_history_from_the_packed_fields(H, C, G, r, d, T, rows, path):
     _fine()
     for h in range(H) if H <= 5 else range(0, H, -(-H // 20)):
         _check_head(c, h, Kp[h], Vp[h], Q[:, h], O[:, h], lse[:, h])
+
+
+def test_a_kept_branch_is_committed():
+    """Keys normed and rotated once go to a branch's pages and, when the branch is kept, to the packed
+    history: the pages hold those rows, and the history grows by them."""
+    g = _gen(61)
+    H, d, new = 2, 64, 40
+    c = q.QuantKVCache(H, d, 16, 16, 4, 4, 200)
+    first = randn(g, 2, 100, H, d).to(BF16)
+    c.build_centroids(*first)
+    c.update_query_stats(randn(g, 16, H, d).to(BF16))
+    c.append_kv(*first)
+    qkv = randn(g, 2 * new, 3 * H, d).to(BF16)
+    w = (1 + 0.3 * randn(g, d)).to(BF16)
+    rope, pos = q.qwm_rope_init(d, d), torch.arange(2 * new, device="cuda", dtype=torch.int32) % new + 100
+    kv = q.PagedKV(*(torch.zeros(6, H, 16, d, dtype=BF16, device="cuda") for _ in range(2)))
+    table, cu = ints([[5, 0, 3], [1, 2, 4]]), ints([0, new, 2 * new])
+    _, K = q.qwm_norm_rope(rope, None, qkv[:, H:2 * H], pos, k_weight=w)
+    kv.append(table, cu, ints([0, 0]), K, qkv[:, 2 * H:])
+    rows = slice(new, 2 * new)   # the second branch is kept
+    c.append_kv(K[rows].contiguous(), qkv[rows, 2 * H:].contiguous())
+    _fine()
+    assert c.len == 100 + new
+    paged = kv.K[table[1].long()].transpose(0, 1).reshape(H, -1, d)[:, :new]
+    assert torch.equal(paged, K[rows].transpose(0, 1))
+    Q = randn(g, 5, H, d).to(BF16)
+    Kp, Vp = c.reconstruct()
+    lse = torch.empty(5, H, device="cuda")
+    O = c.attention_shared(Q, ints([0, 5]), 5, lse=lse)
+    for h in range(H):
+        _check_head(c, h, Kp[h], Vp[h], Q[:, h], O[:, h], lse[:, h])
