@@ -739,3 +739,25 @@ def test_shared_without_a_bound_of_keys():
     want, bound, wl, lb = _shared_want(Kp, Vp, rows, Q, (3, 2), (40, 17), True, 1)
     check("O", O[:5], want[:5], bound[:5])
     check_lse("lse", lse[:5], wl[:5], lb[:5])
+
+
+def test_calls_with_a_stream_in_a_graph():
+    """Calls that name their stream, the capturing one and one that was forked from it, captured and
+    replayed over memory that other work has used since."""
+    calls, _ = _small_calls()
+    alone = {name: call(None) for name, call in calls.items()}
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        kept = [(name, call(s)) for name, call in calls.items() for s in (here, side)]
+        here.wait_stream(side)
+    for _ in range(3):
+        for _, t in kept:
+            t.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(t, alone[name]) for name, t in kept)
+    _fine()
